@@ -44,6 +44,9 @@
  *   w_down   [E+1, D, I]    same
  *   s_gate, s_up [E+1, I/128, D/128] and s_down [E+1, D/128, I/128]:
  *                           fp32 block scales, MOE_FP8_E4M3_B128 only.
+ *                           MOE_MXFP4: w_* hold codes, [E+1, I, D/2] and
+ *                           [E+1, D, I/2] bytes, and s_* point to their scale
+ *                           bytes, [E+1, I, D/32] and [E+1, D, I/32].
  *   w_down_f16 [E+1, D, I]  fp16 copy of w_down (MOE_BF16 layer on tensor
  *                           cores, unless MOE_FLAG_DOWN_HILO); made once by
  *                           moe_convert_down_weights().  Where it is read
@@ -99,8 +102,12 @@ typedef enum moe_status {
  *     token per 128-column group with s = amax/448 and
  *     code = E4M3_rne_satfinite(fp32(v * fp32(448/amax))); fp32 accumulation
  *     with the block scales applied per 128-wide K chunk; router in bf16;
- *     bf16 or fp32 output. */
-typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3_B128 = 2 } moe_dtype;
+ *     bf16 or fp32 output.
+ *   MOE_MXFP4: expert weights in microscaled 4-bit floating point (see
+ *     moe_mx_quantize), and both expert GEMM inputs (x and h) quantised to it
+ *     per token per 32 columns; fp32 accumulation; router in bf16; bf16 or
+ *     fp32 output. */
+typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3_B128 = 2, MOE_MXFP4 = 3 } moe_dtype;
 
 /* moe_config.flags */
 #define MOE_FLAG_FORCE_SIMT 0x1u   /* expert GEMMs on the CUDA-core kernel (cross-check path) */
@@ -218,6 +225,7 @@ typedef struct moe_ws_layout {
                           launch's order (a permutation of 0..E, the shared group E last).
                           Written by the permutation, and only where the split can run: bf16
                           layer, T*top_k >= 64*E (see MOE_FLAG_SPLIT_GEMM_OFF) */
+    size_t few;        /* moe_forward_few, T <= MOE_FEW_MAX: f32 [T, D], then f32 [T*(top_k+1), I] */
 } moe_ws_layout;
 
 /* Validate a configuration and build a host-side plan for `device`.
@@ -352,6 +360,91 @@ MOE_API moe_status moe_check(const moe_plan* plan, const void* ws, void* stream)
  * MOE_ERR_DEVICE_TIMEOUT in the error word and returns normally. */
 MOE_API moe_status moe_selftest_wait_timeout(const moe_plan* plan, void* ws, size_t ws_bytes, int64_t limit_ns,
                                      void* stream);
+
+/* ------------------------------------------------ operators of the block
+ *
+ * What a decoder block runs beside the layer.  None of them needs a plan;
+ * they enqueue on `stream` for the current device, take dense rows at any row
+ * stride (ld_*, in elements, at least the row's length) and allocate nothing.
+ * An empty input (T or rows = 0) returns MOE_OK at once. */
+
+/* The whole layer for a few tokens: the arithmetic of moe_forward for
+ * 1 <= T <= MOE_FEW_MAX (T = 0: MOE_OK) without its permutation, in fewer
+ * launches, each chosen expert's weights read once.  Same arguments and same
+ * errors; the results are within the layer type's tolerance of
+ * moe_forward's, not bit-identical.  Takes every moe_dtype.  Uses
+ * the workspace parts logits, blob and few; workspaces are made ready once by
+ * moe_workspace_init (or by an earlier moe_forward). */
+#define MOE_FEW_MAX 16
+MOE_API moe_status moe_forward_few(const moe_plan* plan, const moe_weights* w, const void* x, int32_t T, void* out,
+                                   int32_t* blob_out, float* logits_out, void* ws, size_t ws_bytes, void* stream);
+
+/* Norms before and after a block.
+ *   N(v) = (v - mu) / sqrt(mean((v - mu)^2) + eps) * (w + w_offset) + b
+ * with mu = mean(v) for MOE_NORM_LAYER and 0 for MOE_NORM_RMS; statistics and
+ * arithmetic in fp32, one rounding at each store.  MOE_NORM_NONE: N(v) = v.
+ * w NULL: no multiplication; b NULL: no addition.  Rows of up to 16384
+ * elements; each element type MOE_F32 or MOE_BF16. */
+typedef enum moe_norm_kind { MOE_NORM_NONE = 0, MOE_NORM_RMS = 1, MOE_NORM_LAYER = 2 } moe_norm_kind;
+typedef enum moe_gate_by { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2, MOE_GATE_FULL = 3 } moe_gate_by;
+
+typedef struct moe_norm {
+    int32_t kind;     /* moe_norm_kind */
+    float eps;        /* >= 0 */
+    float w_offset;   /* added to w (1 where weights are stored about zero) */
+    int32_t p_dtype;  /* of w and b */
+    const void* w;    /* [D] or NULL */
+    const void* b;    /* [D] or NULL */
+} moe_norm;
+
+/* What follows a block's output y:
+ *   r'   = res_scale * r + branch_scale * g * N(y)
+ *   next = N_next(r' as stored)
+ * g: 1, or gate by channel [D], by token [T] or in full [T, D] (row stride
+ * ld_gate), through a sigmoid if gate_sigmoid. */
+typedef struct moe_post {
+    moe_norm norm;           /* of y */
+    moe_norm next;           /* of r'; kind MOE_NORM_NONE: no next norm */
+    float res_scale, branch_scale;
+    int32_t gate_by;         /* moe_gate_by */
+    int32_t gate_dtype;
+    int32_t gate_sigmoid;
+    const void* gate;
+    int64_t ld_gate;
+} moe_post;
+
+/* out = N(x), [T, D]. */
+MOE_API moe_status moe_norm_pre(const moe_norm* n, const void* x, int32_t dtype, int64_t ld_x, int32_t T, int32_t D,
+                                void* out, int32_t out_dtype, int64_t ld_out, void* stream);
+/* out = r' (same type as res; out may be res, at the same row stride), and
+ * next_out = the next norm of it where post->next has one. */
+MOE_API moe_status moe_norm_post(const moe_post* post, const void* y, int32_t dtype, int64_t ld_y, const void* res,
+                                 int32_t res_dtype, int64_t ld_res, int32_t T, int32_t D, void* out, int64_t ld_out,
+                                 void* next_out, int32_t next_dtype, int64_t ld_next, void* stream);
+
+/* Microscaled 4-bit floating point (MXFP4 of the OCP Microscaling Formats
+ * specification).  A row of cols elements is held as nb = ceil(cols/32)
+ * blocks: q [rows, 16*nb] bytes of E2M1 codes (two a byte, the even column in
+ * the low half; a ragged last block is filled up with zeros) and s [rows, nb]
+ * E8M0 scale bytes.  Scale exponent floor(log2(amax)) - 2, at least -127;
+ * codes rounded to nearest even and saturated.  A block of zeros takes the
+ * scale 1; a block with an infinity or a NaN takes the byte 255 and reads
+ * back as NaN.  x fp32 or bf16; q 16-byte aligned. */
+MOE_API moe_status moe_mx_quantize(const void* x, int32_t dtype, int64_t ld_x, int64_t rows, int32_t cols, uint8_t* q,
+                                   uint8_t* s, void* stream);
+MOE_API moe_status moe_mx_dequantize(const uint8_t* q, const uint8_t* s, int64_t rows, int32_t cols, void* out,
+                                     int32_t out_dtype, int64_t ld_out, void* stream);
+
+/* Product of microscaled 4-bit matrices, fp32 accumulation:
+ *   out[r][n] = sum_k a[r][k] * b_g[n][k]
+ * a [rows, K/2] codes and [rows, K/32] scales; b [G, N, K/2] and
+ * [G, N, K/32]; K a multiple of 32.  offsets (device, [G+1], ascending) gives
+ * the rows of each group, offsets[g] .. offsets[g+1]-1; NULL: G = 1, all
+ * rows.  Entries outside [0, rows] are clamped to it; rows of no group are
+ * left as they are.  out [rows, N] fp32 or bf16 at row stride ld_out. */
+MOE_API moe_status moe_mx_gemm(const uint8_t* a, const uint8_t* a_scale, const uint8_t* b, const uint8_t* b_scale,
+                               const int32_t* offsets, int32_t rows, int32_t G, int32_t N, int32_t K, void* out,
+                               int32_t out_dtype, int64_t ld_out, void* stream);
 
 MOE_API const char* moe_status_str(moe_status s);
 

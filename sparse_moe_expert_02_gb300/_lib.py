@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -23,7 +24,7 @@ _lib = None
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE = 0, 1, 2, 3
 MOE_ERR_CUDA, MOE_ERR_DEVICE_TIMEOUT, MOE_ERR_BOUNDS, MOE_ERR_NONFINITE = 4, 5, 6, 7
 # moe_dtype
-MOE_F32, MOE_BF16, MOE_FP8_E4M3_B128 = 0, 1, 2
+MOE_F32, MOE_BF16, MOE_FP8_E4M3_B128, MOE_MXFP4 = 0, 1, 2, 3
 MOE_FLAG_FORCE_SIMT = 0x1
 MOE_FLAG_PAIR_CTA_OFF = 0x2
 MOE_FLAG_PAIR_CTA_ON = 0x4
@@ -36,7 +37,11 @@ MOE_FLAG_TOPK_HIST_OFF = 0x100
 MOE_FLAG_FUSED_COMBINE = 0x200
 MOE_FLAG_SPLIT_GEMM_OFF = 0x400
 
-DTYPE_CODE = {"f32": MOE_F32, "bf16": MOE_BF16, "fp8": MOE_FP8_E4M3_B128}
+DTYPE_CODE = {"f32": MOE_F32, "bf16": MOE_BF16, "fp8": MOE_FP8_E4M3_B128, "mxfp4": MOE_MXFP4}
+MOE_FEW_MAX = 16
+# moe_norm_kind, moe_gate_by
+MOE_NORM_NONE, MOE_NORM_RMS, MOE_NORM_LAYER = 0, 1, 2
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN, MOE_GATE_FULL = 0, 1, 2, 3
 
 # Every symbol include/moe.h declares (tests check the library exports them).
 SYMBOLS = (
@@ -45,6 +50,7 @@ SYMBOLS = (
     "moe_gemm_gateup", "moe_gemm_down", "moe_unpermute", "moe_check", "moe_selftest_wait_timeout",
     "moe_status_str", "moe_last_error_detail", "moe_build_info", "moe_launch_count",
     "moe_permute_index_noalloc", "moe_pack_routing_words", "moe_convert_down_weights", "moe_pointer_kind",
+    "moe_forward_few", "moe_norm_pre", "moe_norm_post", "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_gemm",
 )
 
 
@@ -62,7 +68,7 @@ class moe_weights(ctypes.Structure):
 class moe_ws_layout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in
                 ("total", "err", "logits", "blob", "counts", "offsets", "tiles", "inv", "src_tok", "hist", "xq",
-                 "xq_scale", "xp", "xp_scale", "h", "h_scale", "y", "logits_part", "tiles2", "pairs")]
+                 "xq_scale", "xp", "xp_scale", "h", "h_scale", "y", "logits_part", "tiles2", "pairs", "few")]
 
 
 class MoEError(RuntimeError):
@@ -112,6 +118,12 @@ def lib():
                 "moe_pack_routing_words": (st, [P, I32, P, S, P, P]),
                 "moe_convert_down_weights": (st, [P, P, P, P, S, P]),
                 "moe_pointer_kind": (st, [P, ctypes.POINTER(ctypes.c_int32)]),
+                "moe_forward_few": (st, [P, ctypes.POINTER(moe_weights), P, I32, P, P, P, P, S, P]),
+                "moe_norm_pre": (st, [P, P, I32, I64, I32, I32, P, I32, I64, P]),
+                "moe_norm_post": (st, [P, P, I32, I64, P, I32, I64, I32, I32, P, I64, P, I32, I64, P]),
+                "moe_mx_quantize": (st, [P, I32, I64, I64, I32, P, P, P]),
+                "moe_mx_dequantize": (st, [P, P, I64, I32, P, I32, I64, P]),
+                "moe_mx_gemm": (st, [P, P, P, P, P, I32, I32, I32, I32, P, I32, I64, P]),
             }
             for name, (res, args) in sig.items():
                 fn = getattr(L, name)
@@ -264,6 +276,68 @@ def moe_permute_index_noalloc(idx, T, E, top_k, counts, offsets, tiles, inv, src
 def moe_pack_routing_words(plan, T, ws, words, stream=None):
     _ok(lib().moe_pack_routing_words(plan, T, _ptr(ws), _wsb(ws), _ptr(words), _stream(stream)),
         "moe_pack_routing_words")
+
+
+# Operators of the block.  Rows of a 2-D tensor may be strided (inner stride
+# 1); moe_norm and moe_post are passed packed, as the header lays them out.
+
+_DTYPE_OF = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+NORM_STRUCT = struct.Struct("@iffiPP")
+POST_STRUCT = struct.Struct("@iffiPPiffiPPffiii4xPq")
+
+
+def _rows(t, what: str):
+    """(address, moe_dtype, row stride) of a 2-D device tensor of fp32 or bf16."""
+    dt = _DTYPE_OF.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{what}: fp32 or bf16, not {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: libmoe takes device tensors")
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{what}: a 2-D tensor whose rows are contiguous")
+    # the stride of a single row says nothing (it may be anything)
+    return t.data_ptr(), dt, t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def moe_forward_few(plan, weights: moe_weights, x, T, out, blob_out, logits_out, ws, stream=None):
+    _ok(lib().moe_forward_few(plan, ctypes.byref(weights), _ptr(x), T, _ptr(out, host_mapped_ok=True), _ptr(blob_out),
+                              _ptr(logits_out), _ptr(ws), _wsb(ws), _stream(stream)), "moe_forward_few")
+
+
+def moe_norm_pre(norm: bytes, x, out, stream=None):
+    xp, xt, xl = _rows(x, "x")
+    op, ot, ol = _rows(out, "out")
+    T, D = x.shape
+    _ok(lib().moe_norm_pre(norm, xp, xt, xl, T, D, op, ot, ol, _stream(stream)), "moe_norm_pre")
+
+
+def moe_norm_post(post: bytes, y, res, out, next_out, stream=None):
+    yp, yt, yl = _rows(y, "y")
+    rp, rt, rl = _rows(res, "res")
+    op, ot, ol = _rows(out, "out")
+    if ot != rt:
+        raise ValueError("out: the type of res")
+    np_, nt, nl = (None, MOE_BF16, 0) if next_out is None else _rows(next_out, "next_out")
+    T, D = y.shape
+    _ok(lib().moe_norm_post(post, yp, yt, yl, rp, rt, rl, T, D, op, ol, np_, nt, nl, _stream(stream)), "moe_norm_post")
+
+
+def moe_mx_quantize(x, q, s, stream=None):
+    xp, xt, xl = _rows(x, "x")
+    _ok(lib().moe_mx_quantize(xp, xt, xl, x.shape[0], x.shape[1], _ptr(q), _ptr(s), _stream(stream)),
+        "moe_mx_quantize")
+
+
+def moe_mx_dequantize(q, s, out, stream=None):
+    op, ot, ol = _rows(out, "out")
+    _ok(lib().moe_mx_dequantize(_ptr(q), _ptr(s), out.shape[0], out.shape[1], op, ot, ol, _stream(stream)),
+        "moe_mx_dequantize")
+
+
+def moe_mx_gemm(a, a_scale, b, b_scale, offsets, G: int, N: int, K: int, out, stream=None):
+    op, ot, ol = _rows(out, "out")
+    _ok(lib().moe_mx_gemm(_ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale), _ptr(offsets), out.shape[0], G, N, K, op, ot,
+                          ol, _stream(stream)), "moe_mx_gemm")
 
 
 def moe_launch_count() -> int:

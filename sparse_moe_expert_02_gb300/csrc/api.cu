@@ -152,6 +152,7 @@ void layout(const moe_config& c, int num_sms, int T, moe_ws_layout* L) {
     L->logits_part = S > 1 ? take((size_t)S * T * c.E * 4) : 0;
     L->tiles2 = take((size_t)(c.E + 2) * 4);
     L->pairs = take((size_t)(3 * (c.E + 2) + 2) * 4);
+    L->few = T <= moe::kFewMax ? take(((size_t)T * c.D + (size_t)R * c.I) * 4) : 0;
     L->total = o;
 }
 
@@ -194,8 +195,8 @@ moe_status check_weights(const moe_plan* p, const moe_weights* w, bool router, b
             return arg_fail(MOE_ERR_INVALID_ARG, "w_down_f16 NULL or misaligned (see moe_convert_down_weights)");
         if (f16_only ? (w->w_down && !aligned(w->w_down, 16)) : !ptr_ok(w->w_down))
             return arg_fail(MOE_ERR_INVALID_ARG, "w_down NULL or misaligned");
-        if (p->cfg.dtype == MOE_FP8_E4M3_B128 && (!ptr_ok(w->s_gate) || !ptr_ok(w->s_up) || !ptr_ok(w->s_down)))
-            return arg_fail(MOE_ERR_INVALID_ARG, "FP8 block scales NULL or misaligned");
+        if ((p->cfg.dtype == MOE_FP8_E4M3_B128 || p->cfg.dtype == MOE_MXFP4) && (!ptr_ok(w->s_gate) || !ptr_ok(w->s_up) || !ptr_ok(w->s_down)))
+            return arg_fail(MOE_ERR_INVALID_ARG, "block scales NULL or misaligned");
     }
     return MOE_OK;
 }
@@ -295,7 +296,7 @@ moe_status moe_plan_create(const moe_config* cfg, int device, moe_plan** out) {
     *out = nullptr;
     if (!cfg) return arg_fail(MOE_ERR_INVALID_ARG, "cfg is NULL");
     const moe_config& c = *cfg;
-    if (c.dtype < MOE_F32 || c.dtype > MOE_FP8_E4M3_B128) return arg_fail(MOE_ERR_UNSUPPORTED, "dtype");
+    if (c.dtype < MOE_F32 || c.dtype > MOE_MXFP4) return arg_fail(MOE_ERR_UNSUPPORTED, "dtype");
     if (c.out_dtype != MOE_F32 && c.out_dtype != MOE_BF16) return arg_fail(MOE_ERR_UNSUPPORTED, "out_dtype");
     if (c.E < 1 || c.E > 1024) return arg_fail(MOE_ERR_UNSUPPORTED, "E outside [1, 1024]");
     if (c.top_k < 1 || c.top_k > std::min(c.E, 32)) return arg_fail(MOE_ERR_UNSUPPORTED, "top_k outside [1, min(E,32)]");
@@ -752,6 +753,7 @@ moe_status moe_forward(const moe_plan* p, const moe_weights* w, const void* x, i
     Ws W;
     moe_status st = check_call(p, T, ws, ws_bytes, &W);
     if (st != MOE_OK) return st;
+    if (p->cfg.dtype == MOE_MXFP4) return arg_fail(MOE_ERR_UNSUPPORTED, "MOE_MXFP4 runs through moe_forward_few");
     if ((st = check_weights(p, w, true, true)) != MOE_OK) return st;
     if (!ptr_ok(x) || !ptr_ok(out)) return arg_fail(MOE_ERR_INVALID_ARG, "x or out NULL or misaligned");
     if ((blob_out && !aligned(blob_out, 16)) || (logits_out && !aligned(logits_out, 16)))
@@ -872,6 +874,205 @@ moe_status moe_forward(const moe_plan* p, const moe_weights* w, const void* x, i
     }
     if ((st = moe_unpermute(p, T, out, ws, ws_bytes, stream)) != MOE_OK) return st;
     return copy_routing_out(p, W, T, blob_out, logits_out, s);
+}
+
+// ------------------------------------------------- operators of the block
+
+moe_status moe_forward_few(const moe_plan* p, const moe_weights* w, const void* x, int32_t T, void* out,
+                           int32_t* blob_out, float* logits_out, void* ws, size_t ws_bytes, void* stream) {
+    if (p && T == 0) return MOE_OK;
+    Ws W;
+    moe_status st = check_call(p, T, ws, ws_bytes, &W);
+    if (st != MOE_OK) return st;
+    if (T > moe::kFewMax) return arg_fail(MOE_ERR_UNSUPPORTED, "T above MOE_FEW_MAX (use moe_forward)");
+    if ((st = check_weights(p, w, true, true)) != MOE_OK) return st;
+    if (!ptr_ok(x) || !ptr_ok(out)) return arg_fail(MOE_ERR_INVALID_ARG, "x or out NULL or misaligned");
+    if ((blob_out && !aligned(blob_out, 16)) || (logits_out && !aligned(logits_out, 16)))
+        return arg_fail(MOE_ERR_INVALID_ARG, "blob_out or logits_out misaligned");
+    const moe_config& c = p->cfg;
+    moe::FewParams f = {};
+    f.T = T;
+    f.D = c.D;
+    f.E = c.E;
+    f.I = c.I;
+    f.k = c.top_k;
+    f.dtype = c.dtype;
+    f.out_elem = c.out_dtype == MOE_F32 ? moe::kF32 : moe::kBF16;
+    f.x = x;
+    f.w_router = w->w_router;
+    f.b_router = c.has_router_bias ? w->b_router : nullptr;
+    f.w_gate = w->w_gate;
+    f.w_up = w->w_up;
+    f.down_f16 = f16_down(c) && w->w_down_f16;
+    f.w_down = f.down_f16 ? w->w_down_f16 : w->w_down;
+    f.s_gate = w->s_gate;
+    f.s_up = w->s_up;
+    f.s_down = w->s_down;
+    f.logits = W.at<float>(W.L.logits);
+    f.blob = W.at<int32_t>(W.L.blob);
+    f.xr = W.at<float>(W.L.few);
+    f.h = f.xr + (size_t)T * c.D;
+    f.out = out;
+    f.err = W.at<uint32_t>(W.L.err);
+    cudaStream_t s = (cudaStream_t)stream;
+    MOE_CUDA(cudaMemsetAsync(ws, 0, kErrBlock, s));
+    MOE_CUDA(moe::launch_few(f, s));
+    return copy_routing_out(p, W, T, blob_out, logits_out, s);
+}
+
+namespace {
+
+bool float_type(int dtype) { return dtype == MOE_F32 || dtype == MOE_BF16; }
+int float_elem(int dtype) { return dtype == MOE_F32 ? moe::kF32 : moe::kBF16; }
+// A tensor of rows with any element-aligned base and a row stride that holds a row.
+bool rows_ok(const void* q, int dtype, int64_t ld, int64_t cols) {
+    return q && aligned(q, dtype == MOE_F32 ? 4 : 2) && ld >= cols;
+}
+
+moe_status check_norm(const moe_norm& n, moe::NormParams* out) {
+    if (n.kind < MOE_NORM_NONE || n.kind > MOE_NORM_LAYER) return arg_fail(MOE_ERR_INVALID_ARG, "norm kind");
+    out->kind = n.kind;
+    if (n.kind == MOE_NORM_NONE) return MOE_OK;
+    if (!(n.eps >= 0.0f)) return arg_fail(MOE_ERR_INVALID_ARG, "norm eps negative or NaN");
+    if ((n.w || n.b) && !float_type(n.p_dtype)) return arg_fail(MOE_ERR_UNSUPPORTED, "norm parameters neither fp32 nor bf16");
+    const size_t a = n.p_dtype == MOE_F32 ? 4 : 2;
+    if (!aligned(n.w, a) || !aligned(n.b, a)) return arg_fail(MOE_ERR_INVALID_ARG, "norm parameters misaligned");
+    out->eps = n.eps;
+    out->w_offset = n.w_offset;
+    out->p_bf16 = n.p_dtype == MOE_BF16;
+    out->w = n.w;
+    out->b = n.b;
+    return MOE_OK;
+}
+
+moe_status check_rows(int32_t T, int32_t D) {
+    if (T < 0 || D < 1) return arg_fail(MOE_ERR_INVALID_ARG, "T < 0 or D < 1");
+    if (!moe::norm_supported(D)) return arg_fail(MOE_ERR_UNSUPPORTED, "rows above 16384 elements");
+    return MOE_OK;
+}
+
+}  // namespace
+
+moe_status moe_norm_pre(const moe_norm* n, const void* x, int32_t dtype, int64_t ld_x, int32_t T, int32_t D, void* out,
+                        int32_t out_dtype, int64_t ld_out, void* stream) {
+    if (!n) return arg_fail(MOE_ERR_INVALID_ARG, "norm is NULL");
+    moe::NormParams np = {};
+    moe_status st = check_norm(*n, &np);
+    if (st != MOE_OK || (st = check_rows(T, D)) != MOE_OK) return st;
+    if (!float_type(dtype) || !float_type(out_dtype)) return arg_fail(MOE_ERR_UNSUPPORTED, "x and out must be fp32 or bf16");
+    if (T == 0) return MOE_OK;
+    if (!rows_ok(x, dtype, ld_x, D) || !rows_ok(out, out_dtype, ld_out, D))
+        return arg_fail(MOE_ERR_INVALID_ARG, "x or out NULL or misaligned, or a row stride below D");
+    MOE_CUDA(moe::launch_norm_pre(np, x, float_elem(dtype), ld_x, T, D, out, float_elem(out_dtype), ld_out,
+                                  (cudaStream_t)stream));
+    return MOE_OK;
+}
+
+moe_status moe_norm_post(const moe_post* post, const void* y, int32_t dtype, int64_t ld_y, const void* res,
+                         int32_t res_dtype, int64_t ld_res, int32_t T, int32_t D, void* out, int64_t ld_out,
+                         void* next_out, int32_t next_dtype, int64_t ld_next, void* stream) {
+    if (!post) return arg_fail(MOE_ERR_INVALID_ARG, "post is NULL");
+    moe::PostParams p = {};
+    moe_status st = check_norm(post->norm, &p.norm);
+    if (st != MOE_OK || (st = check_norm(post->next, &p.next)) != MOE_OK || (st = check_rows(T, D)) != MOE_OK) return st;
+    const bool has_next = p.next.kind != MOE_NORM_NONE;
+    if (!float_type(dtype) || !float_type(res_dtype) || (has_next && !float_type(next_dtype)))
+        return arg_fail(MOE_ERR_UNSUPPORTED, "y, res and next_out must be fp32 or bf16");
+    if (post->gate_by < MOE_GATE_NONE || post->gate_by > MOE_GATE_FULL) return arg_fail(MOE_ERR_INVALID_ARG, "gate_by");
+    if (post->gate_by != MOE_GATE_NONE && !float_type(post->gate_dtype))
+        return arg_fail(MOE_ERR_UNSUPPORTED, "the gate must be fp32 or bf16");
+    if (T == 0) return MOE_OK;
+    if (!rows_ok(y, dtype, ld_y, D) || !rows_ok(res, res_dtype, ld_res, D) || !rows_ok(out, res_dtype, ld_out, D) ||
+        (has_next && !rows_ok(next_out, next_dtype, ld_next, D)))
+        return arg_fail(MOE_ERR_INVALID_ARG, "y, res, out or next_out NULL or misaligned, or a row stride below D");
+    if (out == res && ld_out != ld_res) return arg_fail(MOE_ERR_INVALID_ARG, "out = res needs the same row stride");
+    if (post->gate_by != MOE_GATE_NONE &&
+        !rows_ok(post->gate, post->gate_dtype, post->gate_by == MOE_GATE_FULL ? post->ld_gate : D, D))
+        return arg_fail(MOE_ERR_INVALID_ARG, "gate NULL or misaligned, or a row stride below D");
+    p.T = T;
+    p.D = D;
+    p.res_scale = post->res_scale;
+    p.branch_scale = post->branch_scale;
+    p.gate_by = post->gate_by;
+    p.gate_bf16 = post->gate_dtype == MOE_BF16;
+    p.gate_sigmoid = post->gate_sigmoid != 0;
+    p.gate = post->gate;
+    p.ld_gate = post->ld_gate;
+    p.y = y;
+    p.y_elem = float_elem(dtype);
+    p.ld_y = ld_y;
+    p.res = res;
+    p.out = out;
+    p.r_elem = float_elem(res_dtype);
+    p.ld_res = ld_res;
+    p.ld_out = ld_out;
+    p.next_out = next_out;
+    p.n_elem = has_next ? float_elem(next_dtype) : moe::kBF16;
+    p.ld_next = ld_next;
+    MOE_CUDA(moe::launch_norm_post(p, (cudaStream_t)stream));
+    return MOE_OK;
+}
+
+namespace {
+moe_status check_mx(const void* x, int32_t dtype, int64_t ld, int64_t rows, int32_t cols, const void* q, const void* s) {
+    if (rows < 0 || cols < 1) return arg_fail(MOE_ERR_INVALID_ARG, "rows < 0 or cols < 1");
+    if (cols > (1 << 30)) return arg_fail(MOE_ERR_UNSUPPORTED, "cols above 2^30");
+    if (!float_type(dtype)) return arg_fail(MOE_ERR_UNSUPPORTED, "values must be fp32 or bf16");
+    if (rows == 0) return MOE_OK;
+    if (!rows_ok(x, dtype, ld, cols)) return arg_fail(MOE_ERR_INVALID_ARG, "values NULL or misaligned, or a row stride below cols");
+    if (!ptr_ok(q) || !s) return arg_fail(MOE_ERR_INVALID_ARG, "codes NULL or misaligned, or scales NULL");
+    return MOE_OK;
+}
+}  // namespace
+
+moe_status moe_mx_quantize(const void* x, int32_t dtype, int64_t ld_x, int64_t rows, int32_t cols, uint8_t* q, uint8_t* s,
+                           void* stream) {
+    const moe_status st = check_mx(x, dtype, ld_x, rows, cols, q, s);
+    if (st != MOE_OK || rows == 0) return st;
+    MOE_CUDA(moe::launch_mx_quantize(x, float_elem(dtype), ld_x, rows, cols, q, s, (cudaStream_t)stream));
+    return MOE_OK;
+}
+
+moe_status moe_mx_dequantize(const uint8_t* q, const uint8_t* s, int64_t rows, int32_t cols, void* out, int32_t out_dtype,
+                             int64_t ld_out, void* stream) {
+    const moe_status st = check_mx(out, out_dtype, ld_out, rows, cols, q, s);
+    if (st != MOE_OK || rows == 0) return st;
+    MOE_CUDA(moe::launch_mx_dequantize(q, s, rows, cols, out, float_elem(out_dtype), ld_out, (cudaStream_t)stream));
+    return MOE_OK;
+}
+
+moe_status moe_mx_gemm(const uint8_t* a, const uint8_t* a_scale, const uint8_t* b, const uint8_t* b_scale,
+                       const int32_t* offsets, int32_t rows, int32_t G, int32_t N, int32_t K, void* out, int32_t out_dtype,
+                       int64_t ld_out, void* stream) {
+    if (rows < 0 || G < 1 || N < 1 || K < 1) return arg_fail(MOE_ERR_INVALID_ARG, "rows < 0, or G, N or K < 1");
+    if (!offsets && G != 1) return arg_fail(MOE_ERR_INVALID_ARG, "offsets NULL with several groups");
+    if (K % 32 || G > 1025 || N > (1 << 20) || K > (1 << 20) || (int64_t)G * N >= ((int64_t)1 << 31) || rows > (1 << 30))
+        return arg_fail(MOE_ERR_UNSUPPORTED, "K not a multiple of 32, G above 1025, N or K above 2^20, G*N above 2^31 or rows above 2^30");
+    if (!float_type(out_dtype)) return arg_fail(MOE_ERR_UNSUPPORTED, "out must be fp32 or bf16");
+    if (rows == 0) return MOE_OK;
+    if (!ptr_ok(a) || !ptr_ok(b) || !a_scale || !b_scale) return arg_fail(MOE_ERR_INVALID_ARG, "operand NULL or misaligned");
+    if (!rows_ok(out, out_dtype, ld_out, N) || !aligned(offsets, 4))
+        return arg_fail(MOE_ERR_INVALID_ARG, "out NULL or misaligned or its row stride below N, or offsets misaligned");
+    int dev = 0;
+    MOE_CUDA(cudaGetDevice(&dev));
+    static const char key = 0;
+    int sms = 0;
+    MOE_CUDA(moe::per_device_value(&key, [dev](int* v) { return cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev); }, &sms));
+    moe::MxGemm g = {};
+    g.a = a;
+    g.a_scale = a_scale;
+    g.b = b;
+    g.b_scale = b_scale;
+    g.offsets = offsets;
+    g.rows = rows;
+    g.G = G;
+    g.N = N;
+    g.K = K;
+    g.out = out;
+    g.out_elem = float_elem(out_dtype);
+    g.ldo = ld_out;
+    MOE_CUDA(moe::launch_gemm_mx(g, sms, (cudaStream_t)stream));
+    return MOE_OK;
 }
 
 moe_status moe_pointer_kind(const void* ptr, int32_t* kind) {

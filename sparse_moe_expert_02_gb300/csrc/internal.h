@@ -194,6 +194,78 @@ cudaError_t launch_quant_blocks(const float* w, int64_t groups, int rows, int co
 cudaError_t launch_bf16_to_f16(const void* src, void* dst, int64_t n, uint32_t* err, cudaStream_t stream);
 cudaError_t launch_unpermute(const void* y, int y_elem, const int32_t* blob, const int32_t* inv, int T, int D,
                              int k, void* out, int out_elem, uint32_t* err, cudaStream_t stream);
+
+// ------------------------------------------------- operators of the block
+
+struct NormParams {
+    int kind;          // moe_norm_kind
+    float eps, w_offset;
+    int p_bf16;        // w and b are bf16 (else fp32)
+    const void* w;     // [D] or nullptr
+    const void* b;     // [D] or nullptr
+};
+struct PostParams {
+    int T, D;
+    NormParams norm, next;  // next.kind MOE_NORM_NONE: no next norm
+    float res_scale, branch_scale;
+    int gate_by, gate_bf16, gate_sigmoid;
+    const void* gate;
+    int64_t ld_gate;
+    const void* y;
+    int y_elem;
+    int64_t ld_y;
+    const void* res;
+    void* out;  // may be res
+    int r_elem;
+    int64_t ld_res, ld_out;
+    void* next_out;
+    int n_elem;
+    int64_t ld_next;
+};
+bool norm_supported(int D);
+cudaError_t launch_norm_pre(const NormParams& n, const void* x, int x_elem, int64_t ld_x, int T, int D, void* out,
+                            int out_elem, int64_t ld_out, cudaStream_t stream);
+cudaError_t launch_norm_post(const PostParams& p, cudaStream_t stream);
+
+// Microscaled 4-bit rows: codes [rows, 16 * ceil(cols/32)] bytes, scales [rows, ceil(cols/32)] bytes.
+cudaError_t launch_mx_quantize(const void* x, int x_elem, int64_t ld, int64_t rows, int cols, uint8_t* q, uint8_t* s,
+                               cudaStream_t stream);
+cudaError_t launch_mx_dequantize(const uint8_t* q, const uint8_t* s, int64_t rows, int cols, void* out, int out_elem,
+                                 int64_t ld, cudaStream_t stream);
+
+// out[r][n] = sum_k a[r][k] * b_g[n][k] over microscaled 4-bit operands.
+struct MxGemm {
+    const uint8_t* a;        // [rows, K/2]
+    const uint8_t* a_scale;  // [rows, K/32]
+    const uint8_t* b;        // [G, N, K/2]
+    const uint8_t* b_scale;  // [G, N, K/32]
+    const int32_t* offsets;  // [G+1] device, or nullptr (G = 1: all rows)
+    int rows, G, N, K;
+    void* out;               // [rows, ldo]
+    int out_elem;
+    int64_t ldo;
+};
+cudaError_t launch_gemm_mx(const MxGemm& g, int num_sms, cudaStream_t stream);
+
+// The whole layer for T <= kFewMax tokens.
+constexpr int kFewMax = 16;
+struct FewParams {
+    int T, D, E, I, k;
+    int dtype, out_elem;
+    int down_f16;  // bf16 layer: w_down is the fp16 copy
+    const void* x;
+    const void* w_router;
+    const float* b_router;
+    const void *w_gate, *w_up, *w_down;
+    const void *s_gate, *s_up, *s_down;
+    float* logits;   // [T, E]
+    int32_t* blob;   // [2, T, k]
+    float* xr;       // [T, D] x as the products read it
+    float* h;        // [T * (k + 1), I]
+    void* out;
+    uint32_t* err;
+};
+cudaError_t launch_few(const FewParams& p, cudaStream_t stream);
 cudaError_t launch_selftest_timeout(uint32_t* err, int64_t limit_ns, cudaStream_t stream);
 
 }  // namespace moe

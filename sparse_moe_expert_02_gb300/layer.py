@@ -1,7 +1,8 @@
 """MoELayer: one routed-MoE FFN layer held on the GPU, driven through libmoe.
 
 Holds the plan, the device weights (E4M3 codes and block scales for the FP8
-layer, quantised by the library's own kernel), and a workspace sized for
+layer, 4-bit codes and scales for the MXFP4 one, quantised by the library's
+own kernels), and a workspace sized for
 T_max tokens.  forward() is one moe_forward call.
 """
 from __future__ import annotations
@@ -9,6 +10,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib as L
+from . import mx
 
 _TORCH_DT = {"f32": torch.float32, "bf16": torch.bfloat16}
 
@@ -38,6 +40,14 @@ class MoELayer:
                 w[n], w[sn] = q, s
                 if keep_fp32:
                     w[n + "_f32"] = src
+        elif dtype == "mxfp4":
+            for n, sn in (("w_gate", "s_gate"), ("w_up", "s_up"), ("w_down", "s_down")):
+                src = weights[n]
+                if src.dtype == torch.uint8:          # already quantised
+                    w[n], w[sn] = src, weights[sn]
+                else:
+                    q = mx.quantize(src)
+                    w[n], w[sn] = q.codes, q.scales
         else:
             for n in ("w_gate", "w_up", "w_down"):
                 w[n] = weights.get(n)
@@ -77,6 +87,14 @@ class MoELayer:
         if out is None:
             out = self.new_out(T)
         L.moe_forward(self.plan, self.cw, x, T, out, blob_out, logits_out, self.ws)
+        return out
+
+    def forward_few(self, x: torch.Tensor, out: torch.Tensor = None, blob_out=None, logits_out=None) -> torch.Tensor:
+        """forward() for at most MOE_FEW_MAX tokens, without the permutation: one moe_forward_few call."""
+        T = x.shape[0]
+        if out is None:
+            out = self.new_out(T)
+        L.moe_forward_few(self.plan, self.cw, x, T, out, blob_out, logits_out, self.ws)
         return out
 
     def route(self, x):
