@@ -225,7 +225,7 @@ typedef struct moe_ws_layout {
                           launch's order (a permutation of 0..E, the shared group E last).
                           Written by the permutation, and only where the split can run: bf16
                           layer, T*top_k >= 64*E (see MOE_FLAG_SPLIT_GEMM_OFF) */
-    size_t few;        /* moe_forward_few, T <= MOE_FEW_MAX: f32 [T, D], then f32 [T*(top_k+1), I] */
+    size_t few;        /* moe_forward_few, T <= MOE_FEW_MAX: f32 [T*(top_k+1), I] activations h */
 } moe_ws_layout;
 
 /* Validate a configuration and build a host-side plan for `device`.

@@ -109,6 +109,7 @@ int y_elem(const moe_config& c) {
 // byte 64 one pair of unit-scheduling counters per GEMM launch of a forward
 // (each rewound to zero by the kernel that used it).
 constexpr size_t kErrBlock = 256;
+constexpr size_t kFewBarrier = 128;  // uint64 barrier count of moe_forward_few
 enum SchedSlot : int { kSchedRouter = 0, kSchedGateup = 1, kSchedDown = 2, kSchedSharedGateup = 3, kSchedSharedDown = 4 };
 
 int act_bytes(int dtype) { return dtype == MOE_F32 ? 4 : (dtype == MOE_BF16 ? 2 : 1); }
@@ -152,7 +153,7 @@ void layout(const moe_config& c, int num_sms, int T, moe_ws_layout* L) {
     L->logits_part = S > 1 ? take((size_t)S * T * c.E * 4) : 0;
     L->tiles2 = take((size_t)(c.E + 2) * 4);
     L->pairs = take((size_t)(3 * (c.E + 2) + 2) * 4);
-    L->few = T <= moe::kFewMax ? take(((size_t)T * c.D + (size_t)R * c.I) * 4) : 0;
+    L->few = T <= moe::kFewMax ? take((size_t)R * c.I * 4) : 0;
     L->total = o;
 }
 
@@ -910,13 +911,13 @@ moe_status moe_forward_few(const moe_plan* p, const moe_weights* w, const void* 
     f.s_down = w->s_down;
     f.logits = W.at<float>(W.L.logits);
     f.blob = W.at<int32_t>(W.L.blob);
-    f.xr = W.at<float>(W.L.few);
-    f.h = f.xr + (size_t)T * c.D;
+    f.h = W.at<float>(W.L.few);
     f.out = out;
     f.err = W.at<uint32_t>(W.L.err);
+    f.bar = (unsigned long long*)W.at<char>(W.L.err + kFewBarrier);
+    f.spin_ns = p->spin_ns;
     cudaStream_t s = (cudaStream_t)stream;
-    MOE_CUDA(cudaMemsetAsync(ws, 0, kErrBlock, s));
-    MOE_CUDA(moe::launch_few(f, s));
+    MOE_CUDA(moe::launch_few(f, p->num_sms, s));
     return copy_routing_out(p, W, T, blob_out, logits_out, s);
 }
 

@@ -260,12 +260,15 @@ struct FewParams {
     const void *s_gate, *s_up, *s_down;
     float* logits;   // [T, E]
     int32_t* blob;   // [2, T, k]
-    float* xr;       // [T, D] x as the products read it
-    float* h;        // [T * (k + 1), I]
+    float* h;        // [T * (k + 1), I]: routed rows by expert and token, then the shared expert's
     void* out;
     uint32_t* err;
+    unsigned long long* bar;  // grid barrier: a count that only grows, a multiple of the grid between calls
+    int64_t spin_ns;
+    // set by the launcher: a chunk of the tokens, its place in the blob, the shared-memory plan
+    int tok0, plane, hcap, ring_at, stages, tma_scales;
 };
-cudaError_t launch_few(const FewParams& p, cudaStream_t stream);
+cudaError_t launch_few(const FewParams& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_selftest_timeout(uint32_t* err, int64_t limit_ns, cudaStream_t stream);
 
 }  // namespace moe
