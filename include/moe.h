@@ -441,10 +441,13 @@ MOE_API moe_status moe_mx_dequantize(const uint8_t* q, const uint8_t* s, int64_t
  * [G, N, K/32]; K a multiple of 32.  offsets (device, [G+1], ascending) gives
  * the rows of each group, offsets[g] .. offsets[g+1]-1; NULL: G = 1, all
  * rows.  Entries outside [0, rows] are clamped to it; rows of no group are
- * left as they are.  out [rows, N] fp32 or bf16 at row stride ld_out. */
+ * left as they are.  out [rows, N] fp32 or bf16 at row stride ld_out.  err
+ * (device, uint32[4], zeroed by the caller; or NULL): receives
+ * MOE_ERR_DEVICE_TIMEOUT if a bounded device wait runs out, as a workspace's
+ * error word does; the output is then incomplete. */
 MOE_API moe_status moe_mx_gemm(const uint8_t* a, const uint8_t* a_scale, const uint8_t* b, const uint8_t* b_scale,
                                const int32_t* offsets, int32_t rows, int32_t G, int32_t N, int32_t K, void* out,
-                               int32_t out_dtype, int64_t ld_out, void* stream);
+                               int32_t out_dtype, int64_t ld_out, uint32_t* err, void* stream);
 
 MOE_API const char* moe_status_str(moe_status s);
 

@@ -123,7 +123,7 @@ def lib():
                 "moe_norm_post": (st, [P, P, I32, I64, P, I32, I64, I32, I32, P, I64, P, I32, I64, P]),
                 "moe_mx_quantize": (st, [P, I32, I64, I64, I32, P, P, P]),
                 "moe_mx_dequantize": (st, [P, P, I64, I32, P, I32, I64, P]),
-                "moe_mx_gemm": (st, [P, P, P, P, P, I32, I32, I32, I32, P, I32, I64, P]),
+                "moe_mx_gemm": (st, [P, P, P, P, P, I32, I32, I32, I32, P, I32, I64, P, P]),
             }
             for name, (res, args) in sig.items():
                 fn = getattr(L, name)
@@ -334,10 +334,10 @@ def moe_mx_dequantize(q, s, out, stream=None):
         "moe_mx_dequantize")
 
 
-def moe_mx_gemm(a, a_scale, b, b_scale, offsets, G: int, N: int, K: int, out, stream=None):
+def moe_mx_gemm(a, a_scale, b, b_scale, offsets, G: int, N: int, K: int, out, err=None, stream=None):
     op, ot, ol = _rows(out, "out")
     _ok(lib().moe_mx_gemm(_ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale), _ptr(offsets), out.shape[0], G, N, K, op, ot,
-                          ol, _stream(stream)), "moe_mx_gemm")
+                          ol, _ptr(err), _stream(stream)), "moe_mx_gemm")
 
 
 def moe_launch_count() -> int:

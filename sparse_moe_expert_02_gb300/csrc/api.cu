@@ -109,6 +109,7 @@ int y_elem(const moe_config& c) {
 // byte 64 one pair of unit-scheduling counters per GEMM launch of a forward
 // (each rewound to zero by the kernel that used it).
 constexpr size_t kErrBlock = 256;
+constexpr int64_t kDefaultSpinNs = 2000000000LL;
 constexpr size_t kFewBarrier = 128;  // uint64 barrier count of moe_forward_few
 enum SchedSlot : int { kSchedRouter = 0, kSchedGateup = 1, kSchedDown = 2, kSchedSharedGateup = 3, kSchedSharedDown = 4 };
 
@@ -319,7 +320,7 @@ moe_status moe_plan_create(const moe_config* cfg, int device, moe_plan** out) {
     p->cfg = c;
     p->device = device;
     p->num_sms = sms;
-    p->spin_ns = c.spin_limit_ns ? c.spin_limit_ns : 2000000000LL;
+    p->spin_ns = c.spin_limit_ns ? c.spin_limit_ns : kDefaultSpinNs;
     int prev = 0;
     cudaGetDevice(&prev);
     if (cudaSetDevice(device) != cudaSuccess ||
@@ -1044,7 +1045,7 @@ moe_status moe_mx_dequantize(const uint8_t* q, const uint8_t* s, int64_t rows, i
 
 moe_status moe_mx_gemm(const uint8_t* a, const uint8_t* a_scale, const uint8_t* b, const uint8_t* b_scale,
                        const int32_t* offsets, int32_t rows, int32_t G, int32_t N, int32_t K, void* out, int32_t out_dtype,
-                       int64_t ld_out, void* stream) {
+                       int64_t ld_out, uint32_t* err, void* stream) {
     if (rows < 0 || G < 1 || N < 1 || K < 1) return arg_fail(MOE_ERR_INVALID_ARG, "rows < 0, or G, N or K < 1");
     if (!offsets && G != 1) return arg_fail(MOE_ERR_INVALID_ARG, "offsets NULL with several groups");
     if (K % 32 || G > 1025 || N > (1 << 20) || K > (1 << 20) || (int64_t)G * N >= ((int64_t)1 << 31) || rows > (1 << 30))
@@ -1052,8 +1053,8 @@ moe_status moe_mx_gemm(const uint8_t* a, const uint8_t* a_scale, const uint8_t* 
     if (!float_type(out_dtype)) return arg_fail(MOE_ERR_UNSUPPORTED, "out must be fp32 or bf16");
     if (rows == 0) return MOE_OK;
     if (!ptr_ok(a) || !ptr_ok(b) || !a_scale || !b_scale) return arg_fail(MOE_ERR_INVALID_ARG, "operand NULL or misaligned");
-    if (!rows_ok(out, out_dtype, ld_out, N) || !aligned(offsets, 4))
-        return arg_fail(MOE_ERR_INVALID_ARG, "out NULL or misaligned or its row stride below N, or offsets misaligned");
+    if (!rows_ok(out, out_dtype, ld_out, N) || !aligned(offsets, 4) || !aligned(err, 4))
+        return arg_fail(MOE_ERR_INVALID_ARG, "out NULL or misaligned or its row stride below N, or offsets or err misaligned");
     int dev = 0;
     MOE_CUDA(cudaGetDevice(&dev));
     static const char key = 0;
@@ -1072,6 +1073,8 @@ moe_status moe_mx_gemm(const uint8_t* a, const uint8_t* a_scale, const uint8_t* 
     g.out = out;
     g.out_elem = float_elem(out_dtype);
     g.ldo = ld_out;
+    g.err = err;
+    g.spin_ns = kDefaultSpinNs;
     MOE_CUDA(moe::launch_gemm_mx(g, sms, (cudaStream_t)stream));
     return MOE_OK;
 }

@@ -244,6 +244,8 @@ struct MxGemm {
     void* out;               // [rows, ldo]
     int out_elem;
     int64_t ldo;
+    uint32_t* err;           // device error word or nullptr
+    int64_t spin_ns;
 };
 cudaError_t launch_gemm_mx(const MxGemm& g, int num_sms, cudaStream_t stream);
 

@@ -57,11 +57,12 @@ def dequantize(q: MXTensor, dtype: torch.dtype = torch.bfloat16, out: torch.Tens
 
 
 def matmul(a: MXTensor, b: MXTensor, offsets: torch.Tensor = None, out: torch.Tensor = None,
-           out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+           out_dtype: torch.dtype = torch.bfloat16, err: torch.Tensor = None) -> torch.Tensor:
     """a [rows, K] times b [N, K] (or one of b [G, N, K] for each row) transposed.
 
     offsets: int32 [G+1] on the device, group g's rows are offsets[g] ..
-    offsets[g+1]-1; rows of no group are left as they are in out.
+    offsets[g+1]-1; rows of no group are left as they are in out.  err: int32
+    [4], zeroed, receives a device error (see moe_mx_gemm).
     """
     if len(a.shape) != 2 or len(b.shape) not in (2, 3) or a.cols != b.cols:
         raise ValueError(f"matmul: a [rows, K] and b [N, K] or [G, N, K], not {a.shape} and {b.shape}")
@@ -75,5 +76,5 @@ def matmul(a: MXTensor, b: MXTensor, offsets: torch.Tensor = None, out: torch.Te
         out = torch.empty((rows, N), dtype=out_dtype, device=a.codes.device)
     elif tuple(out.shape) != (rows, N):
         raise ValueError(f"out: shape {(rows, N)}, not {tuple(out.shape)}")
-    L.moe_mx_gemm(a.codes, a.scales, b.codes, b.scales, offsets, G, N, a.cols, out)
+    L.moe_mx_gemm(a.codes, a.scales, b.codes, b.scales, offsets, G, N, a.cols, out, err)
     return out

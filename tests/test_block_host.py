@@ -74,10 +74,10 @@ def test_norm_post_checks_before_any_launch(post, change, status):
     (dict(rows=-1), L.MOE_ERR_INVALID_ARG), (dict(G=0), L.MOE_ERR_INVALID_ARG), (dict(K=48), L.MOE_ERR_UNSUPPORTED),
     (dict(offsets=0, G=2), L.MOE_ERR_INVALID_ARG), (dict(G=1026), L.MOE_ERR_UNSUPPORTED), (dict(a=8), L.MOE_ERR_INVALID_ARG),
     (dict(out_dtype=2), L.MOE_ERR_UNSUPPORTED), (dict(ld_out=7), L.MOE_ERR_INVALID_ARG), (dict(b_scale=0), L.MOE_ERR_INVALID_ARG),
-    (dict(offsets=6), L.MOE_ERR_INVALID_ARG), (dict(rows=0), L.MOE_OK),
+    (dict(offsets=6), L.MOE_ERR_INVALID_ARG), (dict(err=6), L.MOE_ERR_INVALID_ARG), (dict(rows=0), L.MOE_OK),
 ])
 def test_mx_gemm_checks_before_any_launch(change, status):
-    a = dict(a=16, a_scale=1, b=16, b_scale=1, offsets=4, rows=3, G=1, N=8, K=64, out=16, out_dtype=0, ld_out=8) | change
+    a = dict(a=16, a_scale=1, b=16, b_scale=1, offsets=4, rows=3, G=1, N=8, K=64, out=16, out_dtype=0, ld_out=8, err=0) | change
     assert L.lib().moe_mx_gemm(*a.values(), None) == status
 
 
