@@ -7,11 +7,12 @@
 // stage (a 128-byte swizzled line per row: 16 KB of A, 32 KB of B), four
 // stages.  The scales' home is tensor memory, in chunks of 128 rows x 4
 // blocks: lane = row % 32, word = row / 32, byte = block, which is not how
-// rows of scale bytes lie in memory; four warps read the stage's scale bytes
-// (a row or two a thread, two stages ahead), write them to shared memory in
-// that order, and the MMA thread copies them on with tcgen05.cp before the
-// stage's four MMAs.  Each stage has its own 24 columns of scales, reused
-// when the stage is, so the stage barriers order the copies too.
+// rows of scale bytes lie in memory; four warps read the scale bytes (two
+// stages of a row a load, a row of A and two of B a thread, two loads ahead),
+// write them to shared memory in that order, and the MMA thread copies them
+// on with tcgen05.cp, a stage ahead of its MMAs.  Each stage has its own 24
+// columns of scales, reused when the stage is, so the stage barriers order
+// the copies too.
 //
 // 448 threads: warp 0 TMA, warp 1 tensor memory + MMA, warps 2-5 scales,
 // warps 6-13 epilogue (two per lane quarter, 128 columns each).  The
@@ -98,23 +99,23 @@ __device__ __forceinline__ Unit unit_at(const MxGemm& p, int u, int NB, const in
     return r;
 }
 
-// The eight scale bytes of a row from block b0 (blocks past the row's end:
-// scale 1; their codes are zeros).  VEC: bytes that rows are aligned to.
-template <int VEC> __device__ __forceinline__ uint2 load_scales(const uint8_t* row, int b0, int blocks) {
-    uint2 v = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-    if constexpr (VEC == 8) {
-        v = __ldg((const uint2*)(row + b0));
+// The sixteen scale bytes of a row from block b0, two stages' worth (blocks
+// past the row's end: scale 1; their codes are zeros).  VEC: bytes that rows
+// are aligned to.
+template <int VEC> __device__ __forceinline__ uint4 load_scales(const uint8_t* row, int b0, int blocks) {
+    uint32_t w[4] = {0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu};
+    if constexpr (VEC == 16) {
+        return __ldg((const uint4*)(row + b0));
     } else if constexpr (VEC == 4) {
-        v.x = __ldg((const uint32_t*)(row + b0));
-        if (b0 + 4 < blocks) v.y = __ldg((const uint32_t*)(row + b0 + 4));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (b0 + 4 * j < blocks) w[j] = __ldg((const uint32_t*)(row + b0 + 4 * j));
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (b0 + i < blocks) v.x = (v.x & ~(255u << (8 * i))) | (uint32_t)__ldg(row + b0 + i) << (8 * i);
-            if (b0 + 4 + i < blocks) v.y = (v.y & ~(255u << (8 * i))) | (uint32_t)__ldg(row + b0 + 4 + i) << (8 * i);
-        }
+        for (int i = 0; i < 16; ++i)
+            if (b0 + i < blocks) w[i / 4] = (w[i / 4] & ~(255u << (8 * (i & 3)))) | (uint32_t)__ldg(row + b0 + i) << (8 * (i & 3));
     }
-    return v;
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <int VEC>
@@ -123,16 +124,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint64_t* bars = (uint64_t*)(smem + kOffBar);
-    const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + kStages);
-    const uint32_t tfull = smem_u32(bars + 2 * kStages), tempty = smem_u32(bars + 2 * kStages + 1), drain = smem_u32(bars + 2 * kStages + 2);
-    uint32_t* tmem_slot = (uint32_t*)(bars + 2 * kStages + 3);
+    const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + kStages), sfull0 = smem_u32(bars + 2 * kStages);
+    const uint32_t tfull = smem_u32(bars + 3 * kStages), tempty = smem_u32(bars + 3 * kStages + 1), drain = smem_u32(bars + 3 * kStages + 2);
+    uint32_t* tmem_slot = (uint32_t*)(bars + 3 * kStages + 3);
     volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
     int32_t* pre = (int32_t*)(smem + kOffTab);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int NB = (p.N + BN - 1) / BN, KB = (p.K / 2 + kKB - 1) / kKB;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(full0 + 8 * s, 1 + kScaleWarps);
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(sfull0 + 8 * s, kScaleWarps);
             mbar_init(empty0 + 8 * s, 1);
         }
         mbar_init(tfull, 1);
@@ -202,9 +204,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         if (lane == 0) {
             // ----------------------------------------------- MMA issuer
-            int stage = 0;
-            uint32_t phase = 0, acc_phase = 0;
+            // A stage's scales are copied before the MMAs of the stage before
+            // it are issued, so that the copies run beside them.
+            int stage = 0, cstage = 0;
+            uint32_t phase = 0, cphase = 0, acc_phase = 0;
             bool ok = true;
+            int64_t copies = units > (int)blockIdx.x ? (int64_t)((units - 1 - blockIdx.x) / gridDim.x + 1) * KB : 0;  // left to make
+            auto copy_scales = [&]() {
+                if (copies-- <= 0 || !ok) return;
+                ok = mbar_wait(sfull0 + 8 * cstage, cphase, lim, abort_flag);
+                if (!ok) {
+                    record_error(p.err, MOE_ERR_DEVICE_TIMEOUT, 55, blockIdx.x, 0);
+                    *abort_flag = 1;
+                    return;
+                }
+                tc_fence_after();
+                const uint32_t sf = smem_u32(smem + kOffSf + cstage * kSfBytes), t = tmem + kAccCols + cstage * kSfCols;
+#pragma unroll
+                for (int c = 0; c < 6; ++c) copy_sf(t + 4 * c, sf + c * kSfChunk);
+                if (++cstage == kStages) {
+                    cstage = 0;
+                    cphase ^= 1;
+                }
+            };
+            copy_scales();
             for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
                 ok = mbar_wait(tempty, acc_phase ^ 1, lim, abort_flag);
                 if (!ok) {
@@ -214,19 +237,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_after();
                 for (int kb = 0; kb < KB; ++kb) {
-                    ok = mbar_wait(full0 + 8 * stage, phase, lim, abort_flag);
+                    copy_scales();
+                    ok = ok && mbar_wait(full0 + 8 * stage, phase, lim, abort_flag);
                     if (!ok) {
                         record_error(p.err, MOE_ERR_DEVICE_TIMEOUT, 53, blockIdx.x, u);
                         *abort_flag = 1;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sf = smem_u32(smem + kOffSf + stage * kSfBytes);
                     const uint32_t sfa = tmem + kAccCols + stage * kSfCols, sfb = sfa + 8;
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) copy_sf(sfa + 4 * c, sf + c * kSfChunk);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) copy_sf(sfb + 4 * c, sf + (2 + c) * kSfChunk);
                     const uint64_t ad = umma_desc(smem_u32(smem + stage * kABytes));
                     const uint64_t bd = umma_desc(smem_u32(smem + kOffB + stage * kBBytes));
 #pragma unroll
@@ -249,61 +268,72 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp < 2 + kScaleWarps) {
         // ------------------------------------------------------- scales
-        // Thread r: row r of A, rows r and 128 + r of B.  Two stages' bytes
-        // are in flight in registers ahead of the one being written.
+        // Thread r: row r of A, rows r and 128 + r of B, sixteen bytes (two
+        // stages) a load; the next two loads of a row are in flight in
+        // registers ahead of the stages being written.
         const int r = threadIdx.x - 64, blocks = p.K / kMxBlock;
         const int64_t brows = (int64_t)p.G * p.N;
+        const int pairs = (KB + 1) / 2;  // loads of a unit
         const uint8_t *ra = nullptr, *rb0 = nullptr, *rb1 = nullptr;
-        int fu = blockIdx.x, fkb = 0;  // the stage to fetch next
-        uint2 q[2][3];
-        auto fetch = [&](uint2 (&v)[3]) {
+        int fu = blockIdx.x, fp = 0;  // the load to issue next
+        uint4 q[2][3];
+        auto fetch = [&](uint4 (&v)[3]) {
             if (fu >= units) return;
-            if (fkb == 0) {
+            if (fp == 0) {
                 const Unit un = unit_at(p, fu, NB, pre);
                 ra = p.a_scale + (int64_t)min(un.row0 + r, p.rows - 1) * blocks;
                 const int64_t b = (int64_t)un.g * p.N + un.n0 + r;
                 rb0 = p.b_scale + min(b, brows - 1) * blocks;
                 rb1 = p.b_scale + min(b + 128, brows - 1) * blocks;
             }
-            v[0] = load_scales<VEC>(ra, fkb * kBlk, blocks);
-            v[1] = load_scales<VEC>(rb0, fkb * kBlk, blocks);
-            v[2] = load_scales<VEC>(rb1, fkb * kBlk, blocks);
-            if (++fkb == KB) {
-                fkb = 0;
+            v[0] = load_scales<VEC>(ra, fp * 2 * kBlk, blocks);
+            v[1] = load_scales<VEC>(rb0, fp * 2 * kBlk, blocks);
+            v[2] = load_scales<VEC>(rb1, fp * 2 * kBlk, blocks);
+            if (++fp == pairs) {
+                fp = 0;
                 fu += gridDim.x;
             }
         };
         fetch(q[0]);
         fetch(q[1]);
-        int stage = 0;
+        int stage = 0, left = KB;  // stages left of the unit being written
         uint32_t phase = 0;
-        const int64_t total = units > (int)blockIdx.x ? (int64_t)((units - 1 - blockIdx.x) / gridDim.x + 1) * KB : 0;
+        const int64_t total = units > (int)blockIdx.x ? (int64_t)((units - 1 - blockIdx.x) / gridDim.x + 1) * pairs : 0;
         // chunk: k half of A; then for each k half the two 128-row halves of B
         uint8_t* dst0 = smem + kOffSf + (r & 31) * 16 + (r >> 5) * 4;
-        auto put = [&](const uint2 (&v)[3]) -> bool {
+        auto put = [&](uint32_t a0, uint32_t a1, uint32_t b00, uint32_t b01, uint32_t b10, uint32_t b11) -> bool {
             const bool ok = mbar_wait(empty0 + 8 * stage, phase ^ 1, lim, abort_flag);
             if (!__all_sync(0xffffffffu, ok)) return false;
             uint8_t* dst = dst0 + stage * kSfBytes;
-            *(uint32_t*)(dst) = v[0].x;
-            *(uint32_t*)(dst + kSfChunk) = v[0].y;
-            *(uint32_t*)(dst + 2 * kSfChunk) = v[1].x;
-            *(uint32_t*)(dst + 3 * kSfChunk) = v[2].x;
-            *(uint32_t*)(dst + 4 * kSfChunk) = v[1].y;
-            *(uint32_t*)(dst + 5 * kSfChunk) = v[2].y;
+            *(uint32_t*)(dst) = a0;
+            *(uint32_t*)(dst + kSfChunk) = a1;
+            *(uint32_t*)(dst + 2 * kSfChunk) = b00;
+            *(uint32_t*)(dst + 3 * kSfChunk) = b10;
+            *(uint32_t*)(dst + 4 * kSfChunk) = b01;
+            *(uint32_t*)(dst + 5 * kSfChunk) = b11;
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive(full0 + 8 * stage);
+            if (lane == 0) mbar_arrive(sfull0 + 8 * stage);
             if (++stage == kStages) {
                 stage = 0;
                 phase ^= 1;
             }
             return true;
         };
+        auto put2 = [&](const uint4 (&v)[3]) -> bool {
+            if (!put(v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y)) return false;
+            if (--left > 0) {
+                if (!put(v[0].z, v[0].w, v[1].z, v[1].w, v[2].z, v[2].w)) return false;
+                --left;
+            }
+            if (left <= 0) left = KB;
+            return true;
+        };
         for (int64_t i = 0; i < total; i += 2) {
-            if (!put(q[0])) break;
+            if (!put2(q[0])) break;
             fetch(q[0]);
             if (i + 1 < total) {
-                if (!put(q[1])) break;
+                if (!put2(q[1])) break;
                 fetch(q[1]);
             }
         }
@@ -422,7 +452,7 @@ cudaError_t launch_gemm_mx(const MxGemm& g, int num_sms, cudaStream_t stream) {
     const int grid = (int)std::min<int64_t>(units, num_sms);
     const int blocks = g.K / kMxBlock;
     const uintptr_t al = (uintptr_t)g.a_scale | (uintptr_t)g.b_scale;
-    if (blocks % 8 == 0 && al % 8 == 0) return launch<8>(g, a, b, grid, stream);
+    if (blocks % 16 == 0 && al % 16 == 0) return launch<16>(g, a, b, grid, stream);
     if (blocks % 4 == 0 && al % 4 == 0) return launch<4>(g, a, b, grid, stream);
     return launch<1>(g, a, b, grid, stream);
 }
