@@ -87,6 +87,8 @@ def lib_path() -> str:
 def lib():
     """Load libmoe (building it first if the sources changed)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.build()
@@ -150,10 +152,17 @@ def _ptr(t, host_mapped_ok: bool = False):
     return t.data_ptr()
 
 
+# torch.cuda.current_stream() without the Stream object it builds (3 us a
+# call, as much as a small operator's launch).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return stream.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _ok(status: int, where: str):
@@ -293,10 +302,11 @@ def _rows(t, what: str):
         raise ValueError(f"{what}: fp32 or bf16, not {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{what}: libmoe takes device tensors")
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+    s = t.stride()
+    if len(s) != 2 or (s[1] != 1 and t.size(1) > 1):
         raise ValueError(f"{what}: a 2-D tensor whose rows are contiguous")
     # the stride of a single row says nothing (it may be anything)
-    return t.data_ptr(), dt, t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return t.data_ptr(), dt, s[0] if t.size(0) > 1 else t.size(1)
 
 
 def moe_forward_few(plan, weights: moe_weights, x, T, out, blob_out, logits_out, ws, stream=None):

@@ -75,20 +75,13 @@ static_assert(kAccCols + kSfSlots * kSfCols <= 512, "tensor memory plan");
 static_assert((2 * kMaxStages + 5) * 8 + 8 <= 256, "barrier block overflows");
 
 // Instruction descriptor of kind::mxf4: E2M1 operands, both K-major, E8M0
-// scales, m features and n rows; sf: which half of the scale words (0 or 2).
-__device__ __forceinline__ uint32_t idesc(int m, int n, int sf) {
-    return ((uint32_t)sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(m >> 4) << 24) |
+// scales, n rows; sf: which half of the scale words (0 or 2).
+__device__ __forceinline__ uint32_t idesc(int n, int sf) {
+    return ((uint32_t)sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(BF >> 4) << 24) |
            ((uint32_t)sf << 29);
 }
-template <bool PAIR>
 __device__ __forceinline__ void umma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t sfa, uint32_t sfb, uint32_t acc) {
-    if (PAIR)
-        asm volatile(
-            "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-            " tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
-            "l"(a), "l"(b), "r"(id), "r"(sfa), "r"(sfb), "r"(acc)
-            : "memory");
-    else asm volatile(
+    asm volatile(
         "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
         " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
         "l"(a), "l"(b), "r"(id), "r"(sfa), "r"(sfb), "r"(acc)
@@ -96,12 +89,9 @@ __device__ __forceinline__ void umma_mxf4(uint32_t d, uint64_t a, uint64_t b, ui
 }
 // One chunk of scales, shared memory to tensor memory (all four quarters):
 // 32 rows of 16 bytes, eight-row groups 128 bytes apart, no swizzle.
-// On a CTA pair each CTA's tensor memory receives its own shared memory's.
-template <bool PAIR>
 __device__ __forceinline__ void copy_sf(uint32_t tmem, uint32_t saddr) {
     const uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
-    if (PAIR) asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
-    else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
 }
 __device__ __forceinline__ void st_cluster(uint32_t addr, float4 v) {
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
@@ -117,21 +107,12 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.b32 %0, 1, 0, q;\n}\n" : "=r"(p));
     return p != 0;
 }
-// Arrival on the pair's leader: the CTA's own writes that it tells of were
-// made visible to the async proxy, which alone reads them, by the proxy fence
-// before; a release at cluster scope would wait for the thread's loads in
-// flight as well (126 us against 69 at 8192 x 4096 x 4096).
-__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
 // A bounded wait of the whole warp; the first to fail records where.
-template <bool PAIR>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int64_t lim, volatile int* abort_flag, uint32_t* err, int where) {
     const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, lim, abort_flag));
     if (!ok && elect_one() && !*abort_flag) {
         record_error(err, MOE_ERR_DEVICE_TIMEOUT, where, blockIdx.x, 0);
-        if (PAIR) raise_abort_pair(abort_flag, cluster_rank());
-        else *abort_flag = 1;
+        *abort_flag = 1;
     }
     return ok;
 }
@@ -149,11 +130,10 @@ struct Unit {
 // pre: prefix of the groups' row tiles, then each group's first row; in
 // shared memory: the offsets themselves are some 1000 cycles away, which the
 // MMA warp would wait for at every tile.
-template <int WIDTH>
 __device__ __forceinline__ Unit unit_at(const MxGemm& p, const Plan& q, int u, int FB, const int32_t* pre) {
     Unit r;
     const int rt = u / FB;
-    r.f0 = (u - rt * FB) * WIDTH;
+    r.f0 = (u - rt * FB) * BF;
     r.g = 0;
     int lo = 0, hi = p.rows, t = rt;
     if (p.offsets) {
@@ -219,14 +199,10 @@ __device__ __forceinline__ void store_block(uint8_t* st, const uint32_t* w, bf16
     }
 }
 
-enum Mode : int { kPlain = 0, kSplit = 1, kPair = 2 };
-
-template <int VEC, int MODE>
+template <int VEC, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_mx_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_r64,
                    const __grid_constant__ CUtensorMap tm_r16, const MxGemm p, const Plan pl) {
-    constexpr bool SPLIT = MODE == kSplit, PAIR = MODE == kPair;
-    constexpr int WIDTH = PAIR ? 2 * BF : BF;  // features of a tile
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* bars = (uint64_t*)(smem + kOffBar);
     const int S = pl.stages, slots = min(kSfSlots, S);
@@ -237,22 +213,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
     int32_t* pre = (int32_t*)(smem + kOffTab);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int FB = (p.N + WIDTH - 1) / WIDTH, KB = (p.K / 2 + kKB - 1) / kKB;
+    const int FB = (p.N + BF - 1) / BF, KB = (p.K / 2 + kKB - 1) / kKB;
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(full0 + 8 * s, 1 + (PAIR ? 2 : 1) * kScaleWarps);
+            mbar_init(full0 + 8 * s, 1 + kScaleWarps);
             mbar_init(empty0 + 8 * s, 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull0 + 8 * b, 1);
-            mbar_init(tempty0 + 8 * b, (PAIR ? 2 : 1) * kEpiWarps);
+            mbar_init(tempty0 + 8 * b, kEpiWarps);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (PAIR && warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 512);
-    if (!PAIR && warp == 1) {
+    if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -282,13 +257,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (PAIR) cluster_sync();  // the peer's barriers and tensor memory exist
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     // Units of this CTA: u0, u0 + step, ...; k-blocks [kb0, kb1) of each.  Split: a cluster takes one
     // unit (or none: the grid covers a bound on their number).
     const int units = (p.offsets ? pre[p.G] : (p.rows + pl.tile_rows - 1) / pl.tile_rows) * FB;
-    const int rank = SPLIT || PAIR ? (int)cluster_rank() : 0, cl = SPLIT ? pl.split : PAIR ? 2 : 1;
+    const int rank = SPLIT ? (int)cluster_rank() : 0, cl = SPLIT ? pl.split : 1;
     const int u0 = (int)blockIdx.x / cl, step = (int)gridDim.x / cl;
     const int KB2 = (KB + 1) / 2;  // split at even blocks: a load of scales is two
     const int kb0 = SPLIT ? 2 * (KB2 * rank / pl.split) : 0, kb1 = SPLIT ? min(KB, 2 * (KB2 * (rank + 1) / pl.split)) : KB;
@@ -301,26 +275,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t phase = 0;
         bool ok = true;
         for (int u = u0; u < units && ok; u += step) {
-            const Unit un = unit_at<WIDTH>(p, pl, u, FB, pre);
+            const Unit un = unit_at(p, pl, u, FB, pre);
             // whole 64-row boxes, then 16-row boxes (rows past the tile are read and ignored)
-            // a pair's CTAs each take their 128 features and half of the rows
-            const int n16 = __shfl_sync(0xffffffffu, PAIR ? (un.rows + 31) >> 5 : (un.rows + 15) >> 4, 0), n64 = n16 >> 2, rest = n16 & 3;
-            const int wrow = __shfl_sync(0xffffffffu, un.g * p.N + un.f0 + (PAIR ? rank * BF : 0), 0);
-            const int row0 = __shfl_sync(0xffffffffu, un.row0 + (PAIR ? rank * n16 * 16 : 0), 0);
+            const int n16 = __shfl_sync(0xffffffffu, (un.rows + 15) >> 4, 0), n64 = n16 >> 2, rest = n16 & 3;
+            const int wrow = __shfl_sync(0xffffffffu, un.g * p.N + un.f0, 0);
+            const int row0 = __shfl_sync(0xffffffffu, un.row0, 0);
             for (int kb = kb0; kb < kb1; ++kb) {
-                ok = warp_wait<PAIR>(empty0 + 8 * stage, phase ^ 1, lim, abort_flag, p.err, 51);
+                ok = warp_wait(empty0 + 8 * stage, phase ^ 1, lim, abort_flag, p.err, 51);
                 if (!ok) break;
                 if (elect_one()) {
-                    // (a pair's loads all count on the leader's barrier)
-                    const uint32_t fb = PAIR ? mapa_shared(full0 + 8 * stage, 0) : full0 + 8 * stage, base = smem0 + stage * pl.stage_bytes;
-                    if (!PAIR || rank == 0) mbar_expect_tx(full0 + 8 * stage, (PAIR ? 2 : 1) * (kWBytes + n16 * 16 * kKB));
-                    auto load = [&](uint32_t dst, const CUtensorMap* map, int row) {
-                        if (PAIR) tma_load_2d_pair(dst, map, fb, kb * kKB, row);
-                        else tma_load_2d(dst, map, fb, kb * kKB, row);
-                    };
-                    load(base, &tm_w, wrow);
-                    for (int i = 0; i < n64; ++i) load(base + kWBytes + i * 64 * kKB, &tm_r64, row0 + i * 64);
-                    for (int i = 0; i < rest; ++i) load(base + kWBytes + (n64 * 64 + i * 16) * kKB, &tm_r16, row0 + n64 * 64 + i * 16);
+                    const uint32_t fb = full0 + 8 * stage, base = smem0 + stage * pl.stage_bytes;
+                    mbar_expect_tx(fb, kWBytes + n16 * 16 * kKB);
+                    tma_load_2d(base, &tm_w, fb, kb * kKB, wrow);
+                    for (int i = 0; i < n64; ++i) tma_load_2d(base + kWBytes + i * 64 * kKB, &tm_r64, fb, kb * kKB, row0 + i * 64);
+                    for (int i = 0; i < rest; ++i)
+                        tma_load_2d(base + kWBytes + (n64 * 64 + i * 16) * kKB, &tm_r16, fb, kb * kKB, row0 + n64 * 64 + i * 16);
                 }
                 __syncwarp();
                 if (++stage == S) {
@@ -331,8 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) sleep_ns(200000);  // copies already issued land before the CTA leaves
     } else if (warp == 1) {
-      if (!PAIR || rank == 0) {
-        // ------------------------------- MMA issuer (of a pair: the leader)
+        // --------------------------------------------------- MMA issuer
         // One wait a stage (its barrier counts the operands' bytes and the
         // scale warps): the issue of a stage takes about as long as its MMAs.
         int stage = 0, slot = 0, acc = 0;
@@ -340,19 +308,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         const bool wide = pl.tile_rows > 128;
         const uint32_t rstep = wide ? 8 : 4;
-        auto commit = [&](uint32_t bar) {
-            if (PAIR) umma_commit_pair(bar);
-            else umma_commit(bar);
-        };
         for (int u = u0; u < units && ok; u += step) {
-            const Unit un = unit_at<WIDTH>(p, pl, u, FB, pre);
-            const int n = __shfl_sync(0xffffffffu, PAIR ? (un.rows + 31) & ~31 : (un.rows + 15) & ~15, 0);
-            const uint32_t id0 = idesc(WIDTH, n, 0), id2 = idesc(WIDTH, n, 2);
-            ok = warp_wait<PAIR>(tempty0 + 8 * acc, acc_phase ^ 1, lim, abort_flag, p.err, 52);
+            const Unit un = unit_at(p, pl, u, FB, pre);
+            const int n = __shfl_sync(0xffffffffu, (un.rows + 15) & ~15, 0);
+            const uint32_t id0 = idesc(n, 0), id2 = idesc(n, 2);
+            ok = warp_wait(tempty0 + 8 * acc, acc_phase ^ 1, lim, abort_flag, p.err, 52);
             if (!ok) break;
             const uint32_t d = tmem + acc * 128;
             for (int kb = kb0; kb < kb1; ++kb) {
-                ok = warp_wait<PAIR>(full0 + 8 * stage, phase, lim, abort_flag, p.err, 53);
+                ok = warp_wait(full0 + 8 * stage, phase, lim, abort_flag, p.err, 53);
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
@@ -360,19 +324,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // rows lie at 8 + 8 half, for 128 at 8 + 4 half)
                     const uint32_t sf = smem0 + kOffSf + slot * kSfBytes, sfw = tmem + kAccCols + slot * kSfCols, sfr = sfw + 8;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) copy_sf<PAIR>(sfw + 4 * c, sf + c * kSfChunk);
+                    for (int c = 0; c < 4; ++c) copy_sf(sfw + 4 * c, sf + c * kSfChunk);
                     if (wide) {
-                        copy_sf<PAIR>(sfw + 16, sf + 4 * kSfChunk);
-                        copy_sf<PAIR>(sfw + 20, sf + 5 * kSfChunk);
+                        copy_sf(sfw + 16, sf + 4 * kSfChunk);
+                        copy_sf(sfw + 20, sf + 5 * kSfChunk);
                     }
                     const uint64_t wd = umma_desc(smem0 + stage * pl.stage_bytes);
                     const uint64_t rd = umma_desc(smem0 + stage * pl.stage_bytes + kWBytes);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        umma_mxf4<PAIR>(d, wd + (uint64_t)(kk * 2), rd + (uint64_t)(kk * 2), kk & 1 ? id2 : id0, sfw + 4 * (kk >> 1),
+                        umma_mxf4(d, wd + (uint64_t)(kk * 2), rd + (uint64_t)(kk * 2), kk & 1 ? id2 : id0, sfw + 4 * (kk >> 1),
                                         sfr + rstep * (kk >> 1), kb != kb0 || kk != 0);
-                    commit(empty0 + 8 * stage);
-                    if (kb + 1 == kb1) commit(tfull0 + 8 * acc);
+                    umma_commit(empty0 + 8 * stage);
+                    if (kb + 1 == kb1) umma_commit(tfull0 + 8 * acc);
                 }
                 __syncwarp();
                 if (++stage == S) {
@@ -386,11 +350,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 acc_phase ^= 1;
             }
         }
-        if (elect_one()) commit(drain);  // everything issued is done before tensor memory is freed
+        if (elect_one()) umma_commit(drain);  // everything issued is done before tensor memory is freed
         __syncwarp();
         volatile int never = 0;
         mbar_wait(drain, 0, 1000000000LL, &never);
-      }
     } else if (warp < 2 + kScaleWarps) {
         // ------------------------------------------------------- scales
         // Thread r: weight row r, rows r and 128 + r of the tile, sixteen
@@ -411,8 +374,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto fetch = [&](uint4 (&v)[3]) {
             if (fu >= units) return;
             if (fp == 0) {
-                const Unit un = unit_at<WIDTH>(p, pl, fu, FB, pre);
-                rw = p.b_scale + min((int64_t)un.g * p.N + un.f0 + (PAIR ? rank * BF : 0) + r, wrows - 1) * blocks;
+                const Unit un = unit_at(p, pl, fu, FB, pre);
+                rw = p.b_scale + min((int64_t)un.g * p.N + un.f0 + r, wrows - 1) * blocks;
                 r0 = p.a_scale + (int64_t)min(un.row0 + r, p.rows - 1) * blocks;
                 r1 = p.a_scale + (int64_t)min(un.row0 + r + 128, p.rows - 1) * blocks;
             }
@@ -448,10 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (++slot == slots) slot = 0;
         };
         auto tell = [&]() {
-            if (lane == 0) {
-                if (PAIR) mbar_arrive_cluster_relaxed(mapa_shared(full0 + 8 * stage, 0));
-                else mbar_arrive(full0 + 8 * stage);
-            }
+            if (lane == 0) mbar_arrive(full0 + 8 * stage);
             if (++stage == S) stage = 0;
         };
         auto put2 = [&](const uint4 (&v)[3]) -> bool {
@@ -498,24 +458,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int u = u0; u < units; u += step) {
-            const Unit un = unit_at<WIDTH>(p, pl, u, FB, pre);
+            const Unit un = unit_at(p, pl, u, FB, pre);
             const bool ok = mbar_wait(tfull0 + 8 * acc, acc_phase, lim, abort_flag);
             if (!__all_sync(0xffffffffu, ok)) {
                 if (lane == 0 && !*abort_flag) {
                     record_error(p.err, MOE_ERR_DEVICE_TIMEOUT, 54, blockIdx.x, u);
-                    if (PAIR) raise_abort_pair(abort_flag, (uint32_t)rank);
-                    else *abort_flag = 1;
+                    *abort_flag = 1;
                 }
                 break;
             }
             tc_fence_after();
             const uint32_t taddr = tmem + acc * 128 + ((uint32_t)(sub * 32) << 16);
-            const uint32_t te = PAIR ? mapa_shared(tempty0 + 8 * acc, 0) : tempty0 + 8 * acc;
+            const uint32_t te = tempty0 + 8 * acc;
             if (++acc == pl.accs) {
                 acc = 0;
                 acc_phase ^= 1;
             }
-            const int f = un.f0 + (PAIR ? rank * BF : 0) + sub * 32, cols = p.N - f;  // features of this warp inside the matrix
+            const int f = un.f0 + sub * 32, cols = p.N - f;  // features of this warp inside the matrix
             // this half's 32-row blocks: 0, 2, 4, 6 or 1, 3, 5, 7
             if (p.out_elem == kF32) {
 #pragma unroll 1
@@ -532,10 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    if (PAIR) mbar_arrive_cluster(te);
-                    else mbar_arrive(te);
-                }
+                if (lane == 0) mbar_arrive(te);
                 continue;
             }
             uint32_t pk[4][16];
@@ -555,10 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                    if (PAIR) mbar_arrive_cluster(te);
-                    else mbar_arrive(te);
-                }
+            if (lane == 0) mbar_arrive(te);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int c = half * 32 + i * 64;
@@ -574,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         cluster_sync();  // every CTA's loads, MMAs and scale copies are done
         const bool has = u0 < units;
-        const Unit un = has ? unit_at<WIDTH>(p, pl, u0, FB, pre) : Unit{};
+        const Unit un = has ? unit_at(p, pl, u0, FB, pre) : Unit{};
         const int quads = (un.rows + 3) >> 2, per = (quads + pl.split - 1) / pl.split;  // four-row slots, of each rank
         const uint32_t part = (uint32_t)(per * BF * 16);                                // bytes a rank sends another
         if (has && ew >= 0) {
@@ -624,10 +577,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (PAIR) cluster_sync();  // the leader's MMAs write the peer's tensor memory
     tc_fence_after();
-    if (PAIR && warp == 1) tmem_dealloc_pair(tmem, 512);
-    if (!PAIR && warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
 // Codes [rows, bytes], boxes of one 128-byte swizzled line by box_rows.
@@ -641,30 +592,10 @@ bool code_map(CUtensorMap* m, const void* base, int64_t rows, int64_t bytes, int
 struct Maps {
     CUtensorMap w, r64, r16;
 };
-template <int VEC, int MODE> cudaError_t launch(const MxGemm& g, const Maps& m, const Plan& pl, int grid, cudaStream_t s) {
-    cudaError_t e = ensure_smem_attr((const void*)gemm_mx_kernel<VEC, MODE>, kSmem);
+template <int VEC, bool SPLIT> cudaError_t launch(const MxGemm& g, const Maps& m, const Plan& pl, int grid, cudaStream_t s) {
+    cudaError_t e = ensure_smem_attr((const void*)gemm_mx_kernel<VEC, SPLIT>, kSmem);
     if (e != cudaSuccess) return e;
-    if (MODE == kPair) {
-        // as many pairs as can be resident at once: units are dealt out in advance
-        static const char key = 0;
-        int pairs = 0;
-        e = per_device_value(&key, [](int* v) {
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3(2 * 4096);
-            cfg.blockDim = dim3(kThreads);
-            cfg.dynamicSmemBytes = kSmem;
-            cudaLaunchAttribute at[1];
-            at[0].id = cudaLaunchAttributeClusterDimension;
-            at[0].val.clusterDim.x = 2;
-            at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-            cfg.attrs = at;
-            cfg.numAttrs = 1;
-            return cudaOccupancyMaxActiveClusters(v, gemm_mx_kernel<VEC, MODE>, &cfg);
-        }, &pairs);
-        if (e != cudaSuccess) return e;
-        grid = std::min(grid, 2 * std::max(1, pairs));
-    }
-    e = launch_kernel(gemm_mx_kernel<VEC, MODE>, dim3(grid), dim3(kThreads), kSmem, s, MODE == kSplit ? pl.split : MODE == kPair ? 2 : 1, m.w, m.r64, m.r16, g, pl);
+    e = launch_kernel(gemm_mx_kernel<VEC, SPLIT>, dim3(grid), dim3(kThreads), kSmem, s, SPLIT ? pl.split : 1, m.w, m.r64, m.r16, g, pl);
     count_launches(1);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -691,24 +622,10 @@ cudaError_t launch_gemm_mx(const MxGemm& g, int num_sms, cudaStream_t stream) {
     const int64_t units = (cdiv(g.rows, pl.tile_rows) + (g.offsets && g.G > 1 ? g.G : 0)) * cdiv(g.N, BF);  // at most
     const int KB = (int)cdiv(g.K / 2, kKB);
     while (pl.split < kMaxSplit && units * pl.split * 2 <= num_sms && KB >= 4 * pl.split) pl.split *= 2;
-    // CTA pairs (tiles of 256 features x 256 rows, each CTA with half of the
-    // rows in its ring: six stages for four) where their tiles fill the SMs
-    const int64_t pair_units = (cdiv(g.rows, 256) + (g.offsets && g.G > 1 ? g.G : 0)) * cdiv(g.N, 2 * BF);
-    const bool pair = pl.tile_rows == 256 && pair_units * 2 >= num_sms;
-    if (pair) {
-        pl.stage_bytes = kWBytes + 128 * kKB;
-        pl.stages = std::min(kMaxStages, kRing / pl.stage_bytes);
-        const int clusters = (int)std::min<int64_t>(pair_units, num_sms / 2);
-        const int blocks = g.K / kMxBlock;
-        const uintptr_t al = (uintptr_t)g.a_scale | (uintptr_t)g.b_scale;
-        if (blocks % 16 == 0 && al % 16 == 0) return launch<16, kPair>(g, m, pl, 2 * clusters, stream);
-        if (blocks % 4 == 0 && al % 4 == 0) return launch<4, kPair>(g, m, pl, 2 * clusters, stream);
-        return launch<1, kPair>(g, m, pl, 2 * clusters, stream);
-    }
     const int grid = pl.split > 1 ? (int)units * pl.split : (int)std::min<int64_t>(units, num_sms);
     const int blocks = g.K / kMxBlock;
     const uintptr_t al = (uintptr_t)g.a_scale | (uintptr_t)g.b_scale;
-#define MOE_MX(V) (pl.split > 1 ? launch<V, kSplit>(g, m, pl, grid, stream) : launch<V, kPlain>(g, m, pl, grid, stream))
+#define MOE_MX(V) (pl.split > 1 ? launch<V, true>(g, m, pl, grid, stream) : launch<V, false>(g, m, pl, grid, stream))
     if (blocks % 16 == 0 && al % 16 == 0) return MOE_MX(16);
     if (blocks % 4 == 0 && al % 4 == 0) return MOE_MX(4);
     return MOE_MX(1);

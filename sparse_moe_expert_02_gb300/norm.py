@@ -18,22 +18,31 @@ GATES = {"none": L.MOE_GATE_NONE, "channel": L.MOE_GATE_CHANNEL, "token": L.MOE_
 
 def _fields(kind: str, eps: float, w_offset: float, w, b, D: int):
     """A moe_norm's fields."""
-    if kind not in KINDS:
+    k = KINDS.get(kind)
+    if k is None:
         raise ValueError(f"kind: one of {sorted(KINDS)}, not {kind!r}")
-    dt = L.MOE_F32
-    for t in (w, b):
-        if t is not None:
-            if t.shape != (D,) or not t.is_cuda or not t.is_contiguous() or t.dtype not in L._DTYPE_OF:
-                raise ValueError("norm parameters: contiguous device tensors [D] of fp32 or bf16")
-            dt = L._DTYPE_OF[t.dtype]
-    if w is not None and b is not None and w.dtype != b.dtype:
-        raise ValueError("norm parameters: w and b of one type")
-    return KINDS[kind], eps, w_offset, dt, 0 if w is None else w.data_ptr(), 0 if b is None else b.data_ptr()
+    wp = bp = dt = 0
+    if w is not None:
+        wp, dt = _vector(w, D, "norm parameters")
+    if b is not None:
+        bp, bd = _vector(b, D, "norm parameters")
+        if w is not None and bd != dt:
+            raise ValueError("norm parameters: w and b of one type")
+        dt = bd
+    return k, eps, w_offset, dt, wp, bp
 
 
-def _same(t, like, what: str):
-    if t.shape != like.shape:
-        raise ValueError(f"{what}: shape {tuple(like.shape)}, not {tuple(t.shape)}")
+def _vector(t, n: int, what: str):
+    """(address, moe_dtype) of a contiguous device vector of n fp32 or bf16."""
+    dt = L._DTYPE_OF.get(t.dtype)
+    if dt is None or not t.is_cuda or t.dim() != 1 or t.size(0) != n or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous device tensor [{n}] of fp32 or bf16")
+    return t.data_ptr(), dt
+
+
+def _same(t, shape, what: str):
+    if t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
 def pre(x, w=None, b=None, *, kind: str = "rms", eps: float = 1e-6, w_offset: float = 0.0, out=None) -> torch.Tensor:
@@ -41,7 +50,7 @@ def pre(x, w=None, b=None, *, kind: str = "rms", eps: float = 1e-6, w_offset: fl
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     else:
-        _same(out, x, "out")
+        _same(out, x.shape, "out")
     L.moe_norm_pre(L.NORM_STRUCT.pack(*_fields(kind, eps, w_offset, w, b, x.shape[-1])), x, out)
     return out
 
@@ -56,26 +65,24 @@ def post(y, res, w=None, b=None, *, kind: str = "rms", eps: float = 1e-6, w_offs
     next_kind (None: kind, or "rms" after kind "none"; "none": no next norm),
     with the same eps and w_offset.  out may be res itself.
     """
-    T, D = y.shape
-    _same(res, y, "res")
+    shape = y.shape
+    T, D = shape
+    _same(res, shape, "res")
     if out is None:
         out = torch.empty(res.shape, dtype=res.dtype, device=res.device)
     else:
-        _same(out, y, "out")
+        _same(out, shape, "out")
     g = gd = gl = 0
     by = L.MOE_GATE_NONE
     if gate is not None and gate_by != "none":
         if gate_by not in GATES:
             raise ValueError(f"gate_by: one of {sorted(GATES)}, not {gate_by!r}")
         by = GATES[gate_by]
-        if gate.shape != {"channel": (D,), "token": (T,), "full": (T, D)}[gate_by]:
-            raise ValueError(f"gate: shape does not fit gate_by={gate_by!r}")
         if by == L.MOE_GATE_FULL:
+            _same(gate, shape, "gate")
             g, gd, gl = L._rows(gate, "gate")
         else:
-            if not gate.is_cuda or not gate.is_contiguous() or gate.dtype not in L._DTYPE_OF:
-                raise ValueError("gate: a contiguous device tensor of fp32 or bf16")
-            g, gd = gate.data_ptr(), L._DTYPE_OF[gate.dtype]
+            g, gd = _vector(gate, D if by == L.MOE_GATE_CHANNEL else T, "gate")
     if next_norm is None:
         next_norm = next_w is not None or next_out is not None
     next_kind = next_kind or (kind if kind != "none" else "rms")
@@ -86,7 +93,7 @@ def post(y, res, w=None, b=None, *, kind: str = "rms", eps: float = 1e-6, w_offs
     elif next_out is None:
         next_out = torch.empty(res.shape, dtype=y.dtype, device=res.device)
     else:
-        _same(next_out, y, "next_out")
+        _same(next_out, shape, "next_out")
     L.moe_norm_post(L.POST_STRUCT.pack(*_fields(kind, eps, w_offset, w, b, D), *nf, res_scale, branch_scale, by, gd,
                                        gate_sigmoid, g, gl), y, res, out, next_out)
     return out, next_out
