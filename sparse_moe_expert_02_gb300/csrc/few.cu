@@ -118,6 +118,15 @@ struct Misc {
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return tc::smem_u32(p); }
+// One lane of the converged producer warp, which runs its loops with all
+// lanes: what the copies take is then in uniform registers (issued from one
+// lane's own branch, a copy costs some 80 cycles more).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.b32 %0, 1, 0, q;\n}\n" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 __device__ __forceinline__ void group_sync(int grp) { asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(32 * NC) : "memory"); }
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 7, %0;" ::"n"(kCons) : "memory"); }
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -475,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     Misc& m = *(Misc*)smem;
     uint8_t* act = smem + up(sizeof(Misc), 128);  // x (P1, P2), then batches of h (P3)
     uint8_t* ring = smem + p.ring_at;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int cta = blockIdx.x, grid = gridDim.x;
     const int D = p.D, I = p.I, E = p.E, T = p.T, k = p.k;
     const int64_t lim = p.spin_ns;
@@ -501,6 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
 
     if (warp == NC * NG) {
         // ------------------------------------------------------- producer
+        const uint32_t ring0 = smem_u32(ring);
         int next[NG] = {0, p.stages};  // group g's ring: stages [g * p.stages, (g + 1) * p.stages)
         uint32_t phases[NG] = {0, 0};
         bool ok = true;
@@ -524,35 +534,40 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         // down), na and nb of them, columns c0 .. of K; whole boxes of eight, or row copies of `cols`.
         auto fill = [&](int grp, int wa, int64_t row0, int na, int wb, int64_t row1, int nb, int K, int c0, int cols) {
             if (!wait_stage(grp)) return;
-            const uint32_t bar = smem_u32(m.full + next[grp]), base = smem_u32(ring + next[grp] * P::stage);
-            const int bytes = bytes_of<W>(cols), sbytes = cols / 32;
-            const bool boxa = na == 8, boxb = nb == 8;
-            const uint32_t sc = base + P::data;
-            const bool scaled = W == MOE_MXFP4 && p.tma_scales;
-            // where the second region's rows and scales start
-            const uint32_t base1 = base + (boxa ? 8 * kBoxRow : na * (bytes + 16)), sc1 = sc + (boxa ? 8 * P::kc / 32 : na * sbytes);
-            if (lane == 0) {
+            if (elect_one()) {
+                const uint32_t bar = smem_u32(m.full + next[grp]), base = ring0 + next[grp] * P::stage;
+                const int bytes = bytes_of<W>(cols), sbytes = cols / 32;
+                const bool boxa = na == 8, boxb = nb == 8;
+                const uint32_t sc = base + P::data;
+                const bool scaled = W == MOE_MXFP4 && p.tma_scales;
+                // where the second region's rows and scales start
+                const uint32_t base1 = base + (boxa ? 8 * kBoxRow : na * (bytes + 16)), sc1 = sc + (boxa ? 8 * P::kc / 32 : na * sbytes);
                 uint32_t total = (boxa ? 8 * kBoxRow : na * bytes) + (boxb ? 8 * kBoxRow : nb * bytes);
                 if (scaled) total += (boxa ? 8 * P::kc / 32 : na * sbytes) + (boxb ? 8 * P::kc / 32 : nb * sbytes);
                 tc::mbar_expect_tx(bar, total);
                 const int line = bytes_of<W>(c0) / Tr<W>::in;
-                if (boxa) box_load(base, &maps.w[wa], bar, (int)row0, line);
-                if (boxb) box_load(base1, &maps.w[wb], bar, (int)row1, line);
-                if (scaled && boxa) tc::tma_load_2d(sc, &maps.s[wa], bar, c0 / 32, (int)row0);
-                if (scaled && boxb) tc::tma_load_2d(sc1, &maps.s[wb], bar, c0 / 32, (int)row1);
-            }
-            __syncwarp();
-            const bool first = lane < 8;
-            const int r = lane & 7, w = first ? wa : wb;
-            if (lane < 16 && (first ? !boxa && r < na : !boxb && r < nb)) {
-                const int64_t row = (first ? row0 : row1) + r;
-                const uint8_t* src = (const uint8_t*)(w == 0 ? p.w_gate : w == 1 ? p.w_up : p.w_down);
-                bulk_load((first ? base : base1) + r * (bytes + 16), src + row * bytes_of<W>(K) + bytes_of<W>(c0), bytes, bar);
-                if (scaled) {
-                    const uint8_t* ss = (const uint8_t*)(w == 0 ? p.s_gate : w == 1 ? p.s_up : p.s_down);
-                    bulk_load((first ? sc : sc1) + r * sbytes, ss + row * (K / 32) + c0 / 32, sbytes, bar);
+                auto rows = [&](int w, int64_t row, int n, uint32_t dst, uint32_t sdst) {
+                    const uint8_t* src = (const uint8_t*)(w == 0 ? p.w_gate : w == 1 ? p.w_up : p.w_down) + row * bytes_of<W>(K) + bytes_of<W>(c0);
+                    const uint8_t* ss = (const uint8_t*)(w == 0 ? p.s_gate : w == 1 ? p.s_up : p.s_down) + row * (K / 32) + c0 / 32;
+                    for (int r = 0; r < n; ++r) {
+                        bulk_load(dst + r * (bytes + 16), src + (int64_t)r * bytes_of<W>(K), bytes, bar);
+                        if (scaled) bulk_load(sdst + r * sbytes, ss + (int64_t)r * (K / 32), sbytes, bar);
+                    }
+                };
+                if (boxa) {
+                    box_load(base, &maps.w[wa], bar, (int)row0, line);
+                    if (scaled) tc::tma_load_2d(sc, &maps.s[wa], bar, c0 / 32, (int)row0);
+                } else {
+                    rows(wa, row0, na, base, sc);
+                }
+                if (boxb) {
+                    box_load(base1, &maps.w[wb], bar, (int)row1, line);
+                    if (scaled) tc::tma_load_2d(sc1, &maps.s[wb], bar, c0 / 32, (int)row1);
+                } else {
+                    rows(wb, row1, nb, base1, sc1);
                 }
             }
+            __syncwarp();
             advance(grp);
         };
         // P0: router rows (fp32 or bf16), row copies
@@ -565,12 +580,14 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                 const int step = router_cols<W>(n, D);
                 for (int c0 = 0; c0 < D; c0 += step) {
                     if (!wait_stage(grp)) break;
-                    const uint32_t bar = smem_u32(m.full + next[grp]), base = smem_u32(ring + next[grp] * P::stage);
-                    const int bytes = min(step, D - c0) * P::eb;
-                    if (lane == 0) tc::mbar_expect_tx(bar, (uint32_t)(n * bytes));
+                    if (elect_one()) {
+                        const uint32_t bar = smem_u32(m.full + next[grp]), base = ring0 + next[grp] * P::stage;
+                        const int bytes = min(step, D - c0) * P::eb;
+                        tc::mbar_expect_tx(bar, (uint32_t)(n * bytes));
+                        const uint8_t* src = (const uint8_t*)p.w_router + ((int64_t)t.at(grp) * D + c0) * P::eb;
+                        for (int r = 0; r < n; ++r) bulk_load(base + r * (bytes + 16), src + (int64_t)r * D * P::eb, bytes, bar);
+                    }
                     __syncwarp();
-                    if (lane < n)
-                        bulk_load(base + lane * (bytes + 16), (const uint8_t*)p.w_router + ((int64_t)(t.at(grp) + lane) * D + c0) * P::eb, bytes, bar);
                     advance(grp);
                 }
             }
@@ -594,13 +611,13 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         // P2: the routed experts, once the list is there
         if (ok && !tc::mbar_wait(smem_u32(&m.list_ready), 0, lim, abort)) ok = false;
         ok = __all_sync(0xffffffffu, ok);
-        const int n = ok ? m.n : 0;
+        const int n = uniform(ok ? m.n : 0);
         const int64_t lo = (int64_t)n * I * cta / grid, hi = (int64_t)n * I * (cta + 1) / grid;
         for (int64_t f = lo; f < hi;) {
             const int pos = (int)(f / I);
             const int64_t first = (int64_t)pos * I;  // the expert's feature 0
             const Pair t((int)(f - first), (int)min((int64_t)I, hi - first), 8);
-            gateup(m.expert[pos], t);
+            gateup(uniform(m.expert[pos]), t);
             f = first + t.end();
         }
         // P3: down rows, pass by pass, batch by batch
@@ -611,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                 for (int c0 = 0; c0 < I; c0 += P::kc) {
                     const int cols = min(P::kc, I - c0);
                     for (int x = bt.x0; x < bt.x1; ++x) {
-                        const int64_t row = (int64_t)(x < 0 ? E : m.expert[x]) * D;
+                        const int64_t row = (int64_t)uniform(x < 0 ? E : m.expert[x]) * D;
 #pragma unroll
                         for (int grp = 0; grp < NG; ++grp) {
                             const int nr = t.n(grp), r0 = t.at(grp);
