@@ -204,17 +204,18 @@ typedef struct moe_ws_layout {
     size_t inv;        /* int32 [T*top_k]: row of pair (t, j) in the grouped layout */
     size_t src_tok;    /* int32 [T*top_k + T]: token of each grouped row */
     size_t hist;       /* int32 [chunks, E]: per-chunk expert histograms (scratch) */
-    size_t xq;         /* FP8: E4M3 [T, D] quantised x */
-    size_t xq_scale;   /* FP8: f32 [T, D/128] */
-    size_t xp;         /* [T*top_k, D] x gathered into grouped order (layer dtype; E4M3 for FP8) */
-    size_t xp_scale;   /* FP8: f32 [T*top_k, D/128] */
+    size_t xq;         /* FP8: E4M3 [T, D] quantised x; MXFP4: codes [T, D/2], right after xp's (not 256-byte aligned) */
+    size_t xq_scale;   /* FP8: f32 [T, D/128]; MXFP4: bytes [T, D/32], right after xp_scale's */
+    size_t xp;         /* [T*top_k, D] x gathered into grouped order (layer dtype; E4M3 for FP8;
+                          MXFP4: codes [T*top_k, D/2]) */
+    size_t xp_scale;   /* FP8: f32 [T*top_k, D/128]; MXFP4: bytes [T*top_k, D/32] */
     size_t h;          /* SwiGLU activations: f32 [R, I] (MOE_F32) | fp16 [R, I] (MOE_BF16) |
                           bf16 hi/lo pair [R, 2I] (MOE_BF16 + MOE_FLAG_DOWN_HILO: hi in
-                          columns 0..I-1, lo = bf16(h - hi) in I..2I-1) | E4M3 [R, I];
-                          R = T*top_k + T */
-    size_t h_scale;    /* FP8: f32 [T*top_k + T, I/128] */
+                          columns 0..I-1, lo = bf16(h - hi) in I..2I-1) | E4M3 [R, I] |
+                          MXFP4 codes [R, I/2]; R = T*top_k + T */
+    size_t h_scale;    /* FP8: f32 [T*top_k + T, I/128]; MXFP4: bytes [T*top_k + T, I/32] */
     size_t y;          /* [R, D] expert outputs: f32 (MOE_F32; MOE_BF16 + MOE_FLAG_DOWN_HILO),
-                          fp16 (MOE_BF16) or bf16 (FP8 layer) */
+                          fp16 (MOE_BF16) or bf16 (FP8 and MXFP4 layers) */
     size_t logits_part;/* f32 [S, T, E] router K-slice partials when T is small (S > 1), else 0 */
     size_t tiles2;     /* int32 [E+2]: exclusive prefix of ceil(counts/256) (row-tile pairs) */
     size_t pairs;      /* int32 [2, E+2], [2], [E+2]: the exclusive prefix of floor(counts/256)
@@ -225,6 +226,7 @@ typedef struct moe_ws_layout {
                           launch's order (a permutation of 0..E, the shared group E last).
                           Written by the permutation, and only where the split can run: bf16
                           layer, T*top_k >= 64*E (see MOE_FLAG_SPLIT_GEMM_OFF) */
+    size_t gu;         /* MXFP4: f32 [2, R, I] gate and up products */
     size_t few;        /* moe_forward_few, T <= MOE_FEW_MAX: f32 [T*(top_k+1), I] activations h */
 } moe_ws_layout;
 

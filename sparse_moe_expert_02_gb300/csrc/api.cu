@@ -100,9 +100,9 @@ bool split_sizes(const moe_config& c, int T) {
     if (c.flags & (MOE_FLAG_SPLIT_GEMM_OFF | MOE_FLAG_PAIR_CTA_ON | MOE_FLAG_FORCE_SIMT)) return false;
     return f16_down(c) && (int64_t)T * c.top_k >= 64LL * c.E;
 }
-// Expert outputs y: bf16 (FP8 layer), fp16 (bf16 layer, fp16 down path), else fp32.
+// Expert outputs y: bf16 (FP8 and MXFP4 layers), fp16 (bf16 layer, fp16 down path), else fp32.
 int y_elem(const moe_config& c) {
-    return c.dtype == MOE_FP8_E4M3_B128 ? moe::kBF16 : f16_down(c) ? moe::kF16 : moe::kF32;
+    return c.dtype == MOE_FP8_E4M3_B128 || c.dtype == MOE_MXFP4 ? moe::kBF16 : f16_down(c) ? moe::kF16 : moe::kF32;
 }
 
 // The first 256 bytes of the workspace: the error word (16 bytes), then from
@@ -138,15 +138,21 @@ void layout(const moe_config& c, int num_sms, int T, moe_ws_layout* L) {
     L->inv = take((size_t)TK * 4);
     L->src_tok = take((size_t)R * 4);
     L->hist = take((size_t)nch * c.E * 4);
+    const bool mx = c.dtype == MOE_MXFP4;
     L->xq = fp8 ? take((size_t)T * c.D) : 0;
     L->xq_scale = fp8 ? take((size_t)T * (c.D / 128) * 4) : 0;
-    L->xp = take((size_t)TK * c.D * ab);
-    L->xp_scale = fp8 ? take((size_t)TK * (c.D / 128) * 4) : 0;
+    // MXFP4: xq's rows follow xp's, so that the GEMMs see one run of R rows
+    L->xp = take(mx ? (size_t)R * c.D / 2 : (size_t)TK * c.D * ab);
+    L->xp_scale = fp8 ? take((size_t)TK * (c.D / 128) * 4) : mx ? take((size_t)R * c.D / 32) : 0;
+    if (mx) {
+        L->xq = L->xp + (size_t)TK * c.D / 2;
+        L->xq_scale = L->xp_scale + (size_t)TK * c.D / 32;
+    }
     // bf16 layer: h in fp16 ([R, I]), or as a bf16 hi/lo pair ([R, 2I]) under
     // MOE_FLAG_DOWN_HILO; a single bf16 rounding of h alone would cost about
     // 1e-2 of the output rms.
-    L->h = take((size_t)R * c.I * (hilo(c) ? 4 : ab));
-    L->h_scale = fp8 ? take((size_t)R * (c.I / 128) * 4) : 0;
+    L->h = take(mx ? (size_t)R * c.I / 2 : (size_t)R * c.I * (hilo(c) ? 4 : ab));
+    L->h_scale = fp8 ? take((size_t)R * (c.I / 128) * 4) : mx ? take((size_t)R * c.I / 32) : 0;
     // y: fp16 for the bf16 layer, bf16 for the FP8 layer, else fp32 (a bf16 y
     // in the bf16 layer would cost about 1.3e-2 of the output rms).
     L->y = take((size_t)R * c.D * (y_elem(c) == moe::kF32 ? 4 : 2));
@@ -154,6 +160,7 @@ void layout(const moe_config& c, int num_sms, int T, moe_ws_layout* L) {
     L->logits_part = S > 1 ? take((size_t)S * T * c.E * 4) : 0;
     L->tiles2 = take((size_t)(c.E + 2) * 4);
     L->pairs = take((size_t)(3 * (c.E + 2) + 2) * 4);
+    L->gu = mx ? take((size_t)2 * R * c.I * 4) : 0;
     L->few = T <= moe::kFewMax ? take((size_t)R * c.I * 4) : 0;
     L->total = o;
 }
@@ -493,7 +500,12 @@ moe_status permute_impl(const moe_plan* p, const void* x, int32_t T, Ws& W, cuda
                                        W.at<uint32_t>(W.L.err), s, hist_ready,
                                        split_sizes(c, T) ? W.at<int32_t>(W.L.pairs) : nullptr,
                                        std::max(1, p->num_sms / 2), prefer_narrow(p, T, true)));
-    if (c.dtype == MOE_FP8_E4M3_B128) {
+    if (c.dtype == MOE_MXFP4) {
+        uint8_t *xq = W.at<uint8_t>(W.L.xq), *sq = W.at<uint8_t>(W.L.xq_scale);
+        MOE_CUDA(moe::launch_mx_quantize(x, moe::kBF16, c.D, T, c.D, xq, sq, s));
+        MOE_CUDA(moe::launch_gather_rows(xq, 1, c.D / 2, W.at<int32_t>(W.L.src_tok), TK, W.at<uint8_t>(W.L.xp), s));
+        MOE_CUDA(moe::launch_gather_rows(sq, 1, c.D / 32, W.at<int32_t>(W.L.src_tok), TK, W.at<uint8_t>(W.L.xp_scale), s));
+    } else if (c.dtype == MOE_FP8_E4M3_B128) {
         // xq (x quantised) is the shared expert's A operand; the routed rows
         // are quantised from x on the way into xp at scatter sizes
         if (quant_x)
@@ -613,6 +625,49 @@ moe::GroupedGemm down_gemm(const moe_plan* p, const moe_weights* w, int32_t T, W
     return g;
 }
 
+// MXFP4: an expert GEMM over all E+1 groups (the shared expert's rows follow
+// the routed ones), gate, up (fp32) or down.
+moe::MxGemm mx_gemm(const moe_plan* p, int32_t T, Ws& W, const uint8_t* a, const uint8_t* as, const void* b, const void* bs,
+                    int N, int K, void* out, int out_elem) {
+    const moe_config& c = p->cfg;
+    moe::MxGemm g = {};
+    g.a = a;
+    g.a_scale = as;
+    g.b = (const uint8_t*)b;
+    g.b_scale = (const uint8_t*)bs;
+    g.offsets = W.at<int32_t>(W.L.offsets);
+    g.rows = T * (c.top_k + 1);
+    g.G = c.E + 1;
+    g.N = N;
+    g.K = K;
+    g.out = out;
+    g.out_elem = out_elem;
+    g.ldo = N;
+    g.err = W.at<uint32_t>(W.L.err);
+    g.spin_ns = p->spin_ns;
+    return g;
+}
+
+// h = silu(gate) * up quantised: two GEMMs, then one pass over their outputs
+// (h's scales need 32 finished columns of both).
+moe_status mx_gateup(const moe_plan* p, const moe_weights* w, int32_t T, Ws& W, cudaStream_t s) {
+    const moe_config& c = p->cfg;
+    const int64_t R = (int64_t)T * (c.top_k + 1);
+    float* gu = W.at<float>(W.L.gu);
+    const uint8_t *a = W.at<uint8_t>(W.L.xp), *as = W.at<uint8_t>(W.L.xp_scale);
+    MOE_CUDA(moe::launch_gemm_mx(mx_gemm(p, T, W, a, as, w->w_gate, w->s_gate, c.I, c.D, gu, moe::kF32), p->num_sms, s));
+    MOE_CUDA(moe::launch_gemm_mx(mx_gemm(p, T, W, a, as, w->w_up, w->s_up, c.I, c.D, gu + R * c.I, moe::kF32), p->num_sms, s));
+    MOE_CUDA(moe::launch_mx_swiglu(gu, gu + R * c.I, R * c.I, W.at<uint8_t>(W.L.h), W.at<uint8_t>(W.L.h_scale), s));
+    return MOE_OK;
+}
+moe_status mx_down(const moe_plan* p, const moe_weights* w, int32_t T, Ws& W, cudaStream_t s) {
+    const moe_config& c = p->cfg;
+    MOE_CUDA(moe::launch_gemm_mx(mx_gemm(p, T, W, W.at<uint8_t>(W.L.h), W.at<uint8_t>(W.L.h_scale), w->w_down, w->s_down, c.D, c.I,
+                                         W.at<void>(W.L.y), moe::kBF16),
+                                 p->num_sms, s));
+    return MOE_OK;
+}
+
 int elem_bytes(int e) { return e == moe::kF32 ? 4 : e == moe::kE4M3 ? 1 : 2; }
 
 // The shared expert alone, as a dense GEMM over its T rows (which sit after
@@ -710,6 +765,7 @@ moe_status moe_gemm_gateup(const moe_plan* p, const moe_weights* w, const void* 
     if (st != MOE_OK) return st;
     if ((st = check_weights(p, w, false, true)) != MOE_OK) return st;
     if (!ptr_ok(x)) return arg_fail(MOE_ERR_INVALID_ARG, "x NULL or misaligned");
+    if (p->cfg.dtype == MOE_MXFP4) return mx_gateup(p, w, T, W, (cudaStream_t)stream);
     return run_stage_gemm(p, gateup_gemm(p, w, x, T, W), 0, T, W, (cudaStream_t)stream, "gate/up GEMM");
 }
 
@@ -719,6 +775,7 @@ moe_status moe_gemm_down(const moe_plan* p, const moe_weights* w, int32_t T, voi
     moe_status st = check_call(p, T, ws, ws_bytes, &W);
     if (st != MOE_OK) return st;
     if ((st = check_weights(p, w, false, true)) != MOE_OK) return st;
+    if (p->cfg.dtype == MOE_MXFP4) return mx_down(p, w, T, W, (cudaStream_t)stream);
     return run_stage_gemm(p, down_gemm(p, w, T, W), 1, T, W, (cudaStream_t)stream, "down GEMM");
 }
 
@@ -755,7 +812,6 @@ moe_status moe_forward(const moe_plan* p, const moe_weights* w, const void* x, i
     Ws W;
     moe_status st = check_call(p, T, ws, ws_bytes, &W);
     if (st != MOE_OK) return st;
-    if (p->cfg.dtype == MOE_MXFP4) return arg_fail(MOE_ERR_UNSUPPORTED, "MOE_MXFP4 runs through moe_forward_few");
     if ((st = check_weights(p, w, true, true)) != MOE_OK) return st;
     if (!ptr_ok(x) || !ptr_ok(out)) return arg_fail(MOE_ERR_INVALID_ARG, "x or out NULL or misaligned");
     if ((blob_out && !aligned(blob_out, 16)) || (logits_out && !aligned(logits_out, 16)))
@@ -765,6 +821,14 @@ moe_status moe_forward(const moe_plan* p, const moe_weights* w, const void* x, i
     MOE_CUDA(cudaMemsetAsync(ws, 0, kErrBlock, s));
     const bool fh = fuse_topk_hist(p, T);
     if (fh) MOE_CUDA(zero_topk_hist(p, T, W, s));
+    if (cf.dtype == MOE_MXFP4) {
+        if ((st = route_impl(p, w, x, T, W, stream, fh)) != MOE_OK) return st;
+        if ((st = permute_impl(p, x, T, W, s, true, fh)) != MOE_OK) return st;
+        if ((st = mx_gateup(p, w, T, W, s)) != MOE_OK) return st;
+        if ((st = mx_down(p, w, T, W, s)) != MOE_OK) return st;
+        if ((st = moe_unpermute(p, T, out, ws, ws_bytes, stream)) != MOE_OK) return st;
+        return copy_routing_out(p, W, T, blob_out, logits_out, s);
+    }
     moe::GroupedGemm gu = gateup_gemm(p, w, x, T, W), dn = down_gemm(p, w, T, W);
     const bool fp8 = cf.dtype == MOE_FP8_E4M3_B128;
     moe::GroupedGemm sgu = shared_only(gu, cf, T, true, fp8 ? (const void*)W.at<uint8_t>(W.L.xq) : x,

@@ -233,6 +233,9 @@ cudaError_t launch_mx_quantize(const void* x, int x_elem, int64_t ld, int64_t ro
 cudaError_t launch_mx_dequantize(const uint8_t* q, const uint8_t* s, int64_t rows, int cols, void* out, int out_elem,
                                  int64_t ld, cudaStream_t stream);
 
+// h = silu(g) * u of n fp32 values (n a multiple of 32), quantised as one row.
+cudaError_t launch_mx_swiglu(const float* g, const float* u, int64_t n, uint8_t* q, uint8_t* s, cudaStream_t stream);
+
 // out[r][n] = sum_k a[r][k] * b_g[n][k] over microscaled 4-bit operands.
 struct MxGemm {
     const uint8_t* a;        // [rows, K/2]

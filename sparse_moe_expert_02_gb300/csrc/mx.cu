@@ -93,6 +93,29 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const T* __restrict__ 
     }
 }
 
+// h = silu(g) * u, quantised: units of eight columns of one long row.
+__global__ void __launch_bounds__(256) mx_swiglu_kernel(const float* __restrict__ g, const float* __restrict__ u, int64_t n,
+                                                        uint8_t* __restrict__ q, uint8_t* __restrict__ s) {
+    const int64_t step = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t w0 = (int64_t)blockIdx.x * blockDim.x + (threadIdx.x & ~31); w0 < n; w0 += step) {
+        const int64_t i = min(w0 + (threadIdx.x & 31), n - 4 + (threadIdx.x & 3));
+        Eight<float> a, b;
+        a.load(g + i * 8);
+        b.load(u + i * 8);
+        a.a = make_float4(swiglu(a.a.x, b.a.x), swiglu(a.a.y, b.a.y), swiglu(a.a.z, b.a.z), swiglu(a.a.w, b.a.w));
+        a.b = make_float4(swiglu(a.b.x, b.b.x), swiglu(a.b.y, b.b.y), swiglu(a.b.z, b.b.z), swiglu(a.b.w, b.b.w));
+        uint32_t m = a.amax();
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const uint32_t sb = mx_scale_byte(m);
+        const uint32_t c = a.codes(mx_inv_scale(sb));
+        if (w0 + (threadIdx.x & 31) < n) {
+            *(uint32_t*)(q + i * 4) = sb == 255u ? 0u : c;
+            if ((i & 3) == 0) s[i >> 2] = (uint8_t)sb;
+        }
+    }
+}
+
 // n blocks, a warp each.
 template <typename T>
 __global__ void __launch_bounds__(256) mx_quantize_any_kernel(const T* __restrict__ x, int64_t ld, int64_t n, int cols, int blocks,
@@ -223,6 +246,12 @@ cudaError_t launch_mx_quantize(const void* x, int x_elem, int64_t ld, int64_t ro
         if (h.vec) mx_quantize_kernel<bf16><<<h.grid, 256, 0, stream>>>((const bf16*)x, ld, h.units, h.per, q, s);
         else mx_quantize_any_kernel<bf16><<<h.grid, 256, 0, stream>>>((const bf16*)x, ld, n, cols, h.blocks, q, s);
     }
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_mx_swiglu(const float* g, const float* u, int64_t n, uint8_t* q, uint8_t* s, cudaStream_t stream) {
+    mx_swiglu_kernel<<<grid_for(n / 8), 256, 0, stream>>>(g, u, n / 8, q, s);
     count_launches(1);
     return cudaGetLastError();
 }

@@ -139,10 +139,11 @@ class MoELayer:
     def views(self, T: int) -> dict:
         k, E, D, I = self.top_k, self.E, self.D, self.I
         TK, R = T * k, T * k + T
-        act = {"f32": torch.float32, "bf16": torch.bfloat16, "fp8": torch.uint8}[self.dtype]
+        act = {"f32": torch.float32, "bf16": torch.bfloat16, "fp8": torch.uint8, "mxfp4": torch.uint8}[self.dtype]
         f16_down = self.dtype == "bf16" and not self.hilo
-        ydt = torch.bfloat16 if self.dtype == "fp8" else torch.float16 if f16_down else torch.float32
-        hcols = 2 * I if self.hilo else I
+        mx4 = self.dtype == "mxfp4"
+        ydt = torch.bfloat16 if self.dtype in ("fp8", "mxfp4") else torch.float16 if f16_down else torch.float32
+        hcols = 2 * I if self.hilo else I // 2 if mx4 else I
         hdt = torch.float16 if f16_down else act
         v = {
             "err": self.ws_view(T, "err", torch.int32, (4,)),
@@ -153,7 +154,7 @@ class MoELayer:
             "tiles": self.ws_view(T, "tiles", torch.int32, (E + 2,)),
             "inv": self.ws_view(T, "inv", torch.int32, (TK,)),
             "src_tok": self.ws_view(T, "src_tok", torch.int32, (R,)),
-            "xp": self.ws_view(T, "xp", act, (TK, D)),
+            "xp": self.ws_view(T, "xp", act, (TK, D // 2 if mx4 else D)),
             "h": self.ws_view(T, "h", hdt, (R, hcols)),
             "y": self.ws_view(T, "y", ydt, (R, D)),
         }
@@ -162,4 +163,7 @@ class MoELayer:
             v["xq_scale"] = self.ws_view(T, "xq_scale", torch.float32, (T, D // 128))
             v["xp_scale"] = self.ws_view(T, "xp_scale", torch.float32, (TK, D // 128))
             v["h_scale"] = self.ws_view(T, "h_scale", torch.float32, (R, I // 128))
+        if mx4:
+            for n, rows, cols in (("xq", T, D // 2), ("xq_scale", T, D // 32), ("xp_scale", TK, D // 32), ("h_scale", R, I // 32)):
+                v[n] = self.ws_view(T, n, torch.uint8, (rows, cols))
         return v

@@ -400,6 +400,38 @@ def test_few_ties_nonfinite_logits_and_refusals():
     assert e.value.status == L.MOE_ERR_UNSUPPORTED
 
 
+# ------------------------------------------- the 4-bit layer at every size
+
+@pytest.mark.parametrize("T,D,E,I,k,zipf", [(1, 256, 16, 128, 2, None), (40, 512, 32, 256, 4, 1.2), (300, 384, 20, 128, 3, 1.0),
+                                            (1100, 256, 24, 128, 2, None)])
+def test_mxfp4_layer_forward(T, D, E, I, k, zipf):
+    shape, inp, layer = few_case("mxfp4", T, D, E, I, k, zipf)
+    out = layer.forward(inp["x"])
+    layer.check()
+    # y is rounded to bf16 before the sum: 2^-9 of each of the k + 1 terms, inside the type's bound
+    few_check("mxfp4", shape, inp, layer, out)
+    v = layer.views(T)
+    src = v["src_tok"].long()
+    q = mx.quantize(inp["x"])
+    assert torch.equal(v["xq"], q.codes) and torch.equal(v["xq_scale"], q.scales)
+    assert torch.equal(v["xp"], q.codes[src[:T * k]]) and torch.equal(v["xp_scale"], q.scales[src[:T * k]])
+    assert torch.equal(layer.forward(inp["x"]), out)
+    if T <= L.MOE_FEW_MAX:
+        assert rel_max_err(f64(layer.forward_few(inp["x"])), f64(out)) <= 2 * TOL["mxfp4"]
+
+
+def test_mxfp4_stages_agree_with_forward():
+    shape, inp, layer = few_case("mxfp4", 70, 256, 16, 128, 2, 1.0)
+    x = inp["x"]
+    out = layer.forward(x)
+    layer.init_ws()
+    layer.route(x)
+    layer.permute(x)
+    layer.gemm_gateup(x)
+    layer.gemm_down(70)
+    assert torch.equal(layer.unpermute(70), out)
+
+
 # --------------------------------------------------------------- MoEBlock
 
 @pytest.mark.parametrize("dtype", ["bf16", "mxfp4"])
@@ -419,3 +451,12 @@ def test_block_runs_the_operators_together(dtype):
     check_norm(n2, f64(r2), "rms", 1e-6, f64(next_w), None, 1.0)
     again, none = block.forward(r, n=n, next_norm=False)
     assert none is None and torch.equal(again, r2)
+
+
+def test_block_prefill_runs_moe_forward():
+    shape, inp, layer = few_case("mxfp4", 50, 256, 16, 128, 2, None, out_dtype="bf16")
+    block = MoEBlock(layer, post_kind="none", next_kind="none")
+    r = rand(50, 256, seed=1, dtype=BF16)
+    r2, none = block.forward(r)
+    n = norm.pre(r)
+    assert none is None and torch.equal(r2, norm.post(layer.forward(n), r, kind="none")[0])
