@@ -66,7 +66,6 @@ constexpr int NW = 12;                       // consumer warps
 constexpr int NP = 4;                        // producer warps, every fourth tile each
 constexpr int kCons = 32 * NW;               // consumer threads
 constexpr int kThreads = kCons + 32 * NP;
-constexpr int kBoxRow = 512;                 // bytes of a box's rows: 4 KB boxes, two a stage
 constexpr int kMaxPairs = kFewMax * 32;      // (token, slot) pairs
 constexpr int kMaxStages = 20;
 constexpr int kHCols = 1024;                 // columns of h in shared memory at a time
@@ -89,9 +88,15 @@ __host__ __device__ constexpr int imax(int a, int b) { return a > b ? a : b; }
 // Bytes of n columns (n a multiple of 64).
 template <int W> __host__ __device__ constexpr int bytes_of(int n) { return n / 64 * Tr<W>::b64; }
 
-template <int W> struct Plan {
-    static constexpr int kc = kBoxRow / Tr<W>::b64 * 64;         // columns of a box
-    static constexpr int data = 16 * (kBoxRow + 16);             // row copies: 16 bytes between rows
+// Bytes of a box's rows, two boxes of eight rows a stage.  16-bit weights like
+// longer rows (one token 56.9 us against 59.3, five with D = 7168 239 against
+// 264) while the ring keeps eight stages or so (16 tokens: 498 against 443);
+// the other types need the stages (4 bits 39.8 against 37.2, FP8 123 against
+// 115).
+template <int W, int NT> struct Plan {
+    static constexpr int box = NT == 1 && (W == MOE_BF16 || W == W_HILO) ? 1024 : 512;
+    static constexpr int kc = box / Tr<W>::b64 * 64;         // columns of a box
+    static constexpr int data = 16 * (box + 16);             // row copies: 16 bytes between rows
     static constexpr int scales = W == MOE_MXFP4 ? 16 * kc / kMxBlock : 0;  // scale bytes of a stage
     static constexpr int stage = up(data + scales, 1024);        // boxes are swizzled by address
     static constexpr int rslice = W == MOE_F32 ? 32 : 64;        // columns of router rows taken at a time
@@ -432,6 +437,25 @@ __device__ __forceinline__ void topk_token(const FewParams& p, int t, Misc& m, u
     if (lane < p.k) m.selw[t * p.k + lane] = ex / sum;
 }
 
+// `total` units over the consumers, UNITS of a thread's at a time: all of
+// their loads (of WORDS 16-byte words), then what is done with each.  Whole
+// warps stay together; `on`: the unit is the lane's own.
+template <int WORDS, int UNITS, class Load, class Store>
+__device__ __forceinline__ void each_unit(int total, Load load, Store store) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int u0 = threadIdx.x & ~31; u0 < total; u0 += UNITS * kCons) {
+        uint4 v[UNITS][WORDS];
+#pragma unroll
+        for (int j = 0; j < UNITS; ++j) load(min(u0 + j * kCons + lane, total - 1), v[j]);
+#pragma unroll
+        for (int j = 0; j < UNITS; ++j) {
+            const int u = u0 + j * kCons + lane;
+            if (u0 + j * kCons < total) store(min(u, total - 1), u < total, v[j]);
+        }
+    }
+}
+
 // Grid barrier on a counter that only grows (every launch adds whole
 // multiples of the grid): arrive returns the count to wait for.
 __device__ __forceinline__ unsigned long long grid_arrive(unsigned long long* bar) {
@@ -526,8 +550,8 @@ struct Maps {
 };
 
 // Columns of a stage of n router rows: a twelfth of them, if it holds that.
-template <int W> __device__ __forceinline__ int router_cols(int n, int D) {
-    return min(up((D + NW - 1) / NW, 64), (16 * kBoxRow / n & -256) / Plan<W>::eb);
+template <int W, int NT> __device__ __forceinline__ int router_cols(int n, int D) {
+    return min(up((D + NW - 1) / NW, 64), (16 * Plan<W, NT>::box / n & -256) / Plan<W, NT>::eb);
 }
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
@@ -580,7 +604,7 @@ struct Yes { static constexpr bool value = true; };
 // ONE: a single token, against 4-bit weights.
 template <int W, int NT, bool ONE>
 __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant__ FewParams p, const __grid_constant__ Maps maps) {
-    using P = Plan<W>;
+    using P = Plan<W, NT>;
     constexpr bool kScaled = W == MOE_FP8_E4M3_B128 || W == MOE_MXFP4;
     constexpr int kSlice = Tr<W>::slice, kIn = Tr<W>::in;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -651,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             if (stage_free(t, i, st) && elect_one()) {
                 const uint32_t bar = smem_u32(m.full + st), bytes = bytes_of<W>(cols), sbytes = cols / 32;
                 const bool scaled = W == MOE_MXFP4 && p.tma_scales;
-                const uint32_t per = bytes + (scaled ? sbytes : 0), box = 8 * kBoxRow + (scaled ? 8 * P::kc / 32 : 0);
+                const uint32_t per = bytes + (scaled ? sbytes : 0), box = 8 * P::box + (scaled ? 8 * P::kc / 32 : 0);
                 tc::mbar_expect_tx(bar, (na == 8 ? box : na * per) + (nb == 8 ? box : nb * per));
                 uint32_t dst = ring0 + st * P::stage, sdst = dst + P::data;
                 const int line = bytes_of<W>(c0) / kIn;
@@ -662,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                     if (n == 8) {
                         box_load(dst, &maps.w[w], bar, (int)row, line);
                         if (scaled) tc::tma_load_2d(sdst, &maps.s[w], bar, c0 / 32, (int)row);
-                        dst += 8 * kBoxRow;
+                        dst += 8 * P::box;
                         sdst += 8 * P::kc / 32;
                     } else {
                         const uint8_t* src = (const uint8_t*)(w == 0 ? p.w_gate : w == 1 ? p.w_up : p.w_down) + row * bytes_of<W>(K) + bytes_of<W>(c0);
@@ -683,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         };
         // P0: router rows (fp32 or bf16), row copies
         for (int e = e_lo; e < e_hi; e += 16) {
-            const int n = min(16, e_hi - e), step = router_cols<W>(n, D), chunks = ceil_div(D, step);
+            const int n = min(16, e_hi - e), step = router_cols<W, NT>(n, D), chunks = ceil_div(D, step);
             Turn t(at, most, 0);
             for (int c = 0, i = 0; c < chunks; ++c) {
                 int st;
@@ -829,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                          int lo_at, float (&acc)[NT][4]) {
         const int bytes = bytes_of<W>(cols);
         const bool boxa = na == 8, boxb = nb == 8;
-        const uint8_t* tile1 = tile + (boxa ? 8 * kBoxRow : na * (bytes + 16));
+        const uint8_t* tile1 = tile + (boxa ? 8 * P::box : na * (bytes + 16));
         RowPair r;
         r.a = tile + (boxa ? rw * kIn : min(rw, na - 1) * (bytes + 16));
         r.xa = boxa ? swz : 0;
@@ -899,32 +923,33 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
 
     // x into shared memory, as the expert products read it
     if constexpr (!kScaled) {
-        const int per = D * Tr<W>::xb / 16;
-#pragma unroll 2
-        for (int u = tid; u < T * per; u += kCons) {
-            const int t = u / per, c = u - t * per;
-            *(uint4*)(act + t * xstride + c * 16) = __ldg((const uint4*)p.x + (int64_t)t * per + c);
-        }
+        const int per = D * Tr<W>::xb / 32;
+        each_unit<2, 2>(
+            T * per, [&](int u, uint4* v) { v[0] = __ldg((const uint4*)p.x + 2 * u), v[1] = __ldg((const uint4*)p.x + 2 * u + 1); },
+            [&](int u, bool on, const uint4* v) {
+                const int t = u / per, c = u - t * per;
+                uint4* dst = (uint4*)(act + t * xstride + c * 32);
+                if (on) dst[0] = v[0], dst[1] = v[1];
+            });
     } else {
-        const int per = D / 16, total = T * per;  // a unit: 16 columns; whole warps stay together
-#pragma unroll 1
-        for (int u0 = tid & ~31; u0 < total; u0 += kCons) {
-            const int u = min(u0 + lane, total - 1), t = u / per, c = u - t * per;
-            const uint4* src = (const uint4*)p.x + (int64_t)u * 2;
-            const uint4 a = __ldg(src), b = __ldg(src + 1);
-            float v[16];
-            const bf16 *pa = (const bf16*)&a, *pb = (const bf16*)&b;
+        const int per = D / 16;  // a unit: 16 columns
+        each_unit<2, 2>(
+            T * per, [&](int u, uint4* v) { v[0] = __ldg((const uint4*)p.x + 2 * u), v[1] = __ldg((const uint4*)p.x + 2 * u + 1); },
+            [&](int u, bool on, const uint4* x) {
+                const int t = u / per, c = u - t * per;
+                float v[16];
+                const bf16* b = (const bf16*)x;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __bfloat162float(pa[i]), v[8 + i] = __bfloat162float(pb[i]);
-            uint8_t* row = act + t * xstride;
-            if constexpr (W == MOE_FP8_E4M3_B128) {
-                const float s = quant16_fp8(v, row + c * 32, u0 + lane < total);
-                if ((c & 7) == 0 && u0 + lane < total) xsc[t * nxs + c / 8] = s;
-            } else {
-                const float s = quant16_mx(v, row + c * 32, u0 + lane < total);
-                if ((c & 1) == 0 && u0 + lane < total) xsc[t * nxs + c / 2] = s;
-            }
-        }
+                for (int i = 0; i < 16; ++i) v[i] = __bfloat162float(b[i]);
+                uint8_t* row = act + t * xstride;
+                if constexpr (W == MOE_FP8_E4M3_B128) {
+                    const float s = quant16_fp8(v, row + c * 32, on);
+                    if ((c & 7) == 0 && on) xsc[t * nxs + c / 8] = s;
+                } else {
+                    const float s = quant16_mx(v, row + c * 32, on);
+                    if ((c & 1) == 0 && on) xsc[t * nxs + c / 2] = s;
+                }
+            });
     }
 #pragma unroll 1
     for (int i = tid; i < 512; i += kCons) m.mask[i] = 0;
@@ -946,7 +971,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     // global memory: its rows are in the caches, and the products below read
     // it quantised)
     for (int e0 = e_lo; e0 < e_hi; e0 += 16) {
-        const int ne = min(16, e_hi - e0), step = router_cols<W>(ne, D), chunks = ceil_div(D, step);
+        const int ne = min(16, e_hi - e0), step = router_cols<W, NT>(ne, D), chunks = ceil_div(D, step);
         float acc[NT][4] = {};
         if (warp < most) {
             Turn turn(at, most, warp);
@@ -1197,54 +1222,51 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                 const int hc = min(kHCols, I - h0);
                 {
                     // this batch's rows of h, 16 columns (8 in fp32) a unit
-                    constexpr int kUnit = W == MOE_F32 ? 8 : 16;
-                    const int per = hc / kUnit, total = bt.rows * per;
-#pragma unroll 1
-                    for (int u0 = tid & ~31; u0 < total; u0 += kCons) {
-                        const int u = min(u0 + lane, total - 1), r = u / per, c = u - r * per;
-                        const bool on = u0 + lane < total;
-                        const int64_t row = r < bt.shared ? T * k + r : bt.row0 + r - bt.shared;
-                        uint8_t* dst = act + r * hstride;
-                        if constexpr (W == MOE_BF16) {
-                            const uint4* src = (const uint4*)((const f16*)p.h + row * I + h0 + c * 16);
-                            const uint4 a = __ldcg(src), b = __ldcg(src + 1);
-                            ((uint4*)(dst + c * 32))[0] = a;
-                            ((uint4*)(dst + c * 32))[1] = b;
-                        } else if constexpr (W == MOE_F32) {
-                            const float4* src = (const float4*)(p.h + row * I + h0 + c * 8);
-                            const float4 a = __ldcg(src), b = __ldcg(src + 1);
-                            ((float4*)(dst + c * 32))[0] = a;
-                            ((float4*)(dst + c * 32))[1] = b;
-                        } else {
-                            const float4* src = (const float4*)(p.h + row * I + h0 + c * 16);
-                            float v[16];
+                    constexpr int kUnit = W == MOE_F32 ? 8 : 16, kWords = W == MOE_F32 || W == MOE_BF16 ? 2 : 4;
+                    const int per = hc / kUnit;
+                    each_unit<kWords, 2>(
+                        bt.rows * per,
+                        [&](int u, uint4* v) {
+                            const int r = u / per, c = u - r * per;
+                            const int64_t row = r < bt.shared ? T * k + r : bt.row0 + r - bt.shared;
+                            const uint4* src = (const uint4*)((const uint8_t*)p.h + (row * I + h0 + c * kUnit) * (W == MOE_BF16 ? 2 : 4));
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float4 a = __ldcg(src + i);
-                                v[4 * i] = a.x; v[4 * i + 1] = a.y; v[4 * i + 2] = a.z; v[4 * i + 3] = a.w;
-                            }
-                            if constexpr (W == MOE_FP8_E4M3_B128) {
-                                const float s = quant16_fp8(v, dst + c * 32, on);
-                                if ((c & 7) == 0 && on) hsc[r * nhs + c / 8] = s;
-                            } else if constexpr (W == MOE_MXFP4) {
-                                const float s = quant16_mx(v, dst + c * 32, on);
-                                if ((c & 1) == 0 && on) hsc[r * nhs + c / 2] = s;
+                            for (int i = 0; i < kWords; ++i) v[i] = __ldcg(src + i);
+                        },
+                        [&](int u, bool on, const uint4* h) {
+                            const int r = u / per, c = u - r * per;
+                            uint8_t* dst = act + r * hstride + c * 32;
+                            if constexpr (kWords == 2) {
+                                if (on) ((uint4*)dst)[0] = h[0], ((uint4*)dst)[1] = h[1];
                             } else {
-                                uint32_t hi[8], lo[8];
+                                float v[16];
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    hi[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-                                    const float2 b = __bfloat1622float2(*(const __nv_bfloat162*)&hi[i]);
-                                    lo[i] = pack_bf16(v[2 * i] - b.x, v[2 * i + 1] - b.y);
+                                for (int i = 0; i < 4; ++i) {
+                                    v[4 * i] = __uint_as_float(h[i].x), v[4 * i + 1] = __uint_as_float(h[i].y);
+                                    v[4 * i + 2] = __uint_as_float(h[i].z), v[4 * i + 3] = __uint_as_float(h[i].w);
                                 }
+                                if constexpr (W == MOE_FP8_E4M3_B128) {
+                                    const float s = quant16_fp8(v, dst, on);
+                                    if ((c & 7) == 0 && on) hsc[r * nhs + c / 8] = s;
+                                } else if constexpr (W == MOE_MXFP4) {
+                                    const float s = quant16_mx(v, dst, on);
+                                    if ((c & 1) == 0 && on) hsc[r * nhs + c / 2] = s;
+                                } else if (on) {
+                                    uint32_t hi[8], lo[8];
 #pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    ((uint4*)(dst + c * 32))[i] = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-                                    ((uint4*)(dst + lo_at + c * 32))[i] = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+                                    for (int i = 0; i < 8; ++i) {
+                                        hi[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+                                        const float2 b = __bfloat1622float2(*(const __nv_bfloat162*)&hi[i]);
+                                        lo[i] = pack_bf16(v[2 * i] - b.x, v[2 * i + 1] - b.y);
+                                    }
+#pragma unroll
+                                    for (int i = 0; i < 2; ++i) {
+                                        ((uint4*)dst)[i] = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+                                        ((uint4*)(dst + lo_at))[i] = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+                                    }
                                 }
                             }
-                        }
-                    }
+                        });
                 }
                 consumers_sync();
                 const int units = (bt.x1 - bt.x0) * tp, warps = min(units, most / tp * tp);
@@ -1359,30 +1381,30 @@ constexpr int kSmemLimit = 232448;
 
 // Shared memory for T tokens: rows of h's buffer, where the ring starts, and
 // its stages.
-template <int W> bool plan_smem(int T, int D, int I, int k, int* hcap, int* ring_at, int* stages) {
+template <int W, int NT> bool plan_smem(int T, int D, int I, int k, int* hcap, int* ring_at, int* stages) {
     const int64_t misc = up((int)sizeof(Misc), 128);
     const int64_t x = (int64_t)up(T * x_stride<W>(D), 128) + up(T * x_scales<W>(D), 128);
     const int64_t hrow = h_stride<W>(I) + h_scales<W>(I);
     // h's buffer takes x's place; at least the rows of one expert, at most
     // all of them, and beyond x only what leaves a ring of twelve stages
     const int64_t all = (int64_t)T * (k + 1);
-    const int64_t room = std::max(x, std::min(all * hrow + 256, (int64_t)kSmemLimit - misc - 12 * Plan<W>::stage));
+    const int64_t room = std::max(x, std::min(all * hrow + 256, (int64_t)kSmemLimit - misc - 12 * 512 / Plan<W, NT>::box * Plan<W, NT>::stage));
     const int64_t cap = std::max<int64_t>(T, std::min(all, (room - 256) / hrow));
     const int64_t at = misc + std::max(x, cap * hrow + 256);
     if (at > kSmemLimit) return false;
     *hcap = (int)cap;
     *ring_at = up((int)at, 1024);
-    *stages = std::min(kMaxStages, (kSmemLimit - *ring_at) / Plan<W>::stage);
+    *stages = std::min(kMaxStages, (kSmemLimit - *ring_at) / Plan<W, NT>::stage);
     return *stages >= 4;
 }
 
-// A matrix of `rows` rows of `bytes` as boxes of 8 rows and kBoxRow bytes,
+// A matrix of `rows` rows of `bytes` as boxes of 8 rows and `box` bytes,
 // laid out [line of `in` bytes][row][in], swizzled over a line.
-template <int W> bool weight_map(CUtensorMap* m, const void* base, int64_t rows, int64_t bytes) {
+template <int W, int NT> bool weight_map(CUtensorMap* m, const void* base, int64_t rows, int64_t bytes) {
     constexpr int in = Tr<W>::in;
     const cuuint64_t dims[3] = {in, (cuuint64_t)rows, (cuuint64_t)(bytes / in)};
     const cuuint64_t strides[2] = {(cuuint64_t)bytes, in};
-    const cuuint32_t box[3] = {in, 8, kBoxRow / in}, es[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {in, 8, Plan<W, NT>::box / in}, es[3] = {1, 1, 1};
     return tc::encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                            in == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -1390,14 +1412,25 @@ template <int W> bool weight_map(CUtensorMap* m, const void* base, int64_t rows,
 // Scale bytes [rows, bytes], boxes of 8 rows and a stage's columns.
 bool scale_map(CUtensorMap* m, const void* base, int64_t rows, int64_t bytes) {
     const cuuint64_t dims[2] = {(cuuint64_t)bytes, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)bytes};
-    const cuuint32_t box[2] = {Plan<MOE_MXFP4>::kc / 32, 8}, es[2] = {1, 1};
+    const cuuint32_t box[2] = {Plan<MOE_MXFP4, 1>::kc / 32, 8}, es[2] = {1, 1};
     return tc::encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                            CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int W, int NT, bool ONE = false> cudaError_t launch(FewParams p, const Maps& maps, int num_sms, cudaStream_t s) {
-    if (!plan_smem<W>(p.T, p.D, p.I, p.k, &p.hcap, &p.ring_at, &p.stages)) return cudaErrorInvalidConfiguration;
-    const int bytes = p.ring_at + p.stages * Plan<W>::stage;
+template <int W, int NT, bool ONE = false> cudaError_t launch(FewParams p, int num_sms, cudaStream_t s) {
+    if (!plan_smem<W, NT>(p.T, p.D, p.I, p.k, &p.hcap, &p.ring_at, &p.stages)) return cudaErrorInvalidConfiguration;
+    Maps maps = {};
+    if (!tc::encode_fn()) return cudaErrorNotSupported;
+    const int64_t gr = (int64_t)(p.E + 1) * p.I, dr = (int64_t)(p.E + 1) * p.D;
+    bool ok = weight_map<W, NT>(&maps.w[0], p.w_gate, gr, bytes_of<W>(p.D)) && weight_map<W, NT>(&maps.w[1], p.w_up, gr, bytes_of<W>(p.D)) &&
+              weight_map<W, NT>(&maps.w[2], p.w_down, dr, bytes_of<W>(p.I));
+    // scales by TMA where their rows are whole 16-byte pieces
+    p.tma_scales = W == MOE_MXFP4 && p.D % 512 == 0 && p.I % 512 == 0;
+    if (p.tma_scales)
+        ok = ok && scale_map(&maps.s[0], p.s_gate, gr, p.D / 32) && scale_map(&maps.s[1], p.s_up, gr, p.D / 32) &&
+             scale_map(&maps.s[2], p.s_down, dr, p.I / 32);
+    if (!ok) return cudaErrorInvalidValue;
+    const int bytes = p.ring_at + p.stages * Plan<W, NT>::stage;
     cudaError_t e = ensure_smem_attr((const void*)few_kernel<W, NT, ONE>, kSmemLimit);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -1419,29 +1452,17 @@ template <int W> cudaError_t launch_chunks(const FewParams& p, int num_sms, cuda
     // As many tokens at a time as their x leaves room for a ring of
     // four stages (16 at D = 4096; wider rows take a few launches).
     int per = std::min(p.T, kFewMax), hcap, ring_at, stages;
-    while (per > 1 && !plan_smem<W>(per, p.D, p.I, p.k, &hcap, &ring_at, &stages)) --per;
-    Maps maps = {};
-    if (!tc::encode_fn()) return cudaErrorNotSupported;
-    const int64_t gr = (int64_t)(p.E + 1) * p.I, dr = (int64_t)(p.E + 1) * p.D;
-    bool ok = weight_map<W>(&maps.w[0], p.w_gate, gr, bytes_of<W>(p.D)) && weight_map<W>(&maps.w[1], p.w_up, gr, bytes_of<W>(p.D)) &&
-              weight_map<W>(&maps.w[2], p.w_down, dr, bytes_of<W>(p.I));
-    // scales by TMA where their rows are whole 16-byte pieces
-    const bool tma_scales = W == MOE_MXFP4 && p.D % 512 == 0 && p.I % 512 == 0;
-    if (tma_scales)
-        ok = ok && scale_map(&maps.s[0], p.s_gate, gr, p.D / 32) && scale_map(&maps.s[1], p.s_up, gr, p.D / 32) &&
-             scale_map(&maps.s[2], p.s_down, dr, p.I / 32);
-    if (!ok) return cudaErrorInvalidValue;
+    while (per > 1 && !(per > 8 ? plan_smem<W, 2> : plan_smem<W, 1>)(per, p.D, p.I, p.k, &hcap, &ring_at, &stages)) --per;
     for (int t0 = 0; t0 < p.T; t0 += per) {
         FewParams c = p;
         c.T = std::min(per, p.T - t0);
         c.tok0 = t0;
-        c.tma_scales = tma_scales;
         c.plane = p.T * p.k;
         c.x = (const char*)p.x + (int64_t)t0 * p.D * (W == MOE_F32 ? 4 : 2);
         c.logits = p.logits + (int64_t)t0 * p.E;
         c.blob = p.blob + t0 * p.k;
         c.out = (char*)p.out + (int64_t)t0 * p.D * (p.out_elem == kF32 ? 4 : 2);
-        const cudaError_t e = W == MOE_MXFP4 && c.T == 1 ? launch<W, 1, W == MOE_MXFP4>(c, maps, num_sms, s) : c.T <= 8 ? launch<W, 1>(c, maps, num_sms, s) : launch<W, 2>(c, maps, num_sms, s);
+        const cudaError_t e = W == MOE_MXFP4 && c.T == 1 ? launch<W, 1, W == MOE_MXFP4>(c, num_sms, s) : c.T <= 8 ? launch<W, 1>(c, num_sms, s) : launch<W, 2>(c, num_sms, s);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
