@@ -31,13 +31,14 @@
 //       keeps their weighted sum in registers; the warps' sums are added once,
 //       in warp order, so there are no atomics and the result does not vary
 //
-// Work is split to the row (flattened ranges, tiles cut where a range or an
-// expert ends), so the SMs' byte counts differ by a row at most.  Eight rows
-// come as one box of 8 x 512 bytes; the rows left over come as row copies,
-// one feature a tile, so that the warps share them.  A dot product does not
-// mind the order of its terms, so each lane takes 16 contiguous bytes (4-bit:
-// 4) of its row and the same columns of its token as fragments; no shuffles,
-// no ldmatrix.
+// Gate and up are split by tiles (flattened over the experts), down to the
+// row.  Eight rows come as one box; rows left over come as row copies.  (Gate
+// and up split to the feature even out the bytes, 67 features a CTA instead of
+// 64 or 72, but then the one tile of row copies is last to finish: 58.5 us
+// instead of @@ for one bf16 token.)  A dot product does not mind the order of
+// its terms, so each lane takes 16 contiguous bytes (4-bit: 4 or 16) of its
+// row and the same columns of its token as fragments; no shuffles, no
+// ldmatrix.
 //
 // Arithmetic, as moe_forward's: products of weights and activations as the
 // type holds them (x and h quantised for FP8 and MXFP4; h as fp16 against
@@ -456,11 +457,11 @@ __device__ __forceinline__ void each_unit(int total, Load load, Store store) {
     }
 }
 
-// Grid barrier on a counter that only grows (every launch adds whole
-// multiples of the grid): arrive returns the count to wait for.
-__device__ __forceinline__ unsigned long long grid_arrive(unsigned long long* bar) {
-    __threadfence();
-    return (atomicAdd(bar, 1ull) / gridDim.x + 1) * gridDim.x;
+// Grid barrier on a counter that only grows: every launch adds whole multiples
+// of the grid, so what a CTA reads before it arrives tells the count to wait
+// for, and nobody waits for an atomic's answer.
+__device__ __forceinline__ void grid_arrive(unsigned long long* bar) {
+    asm volatile("red.release.gpu.global.add.u64 [%0], %1;" ::"l"(bar), "l"(1ull) : "memory");
 }
 __device__ __forceinline__ bool grid_wait(const unsigned long long* bar, unsigned long long target, int64_t limit_ns, volatile int* abort) {
     uint64_t t0 = 0;
@@ -561,27 +562,6 @@ __device__ __forceinline__ void share(int n, int cta, int grid, int& lo, int& hi
     lo = per * cta + min(cta, more);
     hi = lo + per + (cta < more);
 }
-// Features [lo, hi) of the listed experts' n I in tiles of eight that end
-// where an expert does.
-struct Tiles {
-    int first, pos, f, I;  // tiles up to the first expert's end; its place in the list, the first feature
-    int lo, mid, hi;       // mid: where the first expert ends
-    int n;
-    __device__ __forceinline__ Tiles(int a, int b, int width) : I(width), lo(a), hi(b) {
-        pos = lo / I;
-        f = lo - pos * I;
-        mid = min(hi, lo + (I - f));
-        first = (mid - lo + 7) / 8;
-        n = first + (hi - mid + 7) / 8;
-    }
-    // tile j: place in the list, first feature, features
-    __device__ __forceinline__ void get(int j, int& place, int& feature, int& count) const {
-        const int a = j < first ? lo + 8 * j : mid + 8 * (j - first);
-        place = a / I;
-        feature = a - place * I;
-        count = min(8, (j < first ? mid : hi) - a);
-    }
-};
 // dot_one's shares, summed over the four lanes of a row pair.
 __device__ __forceinline__ void sum_quad(float (&acc)[4]) {
 #pragma unroll
@@ -635,10 +615,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     }
     __syncthreads();
 
-    // shares of this CTA: router rows, shared features, output rows
+    // shares of this CTA: router rows, tiles of the shared expert's features, output rows
     int e_lo, e_hi, f_lo, f_hi, d_lo, d_hi;
     share(E, cta, grid, e_lo, e_hi);
-    share(I, cta, grid, f_lo, f_hi);
+    share(I / 8, cta, grid, f_lo, f_hi);
     share(D, cta, grid, d_lo, d_hi);
     Walk at = {p.stages, 0, 0};
 
@@ -728,9 +708,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             finish(most, chunks, 1);
         }
         // P1 (tiles of the shared expert, their stages spread over the warps), P2, then P3's batches
-        int phase = 1, n = 0, f1 = f_lo, bx = -1, h0 = 0, d0 = d_lo;
+        int phase = 1, n = 0, f1 = f_lo, bx = -1, h0 = 0, d0 = d_lo, t_lo = 0, t_hi = 0;
         Batch bt = {};
-        Tiles tiles(0, 0, I);
 #pragma unroll 1
         while (true) {
             int units, warps, steps, K = D, col0 = 0, width = D;  // columns [col0, col0 + width) of rows of K
@@ -738,17 +717,15 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             if (phase == 1 && f1 >= f_hi) {
                 // the routed experts, once the list is there
                 n = wait(smem_u32(&m.list_ready), 0) ? uniform(m.n) : 0;
-                int lo, hi;
-                share(n * I, cta, grid, lo, hi);
-                tiles = Tiles(lo, hi, I);
-                phase = tiles.n > 0 ? 2 : 3;
+                share(n * (I / 8), cta, grid, t_lo, t_hi);
+                phase = t_hi > t_lo ? 2 : 3;
             }
             if (phase == 1) {
                 units = ceil_div(D, P::kc);
                 warps = most;
                 steps = 1;
             } else if (phase == 2) {
-                units = tiles.n;
+                units = t_hi - t_lo;
                 warps = min(units, most);
                 steps = ceil_div(D, P::kc);
             } else {
@@ -772,14 +749,13 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                 int64_t row = 0;
                 int count = 0, c0 = 0;  // count: rows of its first matrix, and of the second << 8
                 if (have && phase == 1) {
-                    row = (int64_t)E * I + f1;
-                    count = min(8, f_hi - f1) * 0x101;
+                    row = (int64_t)E * I + 8 * f1;
+                    count = 8 * 0x101;
                     c0 = u * P::kc;
                 } else if (have && phase == 2) {
-                    int pos, f;
-                    tiles.get(u, pos, f, count);
-                    row = (int64_t)m.expert[pos] * I + f;
-                    count *= 0x101;
+                    const int pos = (t_lo + u) / (I / 8);
+                    row = (int64_t)m.expert[pos] * I + 8 * (t_lo + u - pos * (I / 8));
+                    count = 8 * 0x101;
                 } else if (have) {
                     const int x = bt.x0 + (tp == 2 ? u >> 1 : u), j = tp == 2 ? u & 1 : 0, rows = min(16, nr - 16 * j);
                     row = (int64_t)(x < 0 ? E : m.expert[x]) * D + d0 + 16 * j;
@@ -798,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             }
             finish(warps, units, steps);
             if (phase == 1) {
-                f1 += 8;
+                ++f1;
             } else if (phase == 2) {
                 phase = 3;
             } else if ((h0 += kHCols) >= I) {  // the next batch; after the last, the next rows
@@ -921,6 +897,12 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         }
     };
 
+    unsigned long long target = 0;
+    if (tid == 0) {
+        unsigned long long v;
+        asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p.bar) : "memory");
+        target = (v / grid + 1) * grid;
+    }
     // x into shared memory, as the expert products read it
     if constexpr (!kScaled) {
         const int per = D * Tr<W>::xb / 32;
@@ -1024,8 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         consumers_sync();  // logits written, red read
     }
     consumers_sync();  // x in shared memory (also where there are no router rows)
-    unsigned long long target = 0;
-    if (tid == 0) target = grid_arrive(p.bar);
+    if (tid == 0) grid_arrive(p.bar);
 
     bool overflow = false;
     auto put_h = [&](int64_t o, float h) {
@@ -1036,8 +1017,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             p.h[o] = h;
         }
     };
-    // h of the tile of nf features f0 .. of the expert at place pos (-1: shared)
-    auto put_tile = [&](float (&acc)[NT][4], int pos, int f0, int nf) {
+    // h of the tile of eight features f0 .. of the expert at place pos (-1: shared)
+    auto put_tile = [&](float (&acc)[NT][4], int pos, int f0) {
         if constexpr (ONE) sum_quad(acc[0]);
         const int row = pos < 0 ? T * k : m.hrow[pos];
         const uint32_t tokens = pos < 0 ? 0xFFFFu : m.tokens[pos];
@@ -1046,7 +1027,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const int t = 8 * u + 2 * q + s;
-                if (rw < nf && t < T && ((tokens >> t) & 1u))
+                if (t < T && ((tokens >> t) & 1u))
                     put_h((int64_t)(row + __popc(tokens & ((1u << t) - 1u))) * I + f0 + rw, swiglu(acc[u][s], acc[u][2 + s]));
             }
     };
@@ -1059,9 +1040,9 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             z[0] += a.x; z[1] += a.y; z[2] += a.z; z[3] += a.w;
         }
     };
-    // A stage, columns c0 .., of the tile of nf features f0 .. of expert e.
-    auto gateup_stage = [&](Turn& turn, int e, int f0, int nf, int c0, float (&acc)[NT][4]) {
-        const int cols = min(P::kc, D - c0), fr = f0 + min(rw, nf - 1);
+    // A stage, columns c0 .., of the tile of eight features f0 .. of expert e.
+    auto gateup_stage = [&](Turn& turn, int e, int f0, int c0, float (&acc)[NT][4]) {
+        const int cols = min(P::kc, D - c0), fr = f0 + rw;
         const uint8_t *ta[NT], *tb[NT];
         const float *sa[NT], *sb[NT];
 #pragma unroll
@@ -1083,7 +1064,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             gb = (const uint8_t*)p.s_up + blk;
         }
         const uint8_t* tile = stage_wait(turn);
-        stage_dot(tile, nf, nf, cols, ta, tb, sa, sb, ga, gb, wa, wb, No{}, 0, acc);
+        stage_dot(tile, 8, 8, cols, ta, tb, sa, sb, ga, gb, wa, wb, No{}, 0, acc);
         stage_done(turn);
     };
     // ---------------------------------------------- barrier 1, top-k, list
@@ -1161,25 +1142,27 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     // ------------------------------------------------------------ P1, P2
     // P1's tiles (the shared expert's), as P0's: stages spread over the
     // warps; then P2's, a tile a warp.
-    int share_lo, share_hi;
-    share(n * I, cta, grid, share_lo, share_hi);
-    const Tiles tiles(share_lo, share_hi, I);
+    int t_lo, t_hi;
+    share(n * (I / 8), cta, grid, t_lo, t_hi);
 #pragma unroll 1
-    for (int f1 = f_lo;; f1 += 8) {
+    for (int f1 = f_lo;; ++f1) {
         const bool p1 = f1 < f_hi;
-        const int chunks = ceil_div(D, P::kc), units = p1 ? chunks : tiles.n, warps = p1 ? most : min(units, most);
+        const int chunks = ceil_div(D, P::kc), units = p1 ? chunks : t_hi - t_lo, warps = p1 ? most : min(units, most);
         if (units == 0) break;
         float acc[NT][4] = {};
-        int pos = -1, f0 = f1, nf = min(8, f_hi - f1);
+        int pos = -1, f0 = 8 * f1;
         Turn turn(at, warps, warp);
 #pragma unroll 1
         for (int j = warp; j < (warp < warps ? units : 0); j += warps) {
-            if (!p1) tiles.get(j, pos, f0, nf);
+            if (!p1) {
+                pos = (t_lo + j) / (I / 8);
+                f0 = 8 * (t_lo + j - pos * (I / 8));
+            }
             const int e = p1 ? E : m.expert[pos];
 #pragma unroll 1
-            for (int c0 = p1 ? j * P::kc : 0, c1 = p1 ? c0 + 1 : D; c0 < c1; c0 += P::kc) gateup_stage(turn, e, f0, nf, c0, acc);
+            for (int c0 = p1 ? j * P::kc : 0, c1 = p1 ? c0 + 1 : D; c0 < c1; c0 += P::kc) gateup_stage(turn, e, f0, c0, acc);
             if (!p1) {
-                put_tile(acc, pos, f0, nf);
+                put_tile(acc, pos, f0);
 #pragma unroll
                 for (int u = 0; u < NT; ++u) acc[u][0] = acc[u][1] = acc[u][2] = acc[u][3] = 0.0f;
             }
@@ -1192,14 +1175,15 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         if (warp == 0) {
 #pragma unroll
             for (int u = 0; u < NT; ++u) sum_red(u, acc[u]);
-            put_tile(acc, -1, f0, nf);
+            put_tile(acc, -1, f0);
         }
         consumers_sync();
     }
     if (overflow) record_error(p.err, MOE_ERR_NONFINITE, 5, cta, 0);
     consumers_sync();
     if (tid == 0) {
-        target = grid_arrive(p.bar);
+        grid_arrive(p.bar);
+        target += grid;
         if (!grid_wait(p.bar, target, lim, abort)) {
             if (!*abort) record_error(p.err, MOE_ERR_DEVICE_TIMEOUT, 44, cta, 0);
             *abort = 1;
