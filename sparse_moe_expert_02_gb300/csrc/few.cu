@@ -4,26 +4,36 @@
 // At these sizes the layer is its weights: each touched expert's three
 // matrices pass through the SMs once (T = 1, D = 4096, I = 1024, top_k = 10:
 // 277 MB in bf16, 73 MB in 4 bits) and everything else is latency.  So the
-// kernel is a weight stream.  Two producer warps fill a ring of 8 KB stages
-// by TMA, as far ahead as shared memory allows and across the phases below;
-// twelve consumer warps each take a tile of 16 weight rows through all of its
-// columns, a stage at a time, with mma.sync: the rows are the M side, the
-// tokens the N side (16 x 8), so a tile costs the same for one token as for
-// eight, its sums stay in one warp's registers, and the pointers, waits and
-// routing of a tile are paid once.  (Split over eight warps by columns, with
-// the partial sums added through shared memory, the same tiles cost 2.5
-// times the instructions, and the 4-bit layer was bound by their issue.)  The
-// stages of twelve tiles lie in the ring in turn.  tcgen05 would want 128
-// rows and its operands in its own layout; at HBM speed mma.sync is far from
-// its limit.
+// kernel is a weight stream.  Four producer warps fill a ring of 8 KB (16-bit
+// weights: 16 KB) stages by TMA, as far ahead as shared memory allows and
+// across the phases below; twelve consumer warps each take tiles of 16 weight
+// rows through all of their columns, a stage at a time, with mma.sync: the
+// rows are the M side, the tokens the N side (16 x 8), so a tile costs the
+// same for one token as for eight, its sums stay in one warp's registers, and
+// the pointers, waits and routing of a tile are paid once.  (Two groups of
+// eight warps that split a tile's columns and add up through shared memory
+// took 57.2 us where this takes 37.2, 4 bits, T = 1: the 4-bit layer is bound
+// by instructions.)  tcgen05 would want 128 rows and its operands in its own
+// layout; at HBM speed mma.sync is far from its limit.
+//
+// Measured (D = 4096, I = 1024, top_k = 10, weights from HBM): T = 1 bf16 58.0
+// us, 4.8 TB/s of weights over the whole call, 6 in P2 and 5.2 in P3; 4 bits
+// 34.4 us; T = 8 FP8 112 us, 5.1 TB/s.  What is left is 9 to 12 us until the
+// list of experts stands (launch, router, barrier, top-k: a chain of
+// latencies), 3 us from the last gate/up tile to the first down product, and
+// code that is read from memory on its first use: the kernel runs each line
+// about once, and halving its size (one copy of the fill and of the gate/up
+// loop, loops left rolled) took 48.0 us to 38.4 (4 bits) and 29.4 to 24.6
+// (fp32, T = 5).  So most loops here are kept rolled on purpose.
 //
 //   P0  router logits: the CTA's share of the E rows; arrive at barrier 1
-//   P1  shared expert's gate/up (needs no routing): its share of I features
 //   --  wait for barrier 1; every CTA takes the top-k of all T tokens and
 //       builds the same list of distinct experts
-//   P2  routed gate/up: its share of the (expert, feature) pairs, in tiles of
-//       8 gate rows and the 8 up rows of the same features, so that a
-//       thread's accumulators hold both and SwiGLU is local; h to global
+//   P1  shared expert's gate/up: its share of I features, whose weights need
+//       no list and are in the ring by then
+//   P2  routed gate/up: its share of the (expert, feature) pairs.  Tiles of 8
+//       gate rows and the 8 up rows of the same features, so that a thread's
+//       accumulators hold both and SwiGLU is local; h to global
 //   --  barrier 2 (the ring is already filling with P3's weights)
 //   P3  down: the CTA's share of the D output rows, over all experts, h
 //       brought into shared memory (and quantised) a batch of experts at a
@@ -34,20 +44,19 @@
 // Gate and up are split by tiles (flattened over the experts), down to the
 // row.  Eight rows come as one box; rows left over come as row copies.  (Gate
 // and up split to the feature even out the bytes, 67 features a CTA instead of
-// 64 or 72, but then the one tile of row copies is last to finish: 58.5 us
-// instead of @@ for one bf16 token.)  A dot product does not mind the order of
-// its terms, so each lane takes 16 contiguous bytes (4-bit: 4 or 16) of its
-// row and the same columns of its token as fragments; no shuffles, no
-// ldmatrix.
+// 64 or 72, but then the one tile of row copies is last to finish: 4 bits 37.5
+// us instead of 34.4.)  A dot product does not mind the order of its terms, so
+// each lane takes 16 contiguous bytes (4-bit: 4 or 16) of its row and the same
+// columns of its token as fragments; no shuffles, no ldmatrix.
 //
 // Arithmetic, as moe_forward's: products of weights and activations as the
 // type holds them (x and h quantised for FP8 and MXFP4; h as fp16 against
 // W_down's fp16 copy, or as a bf16 pair, for bf16), fp32 accumulation, block
 // scales applied in fp32 to each block's partial sum.  E4M3 and E2M1 codes
 // become fp16 MMA operands by one conversion per two of them, exactly, and
-// the quantised activations are held as fp16.  (mma.sync with E4M3 operands is
-// no faster here: it converts both to fp16 on its way, three times the
-// instructions for the 4-bit layer, whose codes became E4M3 first.)
+// the quantised activations are held as fp16.  (mma.sync with E4M3 operands,
+// the 4-bit codes made E4M3 by shifts and masks, took 58.5 us instead of 44.3
+// at 4 bits, T = 1, on otherwise the same kernel.)
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -1434,9 +1443,14 @@ template <int W, int NT, bool ONE = false> cudaError_t launch(FewParams p, int n
 
 template <int W> cudaError_t launch_chunks(const FewParams& p, int num_sms, cudaStream_t s) {
     // As many tokens at a time as their x leaves room for a ring of
-    // four stages (16 at D = 4096; wider rows take a few launches).
-    int per = std::min(p.T, kFewMax), hcap, ring_at, stages;
-    while (per > 1 && !(per > 8 ? plan_smem<W, 2> : plan_smem<W, 1>)(per, p.D, p.I, p.k, &hcap, &ring_at, &stages)) --per;
+    // four stages (16 at D = 4096; wider rows take a few launches).  4 bits:
+    // at most eight, since there the products of a second token tile cost
+    // more than reading the weights again (16 tokens, D = 4096, I = 1024,
+    // E = 128: 366 us in one launch, 282 in two; FP8 302 against 332).
+    constexpr int kTiles = W == MOE_MXFP4 ? 1 : 2;
+    const int launches = (p.T + 7) / 8;
+    int per = W == MOE_MXFP4 ? (p.T + launches - 1) / launches : std::min(p.T, kFewMax), hcap, ring_at, stages;
+    while (per > 1 && !(per > 8 ? plan_smem<W, kTiles> : plan_smem<W, 1>)(per, p.D, p.I, p.k, &hcap, &ring_at, &stages)) --per;
     for (int t0 = 0; t0 < p.T; t0 += per) {
         FewParams c = p;
         c.T = std::min(per, p.T - t0);
@@ -1446,7 +1460,7 @@ template <int W> cudaError_t launch_chunks(const FewParams& p, int num_sms, cuda
         c.logits = p.logits + (int64_t)t0 * p.E;
         c.blob = p.blob + t0 * p.k;
         c.out = (char*)p.out + (int64_t)t0 * p.D * (p.out_elem == kF32 ? 4 : 2);
-        const cudaError_t e = W == MOE_MXFP4 && c.T == 1 ? launch<W, 1, W == MOE_MXFP4>(c, num_sms, s) : c.T <= 8 ? launch<W, 1>(c, num_sms, s) : launch<W, 2>(c, num_sms, s);
+        const cudaError_t e = W == MOE_MXFP4 && c.T == 1 ? launch<W, 1, W == MOE_MXFP4>(c, num_sms, s) : c.T <= 8 ? launch<W, 1>(c, num_sms, s) : launch<W, kTiles>(c, num_sms, s);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

@@ -243,6 +243,30 @@ def test_mx_matmul_grouped(sizes, N, K):
             check_product(out, av, bv[g], slice(off[g], off[g + 1]))
 
 
+@pytest.mark.parametrize("out_dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,N,K", [(2600, 4104, 224), (5000, 2050, 64), (130, 33000, 96)])
+def test_mx_matmul_many_tiles_a_cta(out_dtype, rows, N, K):
+    a, av = random_mx((rows, K), 11)
+    b, bv = random_mx((N, K), 12)
+    check_product(mx.matmul(a, b, out_dtype=out_dtype), av, bv)
+
+
+@pytest.mark.parametrize("average", [40, 100, 260])
+@pytest.mark.parametrize("N,K", [(1030, 352)])
+def test_mx_matmul_grouped_many_tiles_a_cta(average, N, K):
+    G = 24
+    sizes = np.random.default_rng(average).integers(0, 2 * average, G)
+    sizes[5] = 0
+    rows = int(sizes.sum())
+    a, av = random_mx((rows, K), 13)
+    b, bv = random_mx((G, N, K), 14)
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    out = mx.matmul(a, b, offsets=torch.from_numpy(off).cuda(), out_dtype=BF16)
+    for g in range(G):
+        if sizes[g]:
+            check_product(out, av, bv[g], slice(off[g], off[g + 1]))
+
+
 def test_mx_matmul_rows_of_no_group_strided_out_and_bad_offsets():
     a, av = random_mx((40, 64), 5)
     b, bv = random_mx((2, 48, 64), 6)
@@ -327,6 +351,17 @@ def test_few_layer(dtype, T, D, E, I, k, zipf):
     layer.check()
     few_check(dtype, shape, inp, layer, out)
     # and again: nothing of the first call is left to disturb the second
+    assert torch.equal(out, layer.forward_few(inp["x"]))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "fp8", "mxfp4"])
+@pytest.mark.parametrize("T,D,E,I,k,zipf", [(2, 1024, 8, 2176, 3, None), (1, 512, 5, 2176, 4, None), (1, 4096, 24, 1024, 10, None),
+                                            (16, 512, 700, 128, 20, None), (12, 512, 6, 4096, 4, 1.0)])
+def test_few_layer_many_tiles_a_warp(dtype, T, D, E, I, k, zipf):
+    shape, inp, layer = few_case(dtype, T, D, E, I, k, zipf, seed=3)
+    out = layer.forward_few(inp["x"])
+    layer.check()
+    few_check(dtype, shape, inp, layer, out)
     assert torch.equal(out, layer.forward_few(inp["x"]))
 
 
