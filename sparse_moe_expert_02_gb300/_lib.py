@@ -9,6 +9,7 @@ there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import struct
 import threading
@@ -287,26 +288,11 @@ def moe_pack_routing_words(plan, T, ws, words, stream=None):
         "moe_pack_routing_words")
 
 
-# Operators of the block.  Rows of a 2-D tensor may be strided (inner stride
-# 1); moe_norm and moe_post are passed packed, as the header lays them out.
+# Operators of the block.  moe_norm and moe_post as lib()'s entry points take
+# them, packed.
 
-_DTYPE_OF = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 NORM_STRUCT = struct.Struct("@iffiPP")
 POST_STRUCT = struct.Struct("@iffiPPiffiPPffiii4xPq")
-
-
-def _rows(t, what: str):
-    """(address, moe_dtype, row stride) of a 2-D device tensor of fp32 or bf16."""
-    dt = _DTYPE_OF.get(t.dtype)
-    if dt is None:
-        raise ValueError(f"{what}: fp32 or bf16, not {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{what}: libmoe takes device tensors")
-    s = t.stride()
-    if len(s) != 2 or (s[1] != 1 and t.size(1) > 1):
-        raise ValueError(f"{what}: a 2-D tensor whose rows are contiguous")
-    # the stride of a single row says nothing (it may be anything)
-    return t.data_ptr(), dt, s[0] if t.size(0) > 1 else t.size(1)
 
 
 def moe_forward_few(plan, weights: moe_weights, x, T, out, blob_out, logits_out, ws, stream=None):
@@ -314,40 +300,56 @@ def moe_forward_few(plan, weights: moe_weights, x, T, out, blob_out, logits_out,
                               _ptr(logits_out), _ptr(ws), _wsb(ws), _stream(stream)), "moe_forward_few")
 
 
-def moe_norm_pre(norm: bytes, x, out, stream=None):
-    xp, xt, xl = _rows(x, "x")
-    op, ot, ol = _rows(out, "out")
-    T, D = x.shape
-    _ok(lib().moe_norm_pre(norm, xp, xt, xl, T, D, op, ot, ol, _stream(stream)), "moe_norm_pre")
+_fast = None
 
 
-def moe_norm_post(post: bytes, y, res, out, next_out, stream=None):
-    yp, yt, yl = _rows(y, "y")
-    rp, rt, rl = _rows(res, "res")
-    op, ot, ol = _rows(out, "out")
-    if ot != rt:
-        raise ValueError("out: the type of res")
-    np_, nt, nl = (None, MOE_BF16, 0) if next_out is None else _rows(next_out, "next_out")
-    T, D = y.shape
-    _ok(lib().moe_norm_post(post, yp, yt, yl, rp, rt, rl, T, D, op, ol, np_, nt, nl, _stream(stream)), "moe_norm_post")
+def fast():
+    """The module that checks and calls the small operators (csrc/fastcall.c)."""
+    global _fast
+    if _fast is None:
+        L = lib()
+        spec = importlib.util.spec_from_file_location("_fastcall", _build.FAST)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        names = ("moe_norm_pre", "moe_norm_post", "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_gemm")
+        raw = _raw_stream or (lambda device: torch.cuda.current_stream(device).cuda_stream)
+        m.init((torch.float32, torch.bfloat16, torch.uint8, torch.int32), getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+               raw, tuple(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names))
+        _fast = m
+    return _fast
 
 
-def moe_mx_quantize(x, q, s, stream=None):
-    xp, xt, xl = _rows(x, "x")
-    _ok(lib().moe_mx_quantize(xp, xt, xl, x.shape[0], x.shape[1], _ptr(q), _ptr(s), _stream(stream)),
-        "moe_mx_quantize")
+# Each takes tensors, checks them and returns after the launch.
+
+def moe_norm_pre(x, w, b, kind: int, eps: float, w_offset: float, out):
+    status = (_fast or fast()).norm_pre(x, w, b, kind, eps, w_offset, out)
+    if status:
+        raise MoEError(status, "moe_norm_pre")
 
 
-def moe_mx_dequantize(q, s, out, stream=None):
-    op, ot, ol = _rows(out, "out")
-    _ok(lib().moe_mx_dequantize(_ptr(q), _ptr(s), out.shape[0], out.shape[1], op, ot, ol, _stream(stream)),
-        "moe_mx_dequantize")
+def moe_norm_post(*args):
+    """y, res, out, next_out, kind, eps, w_offset, w, b, next_kind, next_w, next_b, res_scale, branch_scale, gate_by, gate, gate_sigmoid"""
+    status = (_fast or fast()).norm_post(*args)
+    if status:
+        raise MoEError(status, "moe_norm_post")
 
 
-def moe_mx_gemm(a, a_scale, b, b_scale, offsets, G: int, N: int, K: int, out, err=None, stream=None):
-    op, ot, ol = _rows(out, "out")
-    _ok(lib().moe_mx_gemm(_ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale), _ptr(offsets), out.shape[0], G, N, K, op, ot,
-                          ol, _ptr(err), _stream(stream)), "moe_mx_gemm")
+def moe_mx_quantize(x, q, s, cols: int):
+    status = (_fast or fast()).mx_quantize(x, q, s, cols)
+    if status:
+        raise MoEError(status, "moe_mx_quantize")
+
+
+def moe_mx_dequantize(q, s, cols: int, out):
+    status = (_fast or fast()).mx_dequantize(q, s, cols, out)
+    if status:
+        raise MoEError(status, "moe_mx_dequantize")
+
+
+def moe_mx_gemm(a, a_scale, a_cols: int, b, b_scale, b_cols: int, offsets, out, err=None):
+    status = (_fast or fast()).mx_gemm(a, a_scale, a_cols, b, b_scale, b_cols, offsets, out, err)
+    if status:
+        raise MoEError(status, "moe_mx_gemm")
 
 
 def moe_launch_count() -> int:

@@ -1,4 +1,5 @@
-"""Build libmoe.so (the CUDA path) in-tree with nvcc for sm_103a.
+"""Build libmoe.so (the CUDA path) in-tree with nvcc for sm_103a, and the
+Python module that calls its small operators (csrc/fastcall.c).
 
 Each translation unit under csrc/ compiles to an object in parallel; the
 objects link into sparse_moe_expert_02_gb300/_build/libmoe.so with the CUDA
@@ -11,6 +12,7 @@ import hashlib
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libmoe.so")
+FAST = os.path.join(BUILD, "_fastcall" + sysconfig.get_config_var("EXT_SUFFIX"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -35,7 +38,7 @@ def _sources():
 
 def _fingerprint(flags) -> str:
     h = hashlib.sha256()
-    for f in sorted(_sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
+    for f in sorted(_sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.c"))
                     + glob.glob(os.path.join(INCLUDE, "*.h"))):
         h.update(f.encode())
         with open(f, "rb") as fh:
@@ -50,7 +53,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
                     "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC] + list(extra_flags)
     fp = _fingerprint(flags)
     stamp = os.path.join(BUILD, "libmoe.stamp")
-    if not force and os.path.exists(LIB) and os.path.exists(stamp) and open(stamp).read() == fp:
+    if not force and os.path.exists(LIB) and os.path.exists(FAST) and os.path.exists(stamp) and open(stamp).read() == fp:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -67,9 +70,19 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout + r.stderr, flush=True)
         return obj
 
+    def fast():
+        tmp = FAST + f".tmp{os.getpid()}"
+        r = subprocess.run([cc, "-O2", "-shared", "-cudart", "none", "-Xcompiler", "-fPIC,-fvisibility=hidden", "-I", INCLUDE, "-I",
+                            sysconfig.get_paths()["include"], os.path.join(CSRC, "fastcall.c"), "-o", tmp], capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"fastcall.c failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, FAST)
+
     srcs = _sources()
     with ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+        small = ex.submit(fast)
         objs = list(ex.map(one, srcs))
+        small.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc] + ARCH + ["-shared", "-o", tmp] + objs + ["-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)

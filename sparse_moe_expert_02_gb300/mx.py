@@ -40,9 +40,11 @@ def quantize(x: torch.Tensor, out: MXTensor = None) -> MXTensor:
     """fp32 or bf16 x [..., rows, cols] (strided rows if 2-D) to 4 bits."""
     if out is None:
         out = empty(x.shape[:-1], x.shape[-1], x.device)
-    elif out.shape != tuple(x.shape):
-        raise ValueError(f"out holds {out.shape}, not {tuple(x.shape)}")
-    L.moe_mx_quantize(x if x.dim() == 2 else x.reshape(-1, x.shape[-1]), out.codes, out.scales)
+    if x.dim() != 2 or out.codes.dim() != 2:
+        if out.shape != tuple(x.shape):
+            raise ValueError(f"out holds {out.shape}, not {tuple(x.shape)}")
+        x = x.reshape(-1, x.shape[-1])
+    L.moe_mx_quantize(x, out.codes, out.scales, out.cols)
     return out
 
 
@@ -50,9 +52,12 @@ def dequantize(q: MXTensor, dtype: torch.dtype = torch.bfloat16, out: torch.Tens
     """The values of q, in out's type (dtype if out is None); exact in both."""
     if out is None:
         out = torch.empty(q.shape, dtype=dtype, device=q.codes.device)
-    elif tuple(out.shape) != q.shape:
-        raise ValueError(f"out: shape {q.shape}, not {tuple(out.shape)}")
-    L.moe_mx_dequantize(q.codes, q.scales, out if out.dim() == 2 else out.view(-1, out.shape[-1]))
+    flat = out
+    if out.dim() != 2 or q.codes.dim() != 2:
+        if tuple(out.shape) != q.shape:
+            raise ValueError(f"out: shape {q.shape}, not {tuple(out.shape)}")
+        flat = out.view(-1, out.shape[-1])
+    L.moe_mx_dequantize(q.codes, q.scales, q.cols, flat)
     return out
 
 
@@ -64,17 +69,7 @@ def matmul(a: MXTensor, b: MXTensor, offsets: torch.Tensor = None, out: torch.Te
     offsets[g+1]-1; rows of no group are left as they are in out.  err: int32
     [4], zeroed, receives a device error (see moe_mx_gemm).
     """
-    if len(a.shape) != 2 or len(b.shape) not in (2, 3) or a.cols != b.cols:
-        raise ValueError(f"matmul: a [rows, K] and b [N, K] or [G, N, K], not {a.shape} and {b.shape}")
-    if a.cols % 32:
-        raise ValueError("matmul: K must be a multiple of 32")
-    rows, N = a.shape[0], b.shape[-2]
-    G = b.shape[0] if len(b.shape) == 3 else 1
-    if offsets is not None and (offsets.dtype != torch.int32 or offsets.numel() != G + 1):
-        raise ValueError("matmul: offsets are int32 [G+1]")
     if out is None:
-        out = torch.empty((rows, N), dtype=out_dtype, device=a.codes.device)
-    elif tuple(out.shape) != (rows, N):
-        raise ValueError(f"out: shape {(rows, N)}, not {tuple(out.shape)}")
-    L.moe_mx_gemm(a.codes, a.scales, b.codes, b.scales, offsets, G, N, a.cols, out, err)
+        out = torch.empty((a.codes.shape[0], b.codes.shape[-2]), dtype=out_dtype, device=a.codes.device)
+    L.moe_mx_gemm(a.codes, a.scales, a.cols, b.codes, b.scales, b.cols, offsets, out, err)
     return out

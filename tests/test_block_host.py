@@ -6,9 +6,10 @@ import subprocess
 
 import numpy as np
 import pytest
+import torch
 
 import block_ref as R
-from sparse_moe_expert_02_gb300 import _lib as L
+from sparse_moe_expert_02_gb300 import _lib as L, mx, norm
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -102,3 +103,60 @@ def test_reference_quantiser_rounds_to_the_nearest_code():
     best = np.abs(x[..., None] / unit[..., None] - grid).min(-1)
     assert np.allclose(np.abs(x / unit - v / unit), best)
     assert np.array_equal(R.mx_values(*R.mx_quantize(v.astype(np.float32))), v)  # what is representable stays
+
+
+class Stub:
+    """What the operators read of a device tensor; the address is never used."""
+    is_cuda = True
+
+    def __init__(self, *shape, dtype=torch.float32, stride=None):
+        self.shape, self.dtype = torch.Size(shape), dtype
+        self.strides = stride or tuple(int(np.prod(shape[i + 1:])) for i in range(len(shape)))
+        self.device = torch.device("cpu")
+
+    def stride(self):
+        return self.strides
+
+    def dim(self):
+        return len(self.shape)
+
+    def is_contiguous(self):
+        return self.strides == tuple(int(np.prod(self.shape[i + 1:])) for i in range(len(self.shape)))
+
+    def data_ptr(self):
+        return 4096
+
+
+def stub_mx(*lead, cols=64):
+    t = object.__new__(mx.MXTensor)
+    nb = -(-cols // 32)
+    t.codes, t.scales, t.cols = Stub(*lead, 16 * nb, dtype=torch.uint8), Stub(*lead, nb, dtype=torch.uint8), cols
+    return t
+
+
+def test_operators_refuse_before_any_launch():
+    x, w = Stub(4, 64), Stub(64)
+    for bad in (lambda: norm.pre(torch.zeros(4, 64), out=x), lambda: norm.pre(x, out=Stub(4, 65)), lambda: norm.pre(x, out=Stub(5, 64)),
+                lambda: norm.pre(Stub(4, 64, dtype=torch.float16), out=x), lambda: norm.pre(Stub(4, 8, 8), out=x),
+                lambda: norm.pre(Stub(4, 64, stride=(128, 2)), out=x), lambda: norm.pre(x, Stub(63), out=x),
+                lambda: norm.pre(x, Stub(64, stride=(2,)), out=x), lambda: norm.pre(x, w, Stub(64, dtype=torch.bfloat16), out=x),
+                lambda: norm.pre(x, w, kind="max", out=x),
+                lambda: norm.post(x, Stub(3, 64), out=x), lambda: norm.post(x, x, out=Stub(4, 64, dtype=torch.bfloat16)),
+                lambda: norm.post(x, x, out=x, gate=Stub(4)), lambda: norm.post(x, x, out=x, gate=w, gate_by="token"),
+                lambda: norm.post(x, x, out=x, gate=Stub(4, 63), gate_by="full"), lambda: norm.post(x, x, out=x, gate=w, gate_by="row"),
+                lambda: norm.post(x, x, out=x, next_w=Stub(65), next_out=x), lambda: norm.post(x, x, out=x, next_out=Stub(4, 32)),
+                lambda: mx.quantize(x, out=stub_mx(4, cols=96)), lambda: mx.quantize(x, out=stub_mx(3)),
+                lambda: mx.quantize(Stub(4, 64, dtype=torch.int32), out=stub_mx(4)),
+                lambda: mx.quantize(Stub(2, 4, 64), out=stub_mx(4, 2)),
+                lambda: mx.dequantize(stub_mx(4), out=Stub(4, 65)), lambda: mx.dequantize(stub_mx(2, 2), out=Stub(4, 64)),
+                lambda: mx.matmul(stub_mx(4), stub_mx(8, cols=96), out=Stub(4, 8)), lambda: mx.matmul(stub_mx(4), stub_mx(8), out=Stub(4, 9)),
+                lambda: mx.matmul(stub_mx(4, cols=48), stub_mx(8, cols=48), out=Stub(4, 8)),
+                lambda: mx.matmul(stub_mx(2, 4), stub_mx(8), out=Stub(4, 8)), lambda: mx.matmul(stub_mx(4), stub_mx(1, 2, 8), out=Stub(4, 8)),
+                lambda: mx.matmul(stub_mx(4), stub_mx(2, 8), offsets=Stub(2, dtype=torch.int32), out=Stub(4, 8)),
+                lambda: mx.matmul(stub_mx(4), stub_mx(2, 8), offsets=Stub(3), out=Stub(4, 8))):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(TypeError):
+        L.fast().norm_pre(x, w)
+    with pytest.raises(AttributeError):
+        norm.pre(x, 3.0, out=x)
