@@ -15,9 +15,15 @@
 // bytes lie in memory; four warps read the scale bytes (two stages of a row a
 // load, a weight row and two rows a thread, two loads ahead), write them to
 // shared memory in that order, and the MMA thread copies them on with
-// tcgen05.cp ahead of their MMAs.  Six slots of scales (at most as many as stages), in
-// shared and in tensor memory: a slot's way from the MMAs that free it to
-// those that use it again takes some 1200 cycles.
+// tcgen05.cp ahead of their MMAs.  Six slots of scales (at most as many as
+// stages), in shared and in tensor memory: a slot's way from the MMAs that
+// free it to those that use it again takes some 1200 cycles.
+//
+// Measured: 8192 x 4096 x 4096 61 us (4.5 PFLOP/s; 35 at the peak clock, 43 at
+// the 1.62 GHz that the power limit leaves, the rest is the hand-over of
+// accumulators between tiles); 64 ragged groups of 4001 rows, 1024 x 4096
+// weights, 36 us (150 MB: 22 at the copy bandwidth); 7 rows, 4096 x 4096, 6.2
+// us, latency.
 //
 // 448 threads: warp 0 TMA, warp 1 tensor memory + MMA, warps 2-5 scales,
 // warps 6-13 epilogue (two per lane quarter, half of the tile's rows each).

@@ -6,10 +6,10 @@
 // the block's amax is two shuffles away, a lane's codes are one 32-bit word,
 // and a warp reads 512 bytes of bf16 and writes 128 bytes of codes in one
 // piece; a thread has two such units in flight (16384 x 4096 bf16, quantised
-// and read back: 62 us, 5.4 TB/s; with one 94, with four 64).  Rows that lie one after
-// the other are one long row, which saves a division per unit.  Other rows
-// (any alignment, a ragged last block): a warp takes a block, a column a
-// lane, so that its loads and stores stay in one piece all the same.
+// and read back: 62 us, 5.4 TB/s; with one 94, with four 64).  Rows that lie
+// one after the other are one long row, which saves a division per unit.
+// Other rows (any alignment, a ragged last block): a warp takes a block, a
+// column a lane, so that its loads and stores stay in one piece all the same.
 #include <algorithm>
 
 #include "common.cuh"

@@ -6,7 +6,7 @@
 //   post:   r' = res_scale * r + branch_scale * g * N(y)
 //           n' = N_next(r' as stored)
 //
-// A row is held in registers as fp32, 8 elements a thread, so that every
+// A row is held in registers as fp32, 8 or 16 elements a thread, so that every
 // tensor passes once: the statistics are sums over the registers (the
 // variance is taken about the mean, not from a sum of squares), and the next
 // norm reads r' before it leaves them, rounded as it is stored.
