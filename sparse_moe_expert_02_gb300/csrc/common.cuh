@@ -34,9 +34,11 @@ __device__ __forceinline__ void record_error(uint32_t* err, uint32_t code, uint3
 // waits here before touching anything the earlier kernels write, then lets
 // its own dependents start their prologue.  Without a programmatic
 // dependency both are no-ops.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait_then_release() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    pdl_wait();
+    pdl_release();
 }
 
 __device__ __forceinline__ uint64_t globaltimer_ns() {

@@ -22,7 +22,7 @@
 // Measured: 8192 x 4096 x 4096 61 us (4.5 PFLOP/s; 35 at the peak clock, 43 at
 // the 1.62 GHz that the power limit leaves, the rest is the hand-over of
 // accumulators between tiles); 64 ragged groups of 4001 rows, 1024 x 4096
-// weights, 36 us (150 MB: 22 at the copy bandwidth); 7 rows, 4096 x 4096, 6.2
+// weights, 36 us (150 MB: 22 at the copy bandwidth); 7 rows, 4096 x 4096, 5.7
 // us, latency.
 //
 // 448 threads: warp 0 TMA, warp 1 tensor memory + MMA, warps 2-5 scales,
@@ -237,6 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    pdl_wait();  // what an earlier kernel wrote
     if (p.offsets && warp == 2) {  // prefix of the groups' row tiles, 32 groups at a time
         int base = 0;
         for (int g0 = 0; g0 < p.G; g0 += 32) {
@@ -264,6 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    pdl_release();  // (once tensor memory is ours)
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     // Units of this CTA: u0, u0 + step, ...; k-blocks [kb0, kb1) of each.  Split: a cluster takes one
     // unit (or none: the grid covers a bound on their number).

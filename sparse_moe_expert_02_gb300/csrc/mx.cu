@@ -61,6 +61,7 @@ template <> struct Eight<float> {
 template <typename T>
 __global__ void __launch_bounds__(256) mx_quantize_kernel(const T* __restrict__ x, int64_t ld, int64_t n, int64_t per,
                                                           uint8_t* __restrict__ q, uint8_t* __restrict__ s) {
+    pdl_wait_then_release();
     const int64_t step = (int64_t)gridDim.x * blockDim.x;
     const bool flat = n == per;
     for (int64_t w0 = (int64_t)blockIdx.x * blockDim.x + (threadIdx.x & ~31); w0 < n; w0 += kUnroll * step) {
@@ -120,6 +121,7 @@ __global__ void __launch_bounds__(256) mx_swiglu_kernel(const float* __restrict_
 template <typename T>
 __global__ void __launch_bounds__(256) mx_quantize_any_kernel(const T* __restrict__ x, int64_t ld, int64_t n, int cols, int blocks,
                                                               uint8_t* __restrict__ q, uint8_t* __restrict__ s) {
+    pdl_wait_then_release();
     const int lane = threadIdx.x & 31;
     const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);
     for (int64_t b0 = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); b0 < n; b0 += kUnroll * step) {
@@ -150,6 +152,7 @@ __global__ void __launch_bounds__(256) mx_quantize_any_kernel(const T* __restric
 template <typename T>
 __global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ s, int64_t n,
                                                             int64_t per, T* __restrict__ out, int64_t ld) {
+    pdl_wait_then_release();
     const int64_t step = (int64_t)gridDim.x * blockDim.x;
     const bool flat = n == per;
     for (int64_t u0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; u0 < n; u0 += kUnroll * step) {
@@ -186,6 +189,7 @@ __global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* __res
 template <typename T>
 __global__ void __launch_bounds__(256) mx_dequantize_any_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ s, int64_t n,
                                                                 int cols, int blocks, T* __restrict__ out, int64_t ld) {
+    pdl_wait_then_release();
     const int lane = threadIdx.x & 31;
     const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);
     for (int64_t b0 = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); b0 < n; b0 += kUnroll * step) {
@@ -237,17 +241,18 @@ Shape shape_of(const void* p, int eb, int64_t ld, int64_t rows, int cols) {
 
 cudaError_t launch_mx_quantize(const void* x, int x_elem, int64_t ld, int64_t rows, int cols, uint8_t* q, uint8_t* s,
                                cudaStream_t stream) {
+    cudaError_t e;
     const Shape h = shape_of(x, x_elem == kF32 ? 4 : 2, ld, rows, cols);
     const int64_t n = rows * h.blocks;
     if (x_elem == kF32) {
-        if (h.vec) mx_quantize_kernel<float><<<h.grid, 256, 0, stream>>>((const float*)x, ld, h.units, h.per, q, s);
-        else mx_quantize_any_kernel<float><<<h.grid, 256, 0, stream>>>((const float*)x, ld, n, cols, h.blocks, q, s);
+        if (h.vec) e = launch_kernel(mx_quantize_kernel<float>, dim3(h.grid), dim3(256), 0, stream, 1, (const float*)x, ld, h.units, h.per, q, s);
+        else e = launch_kernel(mx_quantize_any_kernel<float>, dim3(h.grid), dim3(256), 0, stream, 1, (const float*)x, ld, n, cols, h.blocks, q, s);
     } else {
-        if (h.vec) mx_quantize_kernel<bf16><<<h.grid, 256, 0, stream>>>((const bf16*)x, ld, h.units, h.per, q, s);
-        else mx_quantize_any_kernel<bf16><<<h.grid, 256, 0, stream>>>((const bf16*)x, ld, n, cols, h.blocks, q, s);
+        if (h.vec) e = launch_kernel(mx_quantize_kernel<bf16>, dim3(h.grid), dim3(256), 0, stream, 1, (const bf16*)x, ld, h.units, h.per, q, s);
+        else e = launch_kernel(mx_quantize_any_kernel<bf16>, dim3(h.grid), dim3(256), 0, stream, 1, (const bf16*)x, ld, n, cols, h.blocks, q, s);
     }
     count_launches(1);
-    return cudaGetLastError();
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_mx_swiglu(const float* g, const float* u, int64_t n, uint8_t* q, uint8_t* s, cudaStream_t stream) {
@@ -258,17 +263,18 @@ cudaError_t launch_mx_swiglu(const float* g, const float* u, int64_t n, uint8_t*
 
 cudaError_t launch_mx_dequantize(const uint8_t* q, const uint8_t* s, int64_t rows, int cols, void* out, int out_elem,
                                  int64_t ld, cudaStream_t stream) {
+    cudaError_t e;
     const Shape h = shape_of(out, out_elem == kF32 ? 4 : 2, ld, rows, cols);
     const int64_t n = rows * h.blocks;
     if (out_elem == kF32) {
-        if (h.vec) mx_dequantize_kernel<float><<<h.grid, 256, 0, stream>>>(q, s, h.units, h.per, (float*)out, ld);
-        else mx_dequantize_any_kernel<float><<<h.grid, 256, 0, stream>>>(q, s, n, cols, h.blocks, (float*)out, ld);
+        if (h.vec) e = launch_kernel(mx_dequantize_kernel<float>, dim3(h.grid), dim3(256), 0, stream, 1, q, s, h.units, h.per, (float*)out, ld);
+        else e = launch_kernel(mx_dequantize_any_kernel<float>, dim3(h.grid), dim3(256), 0, stream, 1, q, s, n, cols, h.blocks, (float*)out, ld);
     } else {
-        if (h.vec) mx_dequantize_kernel<bf16><<<h.grid, 256, 0, stream>>>(q, s, h.units, h.per, (bf16*)out, ld);
-        else mx_dequantize_any_kernel<bf16><<<h.grid, 256, 0, stream>>>(q, s, n, cols, h.blocks, (bf16*)out, ld);
+        if (h.vec) e = launch_kernel(mx_dequantize_kernel<bf16>, dim3(h.grid), dim3(256), 0, stream, 1, q, s, h.units, h.per, (bf16*)out, ld);
+        else e = launch_kernel(mx_dequantize_any_kernel<bf16>, dim3(h.grid), dim3(256), 0, stream, 1, q, s, n, cols, h.blocks, (bf16*)out, ld);
     }
     count_launches(1);
-    return cudaGetLastError();
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace moe

@@ -152,6 +152,7 @@ __device__ __forceinline__ void normalise(float* v, const NormParams& n, int i, 
 template <int VEC, int PER, int MAXT, typename XT, typename OT>
 __global__ void __launch_bounds__(MAXT) norm_pre_kernel(const NormParams n, const XT* __restrict__ x, int64_t ld_x, int T,
                                                     int D, OT* __restrict__ out, int64_t ld_out, int nthr) {
+    pdl_wait_then_release();
     __shared__ float red[2][32];
     int turn = 0;
     constexpr int C = Row<VEC, PER>::kChunks;
@@ -214,6 +215,7 @@ __device__ __forceinline__ void post_row(const PostParams& p, int64_t t, int i, 
 template <int VEC, int PER, int MAXT, typename YT, typename RT, typename NT>
 __global__ void __launch_bounds__(MAXT) norm_post_kernel(const PostParams p, const YT* __restrict__ y, const RT* res, RT* out,
                                                      NT* __restrict__ next, int nthr) {
+    pdl_wait_then_release();
     __shared__ float red[2][32];
     int turn = 0;
     constexpr int C = Row<VEC, PER>::kChunks;
@@ -283,6 +285,7 @@ template <int PER, typename T> __device__ __forceinline__ void take_row(const ui
 template <int PER, int MAXT, typename YT, typename RT, typename NT>
 __global__ void __launch_bounds__(MAXT) norm_post_rows_kernel(const PostParams p, const YT* __restrict__ y, const RT* res, RT* out,
                                                                      NT* __restrict__ next) {
+    pdl_wait_then_release();
     extern __shared__ uint4 ring[];
     __shared__ float red[2][32];
     int turn = 0;
@@ -314,6 +317,7 @@ __global__ void __launch_bounds__(MAXT) norm_post_rows_kernel(const PostParams p
 template <int PER, int MAXT, typename XT, typename OT>
 __global__ void __launch_bounds__(MAXT) norm_pre_rows_kernel(const NormParams n, const XT* __restrict__ x, int64_t ld_x, int T, int D,
                                                                     OT* __restrict__ out, int64_t ld_out) {
+    pdl_wait_then_release();
     extern __shared__ uint4 ring[];
     __shared__ float red[2][32];
     int turn = 0;
@@ -380,11 +384,11 @@ cudaError_t launch_norm_pre(const NormParams& n, const void* x, int x_elem, int6
     do {                                                                                                         \
         if (many) {                                                                                              \
             if ((e = allow_smem(norm_pre_rows_kernel<PER, MAXT, XT, OT>, ring)) != cudaSuccess) return e;              \
-            norm_pre_rows_kernel<PER, MAXT, XT, OT><<<many, nthr, ring, stream>>>(n, (const XT*)x, ld_x, T, D, (OT*)out, ld_out); \
+            e = launch_kernel(norm_pre_rows_kernel<PER, MAXT, XT, OT>, dim3(many), dim3(nthr), ring, stream, 1, n, (const XT*)x, ld_x, T, D, (OT*)out, ld_out); \
         } else if (vec) {                                                                                        \
-            norm_pre_kernel<8, PER, MAXT, XT, OT><<<grid, block, 0, stream>>>(n, (const XT*)x, ld_x, T, D, (OT*)out, ld_out, nthr); \
+            e = launch_kernel(norm_pre_kernel<8, PER, MAXT, XT, OT>, dim3(grid), dim3(block), 0, stream, 1, n, (const XT*)x, ld_x, T, D, (OT*)out, ld_out, nthr); \
         } else {                                                                                                 \
-            norm_pre_kernel<1, PER, MAXT, XT, OT><<<grid, block, 0, stream>>>(n, (const XT*)x, ld_x, T, D, (OT*)out, ld_out, nthr); \
+            e = launch_kernel(norm_pre_kernel<1, PER, MAXT, XT, OT>, dim3(grid), dim3(block), 0, stream, 1, n, (const XT*)x, ld_x, T, D, (OT*)out, ld_out, nthr); \
         }                                                                                                        \
     } while (0)
 #define MOE_PRE(XT, OT)                          \
@@ -403,7 +407,7 @@ cudaError_t launch_norm_pre(const NormParams& n, const void* x, int x_elem, int6
 #undef MOE_PRE
 #undef MOE_PRE_P
     count_launches(1);
-    return cudaGetLastError();
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_norm_post(const PostParams& p, cudaStream_t stream) {
@@ -422,13 +426,13 @@ cudaError_t launch_norm_post(const PostParams& p, cudaStream_t stream) {
     do {                                                                                                         \
         if (many) {                                                                                              \
             if ((e = allow_smem(norm_post_rows_kernel<PER, MAXT, YT, RT, NT>, ring)) != cudaSuccess) return e;         \
-            norm_post_rows_kernel<PER, MAXT, YT, RT, NT><<<many, nthr, ring, stream>>>(p, (const YT*)p.y, (const RT*)p.res, \
+            e = launch_kernel(norm_post_rows_kernel<PER, MAXT, YT, RT, NT>, dim3(many), dim3(nthr), ring, stream, 1, p, (const YT*)p.y, (const RT*)p.res, \
                                                                                  (RT*)p.out, (NT*)p.next_out);   \
         } else if (vec) {                                                                                        \
-            norm_post_kernel<8, PER, MAXT, YT, RT, NT><<<grid, block, 0, stream>>>(p, (const YT*)p.y, (const RT*)p.res, (RT*)p.out, \
+            e = launch_kernel(norm_post_kernel<8, PER, MAXT, YT, RT, NT>, dim3(grid), dim3(block), 0, stream, 1, p, (const YT*)p.y, (const RT*)p.res, (RT*)p.out, \
                                                                              (NT*)p.next_out, nthr);             \
         } else {                                                                                                 \
-            norm_post_kernel<1, PER, MAXT, YT, RT, NT><<<grid, block, 0, stream>>>(p, (const YT*)p.y, (const RT*)p.res, (RT*)p.out, \
+            e = launch_kernel(norm_post_kernel<1, PER, MAXT, YT, RT, NT>, dim3(grid), dim3(block), 0, stream, 1, p, (const YT*)p.y, (const RT*)p.res, (RT*)p.out, \
                                                                              (NT*)p.next_out, nthr);             \
         }                                                                                                        \
     } while (0)
@@ -454,7 +458,7 @@ cudaError_t launch_norm_post(const PostParams& p, cudaStream_t stream) {
 #undef MOE_POST
 #undef MOE_POST_P
     count_launches(1);
-    return cudaGetLastError();
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace moe

@@ -309,6 +309,25 @@ def test_mx_refusals():
         mx.matmul(a, b)  # several groups, no offsets
 
 
+def test_operators_in_a_row_see_each_other():
+    # each call reads what the one before wrote and overwrites what the one before read
+    def chain(r, w, b, wait):
+        x, z, q = torch.empty_like(r), torch.empty_like(r), mx.empty(r.shape[0], r.shape[1])
+        for _ in range(20):
+            for step in (lambda: norm.pre(r, w, out=x), lambda: mx.quantize(x, out=q), lambda: mx.matmul(q, b, out=z),
+                         lambda: norm.post(z, r, w, res_scale=0.5, out=r, next_w=w, next_out=x), lambda: mx.quantize(x, out=q),
+                         lambda: mx.dequantize(q, out=z), lambda: norm.post(z, r, None, kind="none", branch_scale=0.25, out=r)):
+                step()
+                if wait:
+                    torch.cuda.synchronize()
+        return r
+
+    for rows, D in ((1, 512), (7, 1024), (200, 2048)):
+        b, _ = random_mx((D, D), 21)
+        r, w = rand(rows, D, seed=22).to(BF16), rand(D, seed=23).to(BF16)
+        assert torch.equal(chain(r.clone(), w, b, False), chain(r.clone(), w, b, True))
+
+
 # ------------------------------------------------- the layer for few tokens
 
 TOL = {"f32": 1e-4, "bf16": 1e-2, "fp8": 5e-2, "mxfp4": 5e-2}
