@@ -159,15 +159,15 @@ __device__ __forceinline__ Unit unit_at(const MxGemm& p, const Plan& q, int u, i
 template <int VEC> __device__ __forceinline__ uint4 load_scales(const uint8_t* row, int b0, int blocks) {
     uint32_t w[4] = {0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu};
     if constexpr (VEC == 16) {
-        return b0 < blocks ? __ldg((const uint4*)(row + b0)) : make_uint4(w[0], w[1], w[2], w[3]);
+        return b0 < blocks ? *(const uint4*)(row + b0) : make_uint4(w[0], w[1], w[2], w[3]);
     } else if constexpr (VEC == 4) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (b0 + 4 * j < blocks) w[j] = __ldg((const uint32_t*)(row + b0 + 4 * j));
+            if (b0 + 4 * j < blocks) w[j] = *(const uint32_t*)(row + b0 + 4 * j);
     } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            if (b0 + i < blocks) w[i / 4] = (w[i / 4] & ~(255u << (8 * (i & 3)))) | (uint32_t)__ldg(row + b0 + i) << (8 * (i & 3));
+            if (b0 + i < blocks) w[i / 4] = (w[i / 4] & ~(255u << (8 * (i & 3)))) | (uint32_t)row[b0 + i] << (8 * (i & 3));
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int g = g0 + lane;
             int n = 0;
             if (g < p.G) {
-                const int lo = min(max(__ldg(p.offsets + g), 0), p.rows), hi = min(max(__ldg(p.offsets + g + 1), lo), p.rows);
+                const int lo = min(max(p.offsets[g], 0), p.rows), hi = min(max(p.offsets[g + 1], lo), p.rows);
                 n = (hi - lo + pl.tile_rows - 1) / pl.tile_rows;
                 pre[kMaxG + 1 + g] = lo;
             }
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0) {
             pre[p.G] = base;
-            pre[kMaxG + 1 + p.G] = min(max(__ldg(p.offsets + p.G), 0), p.rows);
+            pre[kMaxG + 1 + p.G] = min(max(p.offsets[p.G], 0), p.rows);
         }
     }
     tc_fence_before();

@@ -19,6 +19,9 @@
 namespace moe {
 namespace {
 
+// Loads go past L1 (each byte is read once) and not through the read-only path:
+// the kernels start while the one before them, which may write what they read,
+// ends (common.cuh, programmatic dependent launch).
 constexpr int kUnroll = 2;
 
 // Eight columns as they lie in memory: their largest magnitude's bits, and
@@ -26,7 +29,7 @@ constexpr int kUnroll = 2;
 template <typename T> struct Eight;
 template <> struct Eight<bf16> {
     uint4 q;
-    __device__ __forceinline__ void load(const bf16* p) { q = __ldg((const uint4*)p); }
+    __device__ __forceinline__ void load(const bf16* p) { q = __ldcg((const uint4*)p); }
     __device__ __forceinline__ uint32_t amax() const {  // two at a time, as 16-bit integers: NaNs count
         const uint32_t m = __vmaxu2(__vmaxu2(q.x & 0x7FFF7FFFu, q.y & 0x7FFF7FFFu), __vmaxu2(q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu));
         return max(m << 16, m & 0xFFFF0000u);
@@ -42,8 +45,8 @@ template <> struct Eight<bf16> {
 template <> struct Eight<float> {
     float4 a, b;
     __device__ __forceinline__ void load(const float* p) {
-        a = __ldg((const float4*)p);
-        b = __ldg((const float4*)p + 1);
+        a = __ldcg((const float4*)p);
+        b = __ldcg((const float4*)p + 1);
     }
     __device__ __forceinline__ uint32_t amax() const {
         const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -133,7 +136,7 @@ __global__ void __launch_bounds__(256) mx_quantize_any_kernel(const T* __restric
             if (b < n) {
                 const int64_t row = b / blocks;
                 const int col = (int)(b - row * blocks) * kMxBlock + lane;
-                if (col < cols) v[j] = to_f32(__ldg(x + row * ld + col));
+                if (col < cols) v[j] = to_f32(__ldcg(x + row * ld + col));
             }
         }
 #pragma unroll
@@ -150,7 +153,7 @@ __global__ void __launch_bounds__(256) mx_quantize_any_kernel(const T* __restric
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ s, int64_t n,
+__global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* __restrict__ q, const uint8_t* s, int64_t n,
                                                             int64_t per, T* __restrict__ out, int64_t ld) {
     pdl_wait_then_release();
     const int64_t step = (int64_t)gridDim.x * blockDim.x;
@@ -160,8 +163,8 @@ __global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* __res
 #pragma unroll
         for (int j = 0; j < kUnroll; ++j) {
             const int64_t u = min(u0 + j * step, n - 1);
-            w[j] = __ldg((const uint32_t*)(q + u * 4));
-            sb[j] = __ldg(s + (u >> 2));
+            w[j] = __ldcg((const uint32_t*)(q + u * 4));
+            sb[j] = s[u >> 2];  // by way of L1: four warps share a sector
         }
 #pragma unroll
         for (int j = 0; j < kUnroll; ++j) {
@@ -198,8 +201,8 @@ __global__ void __launch_bounds__(256) mx_dequantize_any_kernel(const uint8_t* _
         for (int j = 0; j < kUnroll; ++j) {
             const int64_t b = b0 + j * step;
             if (b < n) {
-                w[j] = __ldg(q + b * 16 + (lane >> 1));
-                sb[j] = __ldg(s + b);
+                w[j] = __ldcg(q + b * 16 + (lane >> 1));
+                sb[j] = __ldcg(s + b);
             }
         }
 #pragma unroll

@@ -21,7 +21,7 @@ namespace {
 constexpr int kMaxThreads = 1024;
 
 __device__ __forceinline__ float load_p(const void* p, int is_bf16, int64_t i) {
-    return is_bf16 ? __bfloat162float(__ldg((const bf16*)p + i)) : __ldg((const float*)p + i);
+    return is_bf16 ? __bfloat162float(((const bf16*)p)[i]) : ((const float*)p)[i];
 }
 
 // Row access, VEC elements at a time.  VEC = 8: 16-byte accesses (two for
@@ -41,15 +41,22 @@ __device__ __forceinline__ void unpack8(const uint4& q, float* v) {
         v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
 }
-template <int VEC, typename T> __device__ __forceinline__ void load_vec(const T* p, float* v) {
+// KEEP: by way of L1, for what other rows read too.  Not through the read-only
+// path in either case: these kernels start while the one before them, which may
+// write what they read, ends (common.cuh, programmatic dependent launch).
+template <bool KEEP, typename T> __device__ __forceinline__ T load(const T* p) {
+    if constexpr (KEEP) return *p;
+    else return __ldcg(p);
+}
+template <int VEC, bool KEEP = false, typename T> __device__ __forceinline__ void load_vec(const T* p, float* v) {
     if constexpr (VEC == 1) {
-        v[0] = to_f32(__ldg(p));
+        v[0] = to_f32(load<KEEP>(p));
     } else if constexpr (sizeof(T) == 2) {
-        unpack8(__ldg((const uint4*)p), v);
+        unpack8(load<KEEP>((const uint4*)p), v);
     } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const float4 q = __ldg((const float4*)p + h);
+            const float4 q = load<KEEP>((const float4*)p + h);
             v[4 * h] = q.x; v[4 * h + 1] = q.y; v[4 * h + 2] = q.z; v[4 * h + 3] = q.w;
         }
     }
@@ -81,8 +88,8 @@ template <int VEC, typename T> __device__ __forceinline__ void store_vec(T* p, f
 }
 // VEC values of a parameter vector (w, b, a per-channel gate), either type.
 template <int VEC> __device__ __forceinline__ void load_par(const void* p, int is_bf16, int64_t i, float* v) {
-    if (is_bf16) load_vec<VEC>((const bf16*)p + i, v);
-    else load_vec<VEC>((const float*)p + i, v);
+    if (is_bf16) load_vec<VEC, true>((const bf16*)p + i, v);
+    else load_vec<VEC, true>((const float*)p + i, v);
 }
 
 // Sum over the nthr threads of a row (nthr = 32, or the whole block).  turn
