@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(MAXT) norm_post_kernel(const PostParams p, con
 // (cp.async: the copies are the thread's own, so nothing but the sums waits
 // for other threads).  Without it a block has its loads in flight only until
 // its first sum: 8192 x 4096 bf16 with gate and next norm 69.9 us; with it
-// 60.6 (4.4 TB/s).
+// 59.6 (4.5 TB/s).
 constexpr int kAhead = 2;  // rows in flight (three: 65.4 us, fewer blocks fit)
 
 __device__ __forceinline__ void copy16(void* dst, const void* src) {
