@@ -227,7 +227,7 @@ typedef struct moe_ws_layout {
                           Written by the permutation, and only where the split can run: bf16
                           layer, T*top_k >= 64*E (see MOE_FLAG_SPLIT_GEMM_OFF) */
     size_t gu;         /* MXFP4: f32 [2, R, I] gate and up products */
-    size_t few;        /* moe_forward_few, T <= MOE_FEW_MAX: f32 [T*(top_k+1), I] activations h */
+    size_t few;        /* moe_forward_few: f32 [min(T, MOE_FEW_MAX)*(top_k+1), I] activations h */
 } moe_ws_layout;
 
 /* Validate a configuration and build a host-side plan for `device`.
@@ -240,7 +240,8 @@ MOE_API moe_status moe_plan_create(const moe_config* cfg, int device, moe_plan**
 MOE_API void moe_plan_destroy(moe_plan* plan);
 MOE_API const moe_config* moe_plan_config(const moe_plan* plan);
 
-/* Workspace layout / size for T tokens (1 <= T <= T_max). */
+/* Workspace layout / size for T tokens (1 <= T <= T_max).  The size never
+ * shrinks as T grows: a workspace for T tokens serves every smaller T. */
 MOE_API moe_status moe_workspace_layout(const moe_plan* plan, int32_t T, moe_ws_layout* out);
 MOE_API moe_status moe_workspace_size(const moe_plan* plan, int32_t T, size_t* bytes);
 

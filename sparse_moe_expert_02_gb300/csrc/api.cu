@@ -121,11 +121,14 @@ int route_splits(const moe_config& c, int T, int num_sms) {
     return c.dtype == MOE_F32 ? 1 : moe::router_splits(T, c.E, c.D, num_sms);
 }
 
+// total never shrinks as T grows: a workspace sized for T_max is what callers
+// use for every smaller T.  Parts that a larger T needs less of (hist,
+// logits_part, few) therefore take what the smaller T's need of them.
 void layout(const moe_config& c, int num_sms, int T, moe_ws_layout* L) {
     const int64_t TK = (int64_t)T * c.top_k, R = TK + T;
     const bool fp8 = c.dtype == MOE_FP8_E4M3_B128;
     const int ab = act_bytes(c.dtype);
-    const int64_t nch = moe::cdiv(TK, moe::perm_chunk(TK));
+    const int64_t nch = moe::perm_chunks_most(TK);
     size_t o = 0;
     auto take = [&](size_t bytes) { size_t at = o; o += up256(bytes); return at; };
     memset(L, 0, sizeof(*L));
@@ -156,12 +159,13 @@ void layout(const moe_config& c, int num_sms, int T, moe_ws_layout* L) {
     // y: fp16 for the bf16 layer, bf16 for the FP8 layer, else fp32 (a bf16 y
     // in the bf16 layer would cost about 1.3e-2 of the output rms).
     L->y = take((size_t)R * c.D * (y_elem(c) == moe::kF32 ? 4 : 2));
-    const int S = route_splits(c, T, num_sms);
-    L->logits_part = S > 1 ? take((size_t)S * T * c.E * 4) : 0;
+    const int64_t part_rows = c.dtype == MOE_F32 ? 0 : moe::router_part_rows(T, c.E, c.D, num_sms);
+    const size_t part = part_rows ? take((size_t)part_rows * c.E * 4) : 0;
+    L->logits_part = route_splits(c, T, num_sms) > 1 ? part : 0;
     L->tiles2 = take((size_t)(c.E + 2) * 4);
     L->pairs = take((size_t)(3 * (c.E + 2) + 2) * 4);
     L->gu = mx ? take((size_t)2 * R * c.I * 4) : 0;
-    L->few = T <= moe::kFewMax ? take((size_t)R * c.I * 4) : 0;
+    L->few = take((size_t)std::min(T, moe::kFewMax) * (c.top_k + 1) * c.I * 4);
     L->total = o;
 }
 

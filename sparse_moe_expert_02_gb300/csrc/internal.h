@@ -16,7 +16,13 @@ constexpr int kPermChunk = 1024;   // (t, j) pairs per permute chunk (largest si
 // Pairs per permute chunk for T*k pairs: 128 up to 16384 pairs (more, shorter
 // chunks: the ranking walk is one warp per chunk), 1024 beyond (fewer
 // per-chunk histograms for the scan to walk).
-__host__ __device__ constexpr int perm_chunk(int64_t TK) { return TK <= 16384 ? 128 : kPermChunk; }
+constexpr int64_t kPermShort = 16384;
+__host__ __device__ constexpr int perm_chunk(int64_t TK) { return TK <= kPermShort ? 128 : kPermChunk; }
+// The most chunks that any number of pairs up to TK has.
+constexpr int64_t perm_chunks_most(int64_t TK) {
+    const int64_t mine = (TK + perm_chunk(TK) - 1) / perm_chunk(TK);
+    return TK > kPermShort && mine < kPermShort / 128 ? kPermShort / 128 : mine;
+}
 
 // Element kinds of the GEMM operands.
 enum Elem : int { kF32 = 0, kBF16 = 1, kE4M3 = 2, kF16 = 3 };
@@ -161,6 +167,7 @@ bool gemm_fp8_supported(const GroupedGemm& g);
 cudaError_t launch_topk(const float* part, int S, const float* bias, float* logits_out, int T, int E, int k,
                         int32_t* blob, uint32_t* err, cudaStream_t stream, int32_t* hist = nullptr, int chunk = 1);
 int router_splits(int T, int E, int D, int num_sms);
+int64_t router_part_rows(int T, int E, int D, int num_sms);  // rows of partial logits that T tokens or fewer need at most
 cudaError_t launch_pack_words(const int32_t* blob, int64_t TK, int32_t* words, cudaStream_t stream);
 
 // tiles2 (nullable): exclusive prefix of ceil(counts/256), the row-tile

@@ -226,4 +226,14 @@ int router_splits(int T, int E, int D, int num_sms) {
     return S;
 }
 
+// S slices hold at most num_sms / S units, so up to a last T; the largest S * T'
+// over T' <= T is at that last T of some S, or at T itself.
+int64_t router_part_rows(int T, int E, int D, int num_sms) {
+    const int per = std::max(1, E / 256), kblocks = D / 64;
+    int64_t rows = 0;
+    for (int S = 2; S <= 8 && kblocks % S == 0; S *= 2)
+        rows = std::max(rows, S * std::min<int64_t>(T, 128LL * (num_sms / S / per)));
+    return rows;
+}
+
 }  // namespace moe
