@@ -264,7 +264,15 @@ static PyObject* mx_gemm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
             return NULL;
         }
     }
-    if (a[8] != Py_None && read_tensor(a[8], "err", &err, 0) < 0) return NULL;
+    if (a[8] != Py_None) {
+        if (read_tensor(a[8], "err", &err, 0) < 0) return NULL;
+        int64_t m = 1;
+        for (int i = 0; i < err.dims; ++i) m *= err.size[i];
+        if (err.type != t_i32 || m < 4) { /* the kernel writes four words */
+            fail("err", "int32 [4]");
+            return NULL;
+        }
+    }
     if (read_rows(a[7], "out", &out, NULL) < 0) return NULL;
     if (out.size[0] != rows || out.size[1] != N) {
         PyErr_Format(PyExc_ValueError, "out: shape (%lld, %lld), not (%lld, %lld)", (long long)rows, (long long)N, (long long)out.size[0],

@@ -67,7 +67,8 @@ def matmul(a: MXTensor, b: MXTensor, offsets: torch.Tensor = None, out: torch.Te
 
     offsets: int32 [G+1] on the device, group g's rows are offsets[g] ..
     offsets[g+1]-1; rows of no group are left as they are in out.  err: int32
-    [4], zeroed, receives a device error (see moe_mx_gemm).
+    [4], zeroed, receives a device error (see moe_mx_gemm); without it, an
+    output left incomplete by a wait that ran out goes unreported.
     """
     if out is None:
         out = torch.empty((a.codes.shape[0], b.codes.shape[-2]), dtype=out_dtype, device=a.codes.device)
