@@ -5,7 +5,10 @@
  * after another, so the caller's time counts: reading the tensors and calling
  * through ctypes took 10.7 us for a post-norm with everything (a launch itself
  * is 2 us), here 5.3 us (quantise 5.6 to 3.3, 4-bit product 9.5 to 5.4).
- * Nothing is kept from one call to the next.
+ * Nothing is kept from one call to the next.  The call itself runs without the
+ * interpreter lock, as through ctypes: a launch waits while the stream's queue
+ * is full, for as long as what is queued takes, and a host function queued
+ * there may need the lock.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -144,6 +147,15 @@ static int count(Py_ssize_t n, Py_ssize_t want) {
     return -1;
 }
 
+#define CALL(call)                  \
+    do {                            \
+        moe_status st;              \
+        Py_BEGIN_ALLOW_THREADS      \
+        st = call;                  \
+        Py_END_ALLOW_THREADS        \
+        return PyLong_FromLong(st); \
+    } while (0)
+
 /* x, w, b, kind, eps, w_offset, out */
 static PyObject* norm_pre(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     Tensor x, out;
@@ -152,7 +164,7 @@ static PyObject* norm_pre(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     if (count(n, 7) < 0 || read_rows(a[0], "x", &x, NULL) < 0 || read_rows(a[6], "out", &out, &x) < 0 ||
         read_norm(&m, a[3], a[4], a[5], a[1], a[2], x.size[1]) < 0 || read_stream(&s) < 0)
         return NULL;
-    return PyLong_FromLong(p_norm_pre(&m, x.p, x.dtype, x.stride[0], (int32_t)x.size[0], (int32_t)x.size[1], out.p, out.dtype, out.stride[0], s));
+    CALL(p_norm_pre(&m, x.p, x.dtype, x.stride[0], (int32_t)x.size[0], (int32_t)x.size[1], out.p, out.dtype, out.stride[0], s));
 }
 
 /* y, res, out, next_out | kind, eps, w_offset, w, b | next_kind, next_w, next_b | res_scale, branch_scale |
@@ -189,8 +201,8 @@ static PyObject* norm_post(PyObject* self, PyObject* const* a, Py_ssize_t n) {
         p.gate_dtype = g.dtype;
     }
     if (read_stream(&s) < 0) return NULL;
-    return PyLong_FromLong(p_norm_post(&p, y.p, y.dtype, y.stride[0], res.p, res.dtype, res.stride[0], (int32_t)T, (int32_t)D, out.p,
-                                       out.stride[0], next.p, next.dtype, next.stride[0], s));
+    CALL(p_norm_post(&p, y.p, y.dtype, y.stride[0], res.p, res.dtype, res.stride[0], (int32_t)T, (int32_t)D, out.p,
+                     out.stride[0], next.p, next.dtype, next.stride[0], s));
 }
 
 /* Codes and scales that hold `cols` columns; *rows: of all leading dimensions. */
@@ -224,7 +236,7 @@ static PyObject* mx_quantize(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     if (count(n, 4) < 0 || read_rows(a[0], "x", &x, NULL) < 0 || read_mx(a[1], a[2], a[3], "out", &q, &sc, &rows, &cols) < 0 ||
         held(&x, rows, cols, "out") < 0 || read_stream(&s) < 0)
         return NULL;
-    return PyLong_FromLong(p_quantize(x.p, x.dtype, x.stride[0], rows, (int32_t)cols, (uint8_t*)q.p, (uint8_t*)sc.p, s));
+    CALL(p_quantize(x.p, x.dtype, x.stride[0], rows, (int32_t)cols, (uint8_t*)q.p, (uint8_t*)sc.p, s));
 }
 
 /* codes, scales, cols, out */
@@ -235,7 +247,7 @@ static PyObject* mx_dequantize(PyObject* self, PyObject* const* a, Py_ssize_t n)
     if (count(n, 4) < 0 || read_mx(a[0], a[1], a[2], "q", &q, &sc, &rows, &cols) < 0 || read_rows(a[3], "out", &out, NULL) < 0 ||
         held(&out, rows, cols, "q") < 0 || read_stream(&s) < 0)
         return NULL;
-    return PyLong_FromLong(p_dequantize((const uint8_t*)q.p, (const uint8_t*)sc.p, rows, (int32_t)cols, out.p, out.dtype, out.stride[0], s));
+    CALL(p_dequantize((const uint8_t*)q.p, (const uint8_t*)sc.p, rows, (int32_t)cols, out.p, out.dtype, out.stride[0], s));
 }
 
 /* a codes, scales, cols | b codes, scales, cols | offsets, out, err */
@@ -284,8 +296,8 @@ static PyObject* mx_gemm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
         return NULL;
     }
     if (read_stream(&s) < 0) return NULL;
-    return PyLong_FromLong(p_gemm((const uint8_t*)qa.p, (const uint8_t*)sa.p, (const uint8_t*)qb.p, (const uint8_t*)sb.p, (const int32_t*)off.p,
-                                  (int32_t)rows, (int32_t)G, (int32_t)N, (int32_t)K, out.p, out.dtype, out.stride[0], (uint32_t*)err.p, s));
+    CALL(p_gemm((const uint8_t*)qa.p, (const uint8_t*)sa.p, (const uint8_t*)qb.p, (const uint8_t*)sb.p, (const int32_t*)off.p,
+                (int32_t)rows, (int32_t)G, (int32_t)N, (int32_t)K, out.p, out.dtype, out.stride[0], (uint32_t*)err.p, s));
 }
 
 /* init(types (fp32, bf16, uint8, int32), current device, raw stream of a device, addresses of the five entry points) */

@@ -1,8 +1,16 @@
 """How Python reaches the block operators: what the C module refuses and how it
 calls the library."""
+import ctypes
+import importlib.util
+import os
+import shutil
+import subprocess
+import sysconfig
+
 import pytest
 import torch
 
+from sparse_moe_expert_02_gb300 import build as B
 from sparse_moe_expert_02_gb300 import mx
 from test_block_host import Stub, stub_mx
 
@@ -22,3 +30,25 @@ def test_product_takes_an_error_word():
     assert torch.equal(mx.matmul(a, b, err=word[:4]), mx.matmul(a, b))
     mx.matmul(a, b, err=word)
     assert not word.any()
+
+
+def test_the_interpreter_lock_is_free_while_the_library_runs(tmp_path):
+    # entry points that report whether they were called with the lock, behind a copy of the module
+    fakes = tmp_path / "fakes.c"
+    fakes.write_text("#include <Python.h>\nint probe(void) { return PyGILState_Check() ? 99 : 0; }\n")
+    so = tmp_path / "fakes.so"
+    subprocess.run(["gcc", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], str(fakes), "-o", str(so)], check=True)
+    address = ctypes.cast(ctypes.CDLL(str(so)).probe, ctypes.c_void_p).value
+    B.build()
+    copy = tmp_path / os.path.basename(B.FAST)
+    shutil.copy(B.FAST, copy)
+    spec = importlib.util.spec_from_file_location("_fastcall", copy)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    m.init((torch.float32, torch.bfloat16, torch.uint8, torch.int32), lambda: 0, lambda device: 0, (address,) * 5)
+    x, q, b = Stub(4, 64), stub_mx(4), stub_mx(8)
+    assert m.norm_pre(x, None, None, 1, 1e-6, 0.0, x) == 0
+    assert m.norm_post(x, x, x, None, 1, 1e-6, 0.0, None, None, 0, None, None, 1.0, 1.0, 0, None, False) == 0
+    assert m.mx_quantize(x, q.codes, q.scales, 64) == 0
+    assert m.mx_dequantize(q.codes, q.scales, 64, x) == 0
+    assert m.mx_gemm(q.codes, q.scales, 64, b.codes, b.scales, 64, None, Stub(4, 8), None) == 0
