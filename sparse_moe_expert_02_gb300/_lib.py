@@ -308,6 +308,9 @@ def fast():
     global _fast
     if _fast is None:
         L = lib()
+        if not os.path.exists(_build.FAST):
+            raise RuntimeError("the norms and the 4-bit operators are reached through a C module, which needs Python's headers "
+                               "(Python.h) to be built; the layer itself does not")
         spec = importlib.util.spec_from_file_location("_fastcall", _build.FAST)
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)

@@ -32,6 +32,12 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libmoe")
 
 
+def python_headers():
+    """The folder of Python.h, or None: libmoe does without, only the small operators' module needs it."""
+    inc = sysconfig.get_paths()["include"]
+    return inc if os.path.exists(os.path.join(inc, "Python.h")) else None
+
+
 def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
@@ -53,7 +59,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
                     "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC] + list(extra_flags)
     fp = _fingerprint(flags)
     stamp = os.path.join(BUILD, "libmoe.stamp")
-    if not force and os.path.exists(LIB) and os.path.exists(FAST) and os.path.exists(stamp) and open(stamp).read() == fp:
+    headers = python_headers()
+    if not force and os.path.exists(LIB) and (os.path.exists(FAST) or not headers) and os.path.exists(stamp) and open(stamp).read() == fp:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -71,9 +78,13 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     def fast():
+        if not headers:
+            if os.path.exists(FAST):
+                os.remove(FAST)  # of other sources
+            return
         tmp = FAST + f".tmp{os.getpid()}"
         r = subprocess.run([cc, "-O2", "-shared", "-cudart", "none", "-Xcompiler", "-fPIC,-fvisibility=hidden", "-I", INCLUDE, "-I",
-                            sysconfig.get_paths()["include"], os.path.join(CSRC, "fastcall.c"), "-o", tmp], capture_output=True, text=True)
+                            headers, os.path.join(CSRC, "fastcall.c"), "-o", tmp], capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"fastcall.c failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, FAST)

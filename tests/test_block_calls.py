@@ -10,6 +10,7 @@ import sysconfig
 import pytest
 import torch
 
+from sparse_moe_expert_02_gb300 import _lib as L
 from sparse_moe_expert_02_gb300 import build as B
 from sparse_moe_expert_02_gb300 import mx
 from test_block_host import Stub, stub_mx
@@ -52,3 +53,29 @@ def test_the_interpreter_lock_is_free_while_the_library_runs(tmp_path):
     assert m.mx_quantize(x, q.codes, q.scales, 64) == 0
     assert m.mx_dequantize(q.codes, q.scales, 64, x) == 0
     assert m.mx_gemm(q.codes, q.scales, 64, b.codes, b.scales, 64, None, Stub(4, 8), None) == 0
+
+
+def test_the_library_builds_where_python_has_no_headers(tmp_path, monkeypatch):
+    L.lib()  # the real one
+    cc = tmp_path / "nvcc"  # makes the file after -o
+    cc.write_text('#!/bin/sh\nwhile [ $# -gt 1 ]; do [ "$1" = -o ] && echo made > "$2"; shift; done\n')
+    cc.chmod(0o755)
+    monkeypatch.setenv("NVCC", str(cc))
+    for name in ("BUILD", "LIB", "FAST"):
+        monkeypatch.setattr(B, name, str(tmp_path / "b" / os.path.basename(getattr(B, name)) if name != "BUILD" else tmp_path / "b"))
+    paths = dict(sysconfig.get_paths(), include=str(tmp_path))
+    with monkeypatch.context() as m:
+        m.setattr(B.sysconfig, "get_paths", lambda: paths)
+        # a compiler that finds no Python.h
+        cc.write_text('#!/bin/sh\ncase "$*" in *fastcall.c*) exit 1;; esac\n' + cc.read_text().split("\n", 1)[1])
+        assert B.build() == B.LIB and os.path.exists(B.LIB) and not os.path.exists(B.FAST)
+        os.utime(B.LIB, (1, 1))
+        B.build()
+        assert os.stat(B.LIB).st_mtime == 1  # nothing to do
+        m.setattr(L, "_fast", None)
+        with pytest.raises(RuntimeError, match="Python.h"):
+            mx.quantize(Stub(4, 64), out=stub_mx(4))
+    if B.python_headers():  # then the module is made, although the library is up to date
+        cc.write_text(cc.read_text().replace("exit 1", ":"))
+        B.build()
+        assert os.path.exists(B.FAST)
