@@ -375,8 +375,9 @@ MOE_API moe_status moe_selftest_wait_timeout(const moe_plan* plan, void* ws, siz
  * 1 <= T <= MOE_FEW_MAX (T = 0: MOE_OK) without its permutation, in fewer
  * launches, each chosen expert's weights read once.  Same arguments and same
  * errors; the results are within the layer type's tolerance of
- * moe_forward's, not bit-identical.  Takes every moe_dtype.  Uses
- * the workspace parts logits, blob and few; workspaces are made ready once by
+ * moe_forward's, not bit-identical.  Takes every moe_dtype; rows too wide for
+ * an SM's shared memory (MOE_F32 with D of 43136 or more) run as moe_forward.
+ * Uses the workspace parts logits, blob and few; workspaces are made ready once by
  * moe_workspace_init (or by an earlier moe_forward). */
 #define MOE_FEW_MAX 16
 MOE_API moe_status moe_forward_few(const moe_plan* plan, const moe_weights* w, const void* x, int32_t T, void* out,

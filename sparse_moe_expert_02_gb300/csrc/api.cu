@@ -963,6 +963,8 @@ moe_status moe_forward_few(const moe_plan* p, const moe_weights* w, const void* 
     if ((blob_out && !aligned(blob_out, 16)) || (logits_out && !aligned(logits_out, 16)))
         return arg_fail(MOE_ERR_INVALID_ARG, "blob_out or logits_out misaligned");
     const moe_config& c = p->cfg;
+    const int down_f16 = f16_down(c) && w->w_down_f16;
+    if (!moe::few_fits(c.dtype, down_f16, c.D, c.I, c.top_k)) return moe_forward(p, w, x, T, out, blob_out, logits_out, ws, ws_bytes, stream);
     moe::FewParams f = {};
     f.T = T;
     f.D = c.D;
@@ -976,7 +978,7 @@ moe_status moe_forward_few(const moe_plan* p, const moe_weights* w, const void* 
     f.b_router = c.has_router_bias ? w->b_router : nullptr;
     f.w_gate = w->w_gate;
     f.w_up = w->w_up;
-    f.down_f16 = f16_down(c) && w->w_down_f16;
+    f.down_f16 = down_f16;
     f.w_down = f.down_f16 ? w->w_down_f16 : w->w_down;
     f.s_gate = w->s_gate;
     f.s_up = w->s_up;

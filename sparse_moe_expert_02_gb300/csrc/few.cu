@@ -1468,6 +1468,19 @@ template <int W> cudaError_t launch_chunks(const FewParams& p, int num_sms, cuda
 
 }  // namespace few
 
+// One token fits: its x and a ring of four stages in an SM's shared memory
+// (all that a plan takes but fp32 rows of 43136 columns and more).
+bool few_fits(int dtype, int down_f16, int D, int I, int k) {
+    int hcap, ring_at, stages;
+    switch (dtype) {
+        case MOE_F32: return few::plan_smem<MOE_F32, 1>(1, D, I, k, &hcap, &ring_at, &stages);
+        case MOE_BF16:
+            return (down_f16 ? few::plan_smem<MOE_BF16, 1> : few::plan_smem<few::W_HILO, 1>)(1, D, I, k, &hcap, &ring_at, &stages);
+        case MOE_FP8_E4M3_B128: return few::plan_smem<MOE_FP8_E4M3_B128, 1>(1, D, I, k, &hcap, &ring_at, &stages);
+        default: return few::plan_smem<MOE_MXFP4, 1>(1, D, I, k, &hcap, &ring_at, &stages);
+    }
+}
+
 cudaError_t launch_few(const FewParams& p, int num_sms, cudaStream_t s) {
     switch (p.dtype) {
         case MOE_F32: return few::launch_chunks<MOE_F32>(p, num_sms, s);

@@ -280,6 +280,7 @@ struct FewParams {
     // set by the launcher: a chunk of the tokens, its place in the blob, the shared-memory plan
     int tok0, plane, hcap, ring_at, stages, tma_scales;
 };
+bool few_fits(int dtype, int down_f16, int D, int I, int k);
 cudaError_t launch_few(const FewParams& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_selftest_timeout(uint32_t* err, int64_t limit_ns, cudaStream_t stream);
 
