@@ -73,10 +73,13 @@ __device__ __forceinline__ float e4m3_to_f32(uint8_t q) {
 }
 
 // SiLU(a) * u in fp32: a * u / (1 + e^-a), with the hardware exponential
-// and the fast (reciprocal-based) division: a few ulp of fp32, far below the
-// fp16 / E4M3 rounding of h that follows.  For a < -88, e^-a is infinite
-// and the quotient is 0, SiLU's limit.
+// and the fast (reciprocal-based) division: a few ulp of fp32 about zero, some
+// 20 at a = -60, far below the rounding to fewer bits that follows for h but
+// in moe_forward's fp32 layer.  For a < -88, e^-a is infinite and the quotient
+// is 0, SiLU's limit.
 __device__ __forceinline__ float swiglu(float a, float u) { return __fdividef(a * u, 1.0f + __expf(-a)); }
+// The same where h stays in fp32: within 4 ulp everywhere.
+__device__ __forceinline__ float swiglu_f32(float a, float u) { return a * u / (1.0f + expf(-a)); }
 
 __host__ __device__ constexpr int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 

@@ -1037,7 +1037,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             for (int s = 0; s < 2; ++s) {
                 const int t = 8 * u + 2 * q + s;
                 if (t < T && ((tokens >> t) & 1u))
-                    put_h((int64_t)(row + __popc(tokens & ((1u << t) - 1u))) * I + f0 + rw, swiglu(acc[u][s], acc[u][2 + s]));
+                    put_h((int64_t)(row + __popc(tokens & ((1u << t) - 1u))) * I + f0 + rw,
+                          W == MOE_F32 ? swiglu_f32(acc[u][s], acc[u][2 + s]) : swiglu(acc[u][s], acc[u][2 + s]));
             }
     };
     // the warps' sums of token tile u, in warp order
