@@ -373,8 +373,9 @@ MOE_API moe_status moe_selftest_wait_timeout(const moe_plan* plan, void* ws, siz
 
 /* The whole layer for a few tokens: the arithmetic of moe_forward for
  * 1 <= T <= MOE_FEW_MAX (T = 0: MOE_OK) without its permutation, in fewer
- * launches, each chosen expert's weights read once.  Same arguments and same
- * errors; the results are within the layer type's tolerance of
+ * launches, each chosen expert's weights read once a launch.  Faster than
+ * moe_forward for one token to some ten, by the layer's size and type.  Same
+ * arguments and same errors; the results are within the layer type's tolerance of
  * moe_forward's, not bit-identical.  Takes every moe_dtype; rows too wide for
  * an SM's shared memory (MOE_F32 with D of 43136 or more) run as moe_forward.
  * Uses the workspace parts logits, blob and few; workspaces are made ready once by

@@ -1,7 +1,7 @@
 """MoEBlock: the MoE half of a decoder block at serving time.
 
     n   = N_pre(r)                      (once, at the start of the stack)
-    y   = layer(n)                      (few tokens: one moe_forward_few call)
+    y   = layer(n)                      (where it is the faster: one moe_forward_few call)
     r'  = res_scale * r + branch_scale * gate * N_post(y)
     n'  = N_next(r')                    (fused with the line above)
 
@@ -12,7 +12,6 @@ from __future__ import annotations
 
 import torch
 
-from . import _lib as L
 from . import norm
 from .layer import MoELayer
 
@@ -39,6 +38,6 @@ class MoEBlock:
         T = r.shape[0]
         if n is None:
             n = norm.pre(r, out=torch.empty(r.shape, dtype=self.in_dtype, device=r.device), **self.pre_args)
-        y = self.layer.forward_few(n) if T <= L.MOE_FEW_MAX else self.layer.forward(n)
+        y = self.layer.forward_few(n) if self.layer.few_pays(T) else self.layer.forward(n)
         nxt = torch.empty(r.shape, dtype=self.in_dtype, device=r.device) if next_norm else None
         return norm.post(y, r, next_norm=next_norm, next_out=nxt, gate=self.gate if gate is None else gate, **self.post_args)

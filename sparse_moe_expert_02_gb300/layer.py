@@ -90,12 +90,33 @@ class MoELayer:
         return out
 
     def forward_few(self, x: torch.Tensor, out: torch.Tensor = None, blob_out=None, logits_out=None) -> torch.Tensor:
-        """forward() for at most MOE_FEW_MAX tokens, without the permutation: one moe_forward_few call."""
+        """forward() for at most MOE_FEW_MAX tokens, without the permutation: one moe_forward_few call (few_pays: where
+        it is the faster)."""
         T = x.shape[0]
         if out is None:
             out = self.new_out(T)
         L.moe_forward_few(self.plan, self.cw, x, T, out, blob_out, logits_out, self.ws)
         return out
+
+    def few_pays(self, T: int) -> bool:
+        """Whether forward_few is the faster of the two for T tokens.
+
+        It saves the other's dozen launches and its permutation, but each SM
+        multiplies with mma.sync, so that from some amount of work on the
+        tensor memory's products win: T (top_k + 1) 3 D I multiply-adds.
+        Measured where the two cross (us a call, few against forward; D 4096,
+        I 1024, top 10 of 128 unless said; profiles/few_or_forward.md):
+        bf16 T 12 359 | 365, T 14 375 | 369, D 7168 I 2048 top 8 T 4 388 | 436,
+        T 8 671 | 632.  FP8 T 8 167 | 186, T 10 199 | 197, T 16 298 | 236.
+        4 bits T 8 142 | 149, T 9 190 | 154 (two launches above eight tokens:
+        there D 1024 I 512 top 8 is the limit, T 12 71 | 72, T 14 78 | 73).
+        fp32, on the CUDA cores in both, T 16 2171 | 7825.
+        """
+        if T > L.MOE_FEW_MAX:
+            return False
+        work = T * (self.top_k + 1) * 3 * self.D * self.I
+        limit = {"bf16": 1.7e9, "fp8": 1.2e9, "mxfp4": 1.2e9 if T <= 8 else 1.7e8}.get(self.dtype)
+        return limit is None or work <= limit
 
     def route(self, x):
         L.moe_route(self.plan, self.cw, x, x.shape[0], self.ws)

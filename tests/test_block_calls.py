@@ -12,7 +12,7 @@ import torch
 
 from sparse_moe_expert_02_gb300 import _lib as L
 from sparse_moe_expert_02_gb300 import build as B
-from sparse_moe_expert_02_gb300 import mx
+from sparse_moe_expert_02_gb300 import MoELayer, mx
 from test_block_host import Stub, stub_mx
 
 
@@ -79,3 +79,18 @@ def test_the_library_builds_where_python_has_no_headers(tmp_path, monkeypatch):
         cc.write_text(cc.read_text().replace("exit 1", ":"))
         B.build()
         assert os.path.exists(B.FAST)
+
+
+def test_few_tokens_go_to_the_faster_kernel():
+    def pays(dtype, T, D=4096, I=1024, k=10):
+        layer = object.__new__(MoELayer)
+        layer.dtype, layer.D, layer.I, layer.top_k, layer.plan = dtype, D, I, k, None
+        return layer.few_pays(T)
+
+    for dtype in ("f32", "bf16", "fp8", "mxfp4"):
+        assert pays(dtype, 1) and pays(dtype, 1, 7168, 2048, 8) and pays(dtype, 16, 512, 256, 4) and not pays(dtype, 17, 512, 256, 4)
+    # both sides as measured
+    assert pays("bf16", 12) and not pays("bf16", 16) and pays("bf16", 4, 7168, 2048, 8) and not pays("bf16", 8, 7168, 2048, 8)
+    assert pays("fp8", 8) and not pays("fp8", 12) and not pays("fp8", 8, 7168, 2048, 8)
+    assert pays("mxfp4", 8) and not pays("mxfp4", 9) and not pays("mxfp4", 16, 2048, 768, 8) and not pays("mxfp4", 8, 7168, 2048, 8)
+    assert pays("f32", 16) and pays("f32", 16, 7168, 2048, 8)

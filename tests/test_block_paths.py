@@ -179,3 +179,13 @@ def test_few_layer_of_wide_rows(dtype, D, T):
         layer.check()
     assert e.value.status == L.MOE_ERR_NONFINITE
     assert rel_max_err(f64(got[:T - 1]), f64(out[:T - 1])) <= 1e-5
+
+
+def test_block_takes_the_layer_that_pays():
+    shape, inp, layer = few_case("mxfp4", 16, 1024, 32, 512, 10, None, out_dtype="bf16")
+    block = MoEBlock(layer)
+    for T in (4, 16):
+        r = rand(T, 1024, seed=T, dtype=BF16)
+        n = norm.pre(r)
+        y = layer.forward_few(n) if T == 4 else layer.forward(n)
+        assert torch.equal(block.forward(r, next_norm=False)[0], norm.post(y, r)[0])
