@@ -189,3 +189,48 @@ def test_block_takes_the_layer_that_pays():
         n = norm.pre(r)
         y = layer.forward_few(n) if T == 4 else layer.forward(n)
         assert torch.equal(block.forward(r, next_norm=False)[0], norm.post(y, r)[0])
+
+
+# ------------------------------------------------------- graphs and streams
+
+@pytest.mark.parametrize("rows,D", [(1, 512), (7, 1024), (301, 1023), (2000, 2048)])
+def test_operators_captured_with_copies_and_a_second_stream(rows, D):
+    # launches, copies, memsets and an event's wait between the operators, eagerly and as a graph replayed on new inputs
+    K = D // 32 * 32
+    b, _ = random_mx((D, K), 21)
+    w = rand(D, seed=23)
+    r, x, z = (torch.empty(rows, D, device="cuda") for _ in range(3))
+    side_out, back = torch.empty(rows, D, dtype=BF16, device="cuda"), torch.empty(rows, K, dtype=BF16, device="cuda")
+    q = mx.empty(rows, K)
+    side, done = torch.cuda.Stream(), torch.cuda.Event()
+
+    def step():
+        main = torch.cuda.current_stream()
+        norm.pre(r, w, out=x)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            norm.pre(x, w, kind="layer", out=side_out)
+            done.record()
+        mx.quantize(x[:, :K], out=q)
+        z.zero_()
+        mx.matmul(q, b, out=z)
+        mx.dequantize(q, out=back)
+        main.wait_event(done)
+        norm.post(z, r, w, gate=side_out, gate_by="full", res_scale=0.5, out=r)
+        x.copy_(r)
+        norm.post(x, r, None, kind="none", branch_scale=0.25, out=r)
+
+    inputs = [rand(rows, D, seed=30 + i) for i in range(3)]
+    want = []
+    for v in inputs:
+        r.copy_(v)
+        step()
+        want.append((r.clone(), back.clone(), side_out.clone()))
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        step()
+    for v, (a, c, d) in zip(inputs, want):
+        r.copy_(v)
+        g.replay()
+        assert torch.equal(r, a) and torch.equal(back, c) and torch.equal(side_out, d)
