@@ -234,3 +234,20 @@ def test_operators_captured_with_copies_and_a_second_stream(rows, D):
         r.copy_(v)
         g.replay()
         assert torch.equal(r, a) and torch.equal(back, c) and torch.equal(side_out, d)
+
+
+def test_few_fp32_sums_are_no_single_chain():
+    # h = silu(8) * up . x of 4096 random terms.  A chain of n fp32 additions is off by some 2.5e-8 sqrt(n/2) of the sum
+    # (rms; half an ulp uniformly, partial sums growing): 1.1e-6 for one of 4096, 2e-7 for one of 128 blocks of 32,
+    # whose own chains are of far smaller sums; silu adds 1.2e-7.  Between the two: 5e-7
+    T, D, I = 3, 4096, 512
+    x = rand(T, D, seed=1)
+    x[:, 0] = 8
+    gate, up = torch.zeros(2, I, D, device="cuda"), rand(2, I, D, seed=2)
+    gate[:, :, 0], up[:, :, 0] = 1, 0
+    layer = MoELayer(D, 1, I, 1, "f32", {"w_router": rand(1, D, seed=3), "w_gate": gate, "w_up": up, "w_down": rand(2, D, I, seed=4)}, T_max=T)
+    layer.forward_few(x)
+    layer.check()
+    h = f64(layer.ws_view(T, "few", F32, (2 * T, I)))
+    ref = 8 / (1 + np.exp(-8.0)) * np.concatenate([f64(x) @ f64(up[e]).T for e in (0, 1)])
+    assert np.sqrt(np.mean((h - ref) ** 2) / np.mean(ref ** 2)) <= 5e-7
