@@ -243,45 +243,32 @@ __global__ void __launch_bounds__(MAXT) norm_post_kernel(const PostParams p, con
     post_row<VEC, PER>(p, t, i, nthr, v, r, out, next, red, turn);
 }
 
-// Many rows: a block takes row after row, and each thread copies its own
-// elements of the next rows into shared memory while it works on this one
+// Many rows of bf16: a block takes row after row, and each thread copies its
+// own elements of the next rows into shared memory while it works on this one
 // (cp.async: the copies are the thread's own, so nothing but the sums waits
 // for other threads).  Without it a block has its loads in flight only until
-// its first sum: 8192 x 4096 bf16 with gate and next norm 69.9 us; with it
-// 59.6 (4.5 TB/s).
+// its first sum: 8192 x 4096 with gate and next norm 69.3 us; with it 58.4
+// (4.6 TB/s).  Rows of fp32 do without: a lane's eight elements are two pieces
+// of a 32-byte sector then, fetched by two copies, and 8192 x 4096 fp32 took
+// 157 us with the ring, 105 without (pre 79 and 43).
 constexpr int kAhead = 2;  // rows in flight (three: 65.4 us, fewer blocks fit)
 
 __device__ __forceinline__ void copy16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
 }
 // This thread's elements of a row: 16-byte pieces [piece][thread].
-template <int PER, typename T> __device__ __forceinline__ void copy_row(uint4* dst, const T* row, int i, int nthr, int D) {
-    constexpr int P = (int)sizeof(T) / 2;  // pieces of eight elements
+template <int PER> __device__ __forceinline__ void copy_row(uint4* dst, const bf16* row, int i, int nthr, int D) {
 #pragma unroll
     for (int c = 0; c < PER / 8; ++c) {
         const int col = (c * nthr + i) * 8;
-        if (col < D) {
-#pragma unroll
-            for (int h = 0; h < P; ++h) copy16(dst + (c * P + h) * nthr, (const uint4*)(row + col) + h);
-        }
+        if (col < D) copy16(dst + c * nthr, row + col);
     }
 }
-template <int PER, typename T> __device__ __forceinline__ void take_row(const uint4* src, float* v, int i, int nthr, int D) {
-    constexpr int P = (int)sizeof(T) / 2;
+template <int PER> __device__ __forceinline__ void take_row(const uint4* src, float* v, int i, int nthr, int D) {
 #pragma unroll
     for (int c = 0; c < PER / 8; ++c) {
         if ((c * nthr + i) * 8 < D) {
-#pragma unroll
-            for (int h = 0; h < P; ++h) {
-                const uint4 q = src[(c * P + h) * nthr];
-                if constexpr (P == 1) {
-                    unpack8(q, v + c * 8);
-                } else {
-                    const float* e = (const float*)&q;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) v[c * 8 + h * 4 + k] = e[k];
-                }
-            }
+            unpack8(src[c * nthr], v + c * 8);
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[c * 8 + k] = 0.0f;
@@ -289,21 +276,20 @@ template <int PER, typename T> __device__ __forceinline__ void take_row(const ui
     }
 }
 
-template <int PER, int MAXT, typename YT, typename RT, typename NT>
-__global__ void __launch_bounds__(MAXT) norm_post_rows_kernel(const PostParams p, const YT* __restrict__ y, const RT* res, RT* out,
-                                                                     NT* __restrict__ next) {
+template <int PER, int MAXT, typename NT>
+__global__ void __launch_bounds__(MAXT) norm_post_rows_kernel(const PostParams p, const bf16* __restrict__ y, const bf16* res, bf16* out,
+                                                              NT* __restrict__ next) {
     pdl_wait_then_release();
     extern __shared__ uint4 ring[];
     __shared__ float red[2][32];
     int turn = 0;
     const int nthr = blockDim.x, i = threadIdx.x;
-    constexpr int kY = PER * (int)sizeof(YT) / 16, kR = PER * (int)sizeof(RT) / 16;  // 16-byte pieces a thread's elements take
-    const int row_pieces = (kY + kR) * nthr;
+    const int half = PER / 8 * nthr;  // 16-byte pieces of a row
     auto start = [&](int64_t t, int slot) {
         if (t < p.T) {
-            uint4* dst = ring + slot * row_pieces + i;
+            uint4* dst = ring + 2 * slot * half + i;
             copy_row<PER>(dst, y + t * p.ld_y, i, nthr, p.D);
-            copy_row<PER>(dst + kY * nthr, res + t * p.ld_res, i, nthr, p.D);
+            copy_row<PER>(dst + half, res + t * p.ld_res, i, nthr, p.D);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -313,23 +299,23 @@ __global__ void __launch_bounds__(MAXT) norm_post_rows_kernel(const PostParams p
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
         float v[PER], r[PER];
-        take_row<PER, YT>(ring + slot * row_pieces + i, v, i, nthr, p.D);
-        take_row<PER, RT>(ring + slot * row_pieces + kY * nthr + i, r, i, nthr, p.D);
+        take_row<PER>(ring + 2 * slot * half + i, v, i, nthr, p.D);
+        take_row<PER>(ring + (2 * slot + 1) * half + i, r, i, nthr, p.D);
         start(t + (int64_t)kAhead * gridDim.x, slot);
         if (++slot == kAhead) slot = 0;
         post_row<8, PER>(p, t, i, nthr, v, r, out, next, red, turn);
     }
 }
 
-template <int PER, int MAXT, typename XT, typename OT>
-__global__ void __launch_bounds__(MAXT) norm_pre_rows_kernel(const NormParams n, const XT* __restrict__ x, int64_t ld_x, int T, int D,
-                                                                    OT* __restrict__ out, int64_t ld_out) {
+template <int PER, int MAXT, typename OT>
+__global__ void __launch_bounds__(MAXT) norm_pre_rows_kernel(const NormParams n, const bf16* __restrict__ x, int64_t ld_x, int T, int D,
+                                                             OT* __restrict__ out, int64_t ld_out) {
     pdl_wait_then_release();
     extern __shared__ uint4 ring[];
     __shared__ float red[2][32];
     int turn = 0;
     const int nthr = blockDim.x, i = threadIdx.x;
-    const int row_pieces = PER * (int)sizeof(XT) / 16 * nthr;
+    const int row_pieces = PER / 8 * nthr;
     auto start = [&](int64_t t, int slot) {
         if (t < T) copy_row<PER>(ring + slot * row_pieces + i, x + t * ld_x, i, nthr, D);
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -340,7 +326,7 @@ __global__ void __launch_bounds__(MAXT) norm_pre_rows_kernel(const NormParams n,
     for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
         float v[PER];
-        take_row<PER, XT>(ring + slot * row_pieces + i, v, i, nthr, D);
+        take_row<PER>(ring + slot * row_pieces + i, v, i, nthr, D);
         start(t + (int64_t)kAhead * gridDim.x, slot);
         if (++slot == kAhead) slot = 0;
         normalise<8, PER>(v, n, i, nthr, D, red, turn);
@@ -352,8 +338,8 @@ __global__ void __launch_bounds__(MAXT) norm_pre_rows_kernel(const NormParams n,
     }
 }
 
-// Elements of a thread: eight (one token: 3.8 us against 4.6 with sixteen),
-// or sixteen where the rows alone fill the GPU and a thread's fixed work (two
+// Elements of a thread: eight (one token, before programmatic launches: 3.8 us
+// against 4.6 with sixteen), or sixteen where the rows alone fill the GPU and a thread's fixed work (two
 // sums) counts, or where eight would need more than 1024 threads.
 int row_per(int T, int D) { return D > 8 * kMaxThreads || (T >= 608 && D >= 1024) ? 16 : 8; }
 // Threads of a row: a whole number of warps.
@@ -364,9 +350,9 @@ bool vec_ok(const void* p, int64_t ld, int bytes) {
 }
 bool par_ok(const NormParams& n) { return vec_ok(n.w, 0, 1) && vec_ok(n.b, 0, 1); }
 
-// The row-after-row kernels: shared memory of a block and the grid, or 0
-// where they do not apply: rows of one warp, too few rows for every block to
-// have several, or rows too long for the ring.
+// The row-after-row kernels' grid, or 0 where they do not apply: rows of one
+// warp, too few rows for every block to have several, or rows too long for the
+// ring (above 14336 columns after a block).
 int rows_grid(int T, int nthr, int ring_bytes) {
     constexpr int kSms = 152, kSmem = 226 * 1024;
     if (nthr < 64 || ring_bytes > kSmem / 2) return 0;
@@ -385,13 +371,13 @@ cudaError_t launch_norm_pre(const NormParams& n, const void* x, int x_elem, int6
     const dim3 grid((unsigned)cdiv(T, rows)), block(nthr * rows);
     const bool vec = D % 8 == 0 && vec_ok(x, ld_x, x_elem == kF32 ? 4 : 2) &&
                      vec_ok(out, ld_out, out_elem == kF32 ? 4 : 2) && par_ok(n);
-    const int ring = kAhead * nthr * per * (x_elem == kF32 ? 4 : 2), many = vec ? rows_grid(T, nthr, ring) : 0;
+    const int ring = kAhead * nthr * per * 2, many = vec && x_elem == kBF16 ? rows_grid(T, nthr, ring) : 0;
     cudaError_t e = cudaSuccess;
 #define MOE_PRE_P(PER, MAXT, XT, OT)                                                                                   \
     do {                                                                                                         \
         if (many) {                                                                                              \
-            if ((e = allow_smem(norm_pre_rows_kernel<PER, MAXT, XT, OT>, ring)) != cudaSuccess) return e;              \
-            e = launch_kernel(norm_pre_rows_kernel<PER, MAXT, XT, OT>, dim3(many), dim3(nthr), ring, stream, 1, n, (const XT*)x, ld_x, T, D, (OT*)out, ld_out); \
+            if ((e = allow_smem(norm_pre_rows_kernel<PER, MAXT, OT>, ring)) != cudaSuccess) return e;            \
+            e = launch_kernel(norm_pre_rows_kernel<PER, MAXT, OT>, dim3(many), dim3(nthr), ring, stream, 1, n, (const bf16*)x, ld_x, T, D, (OT*)out, ld_out); \
         } else if (vec) {                                                                                        \
             e = launch_kernel(norm_pre_kernel<8, PER, MAXT, XT, OT>, dim3(grid), dim3(block), 0, stream, 1, n, (const XT*)x, ld_x, T, D, (OT*)out, ld_out, nthr); \
         } else {                                                                                                 \
@@ -427,14 +413,16 @@ cudaError_t launch_norm_post(const PostParams& p, cudaStream_t stream) {
                      (!has_next || vec_ok(p.next_out, p.ld_next, bytes(p.n_elem))) &&
                      (p.gate_by == MOE_GATE_NONE || p.gate_by == MOE_GATE_TOKEN ||
                       vec_ok(p.gate, p.gate_by == MOE_GATE_FULL ? p.ld_gate : 0, p.gate_bf16 ? 2 : 4));
-    const int ring = kAhead * nthr * per * (bytes(p.y_elem) + bytes(p.r_elem)), many = vec ? rows_grid(p.T, nthr, ring) : 0;
+    // (8192 x 512 with gate and next norm: 13.4 us row after row, 10.9 not; 16384 x 1024: 30.8 and 34.1)
+    const bool rows_pay = p.y_elem == kBF16 && p.r_elem == kBF16 && p.D >= 1024;
+    const int ring = kAhead * nthr * per * 4, many = vec && rows_pay ? rows_grid(p.T, nthr, ring) : 0;
     cudaError_t e = cudaSuccess;
 #define MOE_POST_P(PER, MAXT, YT, RT, NT)                                                                              \
     do {                                                                                                         \
         if (many) {                                                                                              \
-            if ((e = allow_smem(norm_post_rows_kernel<PER, MAXT, YT, RT, NT>, ring)) != cudaSuccess) return e;         \
-            e = launch_kernel(norm_post_rows_kernel<PER, MAXT, YT, RT, NT>, dim3(many), dim3(nthr), ring, stream, 1, p, (const YT*)p.y, (const RT*)p.res, \
-                                                                                 (RT*)p.out, (NT*)p.next_out);   \
+            if ((e = allow_smem(norm_post_rows_kernel<PER, MAXT, NT>, ring)) != cudaSuccess) return e;           \
+            e = launch_kernel(norm_post_rows_kernel<PER, MAXT, NT>, dim3(many), dim3(nthr), ring, stream, 1, p, (const bf16*)p.y, (const bf16*)p.res, \
+                                                                                 (bf16*)p.out, (NT*)p.next_out); \
         } else if (vec) {                                                                                        \
             e = launch_kernel(norm_post_kernel<8, PER, MAXT, YT, RT, NT>, dim3(grid), dim3(block), 0, stream, 1, p, (const YT*)p.y, (const RT*)p.res, (RT*)p.out, \
                                                                              (NT*)p.next_out, nthr);             \

@@ -65,14 +65,15 @@ def test_block_takes_a_gate_by_call_and_biases(gate_by):
 
 # ------------------------------------------------------------ long prompts
 
-# Row counts from which the norms go row after row (a block takes at least three): 456 times the blocks an SM holds.
+# Row counts from which a block of bf16 takes row after row (three at least): 456 times the blocks an SM holds.
 LONG_POST = [(4777, 520, BF16, BF16, BF16), (2001, 4096, BF16, BF16, BF16), (1500, 4104, F32, F32, BF16), (7301, 1024, BF16, F32, F32),
-             (3003, 2056, F32, BF16, BF16), (900, 8192, F32, F32, F32)]
+             (3003, 2056, F32, BF16, BF16), (900, 8192, F32, F32, F32), (7301, 1032, BF16, BF16, F32), (1000, 8192, BF16, BF16, BF16),
+             (500, 14336, BF16, BF16, BF16)]
 
 
 @pytest.mark.parametrize("kind", ["rms", "layer"])
 @pytest.mark.parametrize("T,D,xt,ot", [(4777, 520, F32, F32), (2900, 4096, BF16, BF16), (1537, 4104, F32, BF16), (500, 16384, BF16, F32),
-                                       (9200, 1024, BF16, BF16)])
+                                       (9200, 1024, BF16, BF16), (5001, 520, BF16, F32), (1900, 4104, BF16, BF16)])
 def test_norm_pre_of_a_long_prompt(kind, T, D, xt, ot):
     wide = rand(T, D + 16, seed=1, dtype=xt, std=3)
     x, w, b = wide[:, 8:8 + D], rand(D, seed=2), rand(D, seed=3)
