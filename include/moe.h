@@ -110,7 +110,8 @@ typedef enum moe_status {
 typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3_B128 = 2, MOE_MXFP4 = 3 } moe_dtype;
 
 /* moe_config.flags */
-#define MOE_FLAG_FORCE_SIMT 0x1u   /* expert GEMMs on the CUDA-core kernel (cross-check path) */
+#define MOE_FLAG_FORCE_SIMT 0x1u   /* expert GEMMs on the CUDA-core kernel (cross-check path; MOE_FP8_E4M3_B128
+                                      and MOE_MXFP4 have none, and moe_forward_few is one kernel in any case) */
 #define MOE_FLAG_PAIR_CTA_OFF 0x2u /* bf16 expert GEMMs never on CTA pairs (the default) */
 #define MOE_FLAG_PAIR_CTA_ON 0x4u  /* bf16 expert GEMMs on CTA pairs (cta_group::2, 256-row tiles; a
                                       group's ragged last tile runs transposed unless

@@ -16,9 +16,10 @@
 // by instructions.)  tcgen05 would want 128 rows and its operands in its own
 // layout; at HBM speed mma.sync is far from its limit.
 //
-// Measured (D = 4096, I = 1024, top_k = 10, weights from HBM): T = 1 bf16 58.0
+// Measured (D = 4096, I = 1024, top_k = 10, weights from HBM): T = 1 bf16 58.3
 // us, 4.8 TB/s of weights over the whole call, 6 in P2 and 5.2 in P3; 4 bits
-// 34.4 us; T = 8 FP8 112 us, 5.1 TB/s.  What is left is 9 to 12 us until the
+// 34.9 us; T = 8 FP8 112 us, 5.1 TB/s.  From some ten tokens on moe_forward is
+// the faster (MoELayer.few_pays).  What is left is 9 to 12 us until the
 // list of experts stands (launch, router, barrier, top-k: a chain of
 // latencies), 3 us from the last gate/up tile to the first down product, and
 // code that is read from memory on its first use: the kernel runs each line

@@ -19,11 +19,13 @@
 // stages), in shared and in tensor memory: a slot's way from the MMAs that
 // free it to those that use it again takes some 1200 cycles.
 //
-// Measured: 8192 x 4096 x 4096 61 us (4.5 PFLOP/s; 35 at the peak clock, 43 at
-// the 1.62 GHz that the power limit leaves, the rest is the hand-over of
-// accumulators between tiles); 64 ragged groups of 4001 rows, 1024 x 4096
-// weights, 36 us (150 MB: 22 at the copy bandwidth); 7 rows, 4096 x 4096, 5.7
-// us, latency.
+// Measured: 8192 x 4096 x 4096 61 us (4.5 PFLOP/s) under the power limit.  Of
+// the MMA warp's 106,000 cycles (seven tiles; the mean is 6.7) 37,000 are waits
+// for a stage's operands and scales, 5,000 for an accumulator, the rest issue,
+// with 57,000 the MMAs' own.  64 ragged groups of 4001 rows, 1024 x 4096
+// weights, 36 us (150 MB: 22 at the copy bandwidth): 18,000 of 51,000 cycles
+// are waits for stages, and the CTAs with five units instead of four take
+// 63,000.  7 rows, 4096 x 4096, 5.8 us, latency.
 //
 // 448 threads: warp 0 TMA, warp 1 tensor memory + MMA, warps 2-5 scales,
 // warps 6-13 epilogue (two per lane quarter, half of the tile's rows each).

@@ -340,7 +340,8 @@ __global__ void __launch_bounds__(MAXT) norm_pre_rows_kernel(const NormParams n,
 
 // Elements of a thread: eight (one token, before programmatic launches: 3.8 us
 // against 4.6 with sixteen), or sixteen where the rows alone fill the GPU and a thread's fixed work (two
-// sums) counts, or where eight would need more than 1024 threads.
+// sums) counts (from four rows an SM), or where eight would need more than 1024
+// threads.
 int row_per(int T, int D) { return D > 8 * kMaxThreads || (T >= 608 && D >= 1024) ? 16 : 8; }
 // Threads of a row: a whole number of warps.
 int row_threads(int D, int per) { return (int)(32 * cdiv(cdiv(D, per), 32)); }
