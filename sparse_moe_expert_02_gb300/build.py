@@ -1,5 +1,6 @@
 """Build libmoe.so (the CUDA path) in-tree with nvcc for sm_103a, and the
-Python module that calls its small operators (csrc/fastcall.c).
+Python module that calls its small operators (csrc/fastcall.c; left out where
+Python has no headers).
 
 Each translation unit under csrc/ compiles to an object in parallel; the
 objects link into sparse_moe_expert_02_gb300/_build/libmoe.so with the CUDA

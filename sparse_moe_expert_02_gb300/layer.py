@@ -105,9 +105,8 @@ class MoELayer:
         multiplies with mma.sync, so that from some amount of work on the
         tensor memory's products win: T (top_k + 1) 3 D I multiply-adds.
         Measured where the two cross (us a call, few against forward; D 4096,
-        I 1024, top 10 of 128 unless said; profiles/few_or_forward.md):
-        bf16 T 12 359 | 365, T 14 375 | 369, D 7168 I 2048 top 8 T 4 388 | 436,
-        T 8 671 | 632.  FP8 T 8 167 | 186, T 10 199 | 197, T 16 298 | 236.
+        I 1024, top 10 of 128 unless said): bf16 T 12 359 | 365,
+        T 14 375 | 369, D 7168 I 2048 top 8 T 4 388 | 436, T 8 671 | 632.  FP8 T 8 167 | 186, T 10 199 | 197, T 16 298 | 236.
         4 bits T 8 142 | 149, T 9 190 | 154 (two launches above eight tokens:
         there D 1024 I 512 top 8 is the limit, T 12 71 | 72, T 14 78 | 73).
         fp32, on the CUDA cores in both, T 16 2171 | 7825.
