@@ -455,6 +455,83 @@ MOE_API moe_status moe_mx_gemm(const uint8_t* a, const uint8_t* a_scale, const u
                                const int32_t* offsets, int32_t rows, int32_t G, int32_t N, int32_t K, void* out,
                                int32_t out_dtype, int64_t ld_out, uint32_t* err, void* stream);
 
+/* ------------------------------------------------ the experts' products
+ *
+ * What an expert's feed-forward runs where the layer call does not run it:
+ * when its weights are trained, and when they are held in four bits beside
+ * 16- or 32-bit activations.  Conventions as for the operators of the block:
+ * no plan, the current device, dense rows at any row stride and any address
+ * aligned to an element, nothing allocated, rows = 0 returns MOE_OK at once
+ * (moe_grouped_gemm_dw: writes zeros).  Outputs may not overlap inputs unless
+ * said.
+ *
+ * Groups: offsets (device, [G+1], ascending, G <= 1025) gives the rows of each
+ * group, offsets[g] .. offsets[g+1]-1, as moe_permute_index_noalloc writes
+ * them; NULL: G = 1, all rows.  Entries outside [0, rows] are clamped to it.
+ * Rows of no group are not read and are left as they are.  err (device,
+ * uint32[4], zeroed by the caller; or NULL): receives MOE_ERR_DEVICE_TIMEOUT
+ * if a bounded device wait runs out; the output is then incomplete. */
+
+/* Rows times their group's matrix, and the gradients of that:
+ *   out[r][n]  = sum_k x[r][k] w_g[n][k]
+ *   dx[r][k]   = sum_n dy[r][n] w_g[n][k]
+ *   dw_g[n][k] = sum over the rows r of g of dy[r][n] x[r][k]
+ * x [rows, K], dy [rows, N], w and dw [G, N, K] dense.  Both operands fp32, in
+ * fp32 arithmetic, or both bf16, on the tensor cores with fp32 sums; outputs
+ * fp32 or bf16, rounded once.  dw of a group without rows is zeros;
+ * accumulate != 0: the sum is added to what dw holds (and rounded once). */
+MOE_API moe_status moe_grouped_gemm(const void* x, int64_t ld_x, const void* w, int32_t dtype, const int32_t* offsets,
+                                    int32_t rows, int32_t G, int32_t N, int32_t K, void* out, int32_t out_dtype,
+                                    int64_t ld_out, uint32_t* err, void* stream);
+MOE_API moe_status moe_grouped_gemm_dx(const void* dy, int64_t ld_dy, const void* w, int32_t dtype,
+                                       const int32_t* offsets, int32_t rows, int32_t G, int32_t N, int32_t K, void* dx,
+                                       int32_t out_dtype, int64_t ld_dx, uint32_t* err, void* stream);
+MOE_API moe_status moe_grouped_gemm_dw(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, int32_t dtype,
+                                       const int32_t* offsets, int32_t rows, int32_t G, int32_t N, int32_t K, void* dw,
+                                       int32_t out_dtype, int32_t accumulate, uint32_t* err, void* stream);
+
+/* The activation between an expert's products, with the routing weight of a
+ * row, and its gradient (s = 1 / (1 + e^-gate), arithmetic in fp32):
+ *   h       = weight * gate s * up
+ *   dup     = weight * dh * gate s
+ *   dgate   = weight * dh * up * s (1 + gate (1 - s))
+ *   dweight = sum over the row of dh * gate s * up
+ * gate, up, dh, dgate, dup [rows, I], all fp32 or all bf16 (gate and up may be
+ * the halves of one buffer); h fp32 or bf16; weight [rows] fp32 or NULL (1);
+ * dweight [rows] fp32 or NULL (not computed).  An output may be an input of
+ * its own type at the same address and row stride. */
+MOE_API moe_status moe_swiglu(const void* gate, int64_t ld_gate, const void* up, int64_t ld_up, int32_t dtype,
+                              const float* weight, int32_t rows, int32_t I, void* out, int32_t out_dtype, int64_t ld_out,
+                              void* stream);
+MOE_API moe_status moe_swiglu_grad(const void* dh, int64_t ld_dh, const void* gate, int64_t ld_gate, const void* up,
+                                   int64_t ld_up, int32_t dtype, const float* weight, int32_t rows, int32_t I, void* dgate,
+                                   int64_t ld_dgate, void* dup, int64_t ld_dup, float* dweight, void* stream);
+
+/* 4-bit integers with a scale per group of columns: a row of cols columns (a
+ * multiple of 32) is cols/2 bytes of codes, the even column in the low half,
+ * and nb = ceil(cols/group) scales, fp32 or bf16; group 32, 64 or 128, the
+ * last of a row may be short.  value = scale * (code - zero), zero one byte a
+ * group (0 .. 15), or 8 where zeros is NULL.  codes 16-byte aligned.
+ * Quantising: scale = amax/7, or with zeros (max(0, v) - min(0, v))/15,
+ * rounded to its type (1 where that gives 0); zero = -min(0, v)/scale and
+ * codes v/scale + zero to the nearest, ties to even, in 0 .. 15.  A group with
+ * an infinity or a NaN reads back as NaN. */
+MOE_API moe_status moe_int4_quantize(const void* x, int32_t dtype, int64_t ld_x, int64_t rows, int32_t cols,
+                                     int32_t group, uint8_t* codes, void* scales, int32_t scale_dtype, uint8_t* zeros,
+                                     void* stream);
+MOE_API moe_status moe_int4_dequantize(const uint8_t* codes, const void* scales, int32_t scale_dtype,
+                                       const uint8_t* zeros, int32_t group, int64_t rows, int32_t cols, void* out,
+                                       int32_t out_dtype, int64_t ld_out, void* stream);
+
+/* Rows of 16- or 32-bit activations times 4-bit weights, fp32 sums:
+ *   out[r][n] = sum_k x[r][k] w_g[n][k]
+ * x [rows, K] and out [rows, N] fp32 or bf16; w_g the values of [G, N] rows of
+ * K columns as above. */
+MOE_API moe_status moe_int4_gemm(const void* x, int32_t dtype, int64_t ld_x, const uint8_t* codes, const void* scales,
+                                 int32_t scale_dtype, const uint8_t* zeros, int32_t group, const int32_t* offsets,
+                                 int32_t rows, int32_t G, int32_t N, int32_t K, void* out, int32_t out_dtype,
+                                 int64_t ld_out, uint32_t* err, void* stream);
+
 MOE_API const char* moe_status_str(moe_status s);
 
 /* Human-readable detail of the last error returned on this host thread

@@ -52,6 +52,8 @@ SYMBOLS = (
     "moe_status_str", "moe_last_error_detail", "moe_build_info", "moe_launch_count",
     "moe_permute_index_noalloc", "moe_pack_routing_words", "moe_convert_down_weights", "moe_pointer_kind",
     "moe_forward_few", "moe_norm_pre", "moe_norm_post", "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_gemm",
+    "moe_grouped_gemm", "moe_grouped_gemm_dx", "moe_grouped_gemm_dw", "moe_swiglu", "moe_swiglu_grad", "moe_int4_quantize",
+    "moe_int4_dequantize", "moe_int4_gemm",
 )
 
 
@@ -127,6 +129,14 @@ def lib():
                 "moe_mx_quantize": (st, [P, I32, I64, I64, I32, P, P, P]),
                 "moe_mx_dequantize": (st, [P, P, I64, I32, P, I32, I64, P]),
                 "moe_mx_gemm": (st, [P, P, P, P, P, I32, I32, I32, I32, P, I32, I64, P, P]),
+                "moe_grouped_gemm": (st, [P, I64, P, I32, P, I32, I32, I32, I32, P, I32, I64, P, P]),
+                "moe_grouped_gemm_dx": (st, [P, I64, P, I32, P, I32, I32, I32, I32, P, I32, I64, P, P]),
+                "moe_grouped_gemm_dw": (st, [P, I64, P, I64, I32, P, I32, I32, I32, I32, P, I32, I32, P, P]),
+                "moe_swiglu": (st, [P, I64, P, I64, I32, P, I32, I32, P, I32, I64, P]),
+                "moe_swiglu_grad": (st, [P, I64, P, I64, P, I64, I32, P, I32, I32, P, I64, P, I64, P, P]),
+                "moe_int4_quantize": (st, [P, I32, I64, I64, I32, I32, P, P, I32, P, P]),
+                "moe_int4_dequantize": (st, [P, P, I32, P, I32, I64, I32, P, I32, I64, P]),
+                "moe_int4_gemm": (st, [P, I32, I64, P, P, I32, P, I32, P, I32, I32, I32, I32, P, I32, I64, P, P]),
             }
             for name, (res, args) in sig.items():
                 fn = getattr(L, name)
@@ -309,15 +319,17 @@ def fast():
     if _fast is None:
         L = lib()
         if not os.path.exists(_build.FAST):
-            raise RuntimeError("the norms and the 4-bit operators are reached through a C module, which needs Python's headers "
+            raise RuntimeError("the norms, the 4-bit operators and the experts' products are reached through a C module, which needs Python's headers "
                                "(Python.h) to be built; the layer itself does not")
         spec = importlib.util.spec_from_file_location("_fastcall", _build.FAST)
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)
         names = ("moe_norm_pre", "moe_norm_post", "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_gemm")
+        products = ("moe_grouped_gemm", "moe_grouped_gemm_dx", "moe_grouped_gemm_dw", "moe_swiglu", "moe_swiglu_grad", "moe_int4_quantize",
+                    "moe_int4_dequantize", "moe_int4_gemm")
         raw = _raw_stream or (lambda device: torch.cuda.current_stream(device).cuda_stream)
         m.init((torch.float32, torch.bfloat16, torch.uint8, torch.int32), getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
-               raw, tuple(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names))
+               raw, *(tuple(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in group) for group in (names, products)))
         _fast = m
     return _fast
 
@@ -353,6 +365,54 @@ def moe_mx_gemm(a, a_scale, a_cols: int, b, b_scale, b_cols: int, offsets, out, 
     status = (_fast or fast()).mx_gemm(a, a_scale, a_cols, b, b_scale, b_cols, offsets, out, err)
     if status:
         raise MoEError(status, "moe_mx_gemm")
+
+
+def moe_grouped_gemm(x, w, offsets, out, err=None):
+    status = (_fast or fast()).grouped(0, x, w, offsets, out, err)
+    if status:
+        raise MoEError(status, "moe_grouped_gemm")
+
+
+def moe_grouped_gemm_dx(dy, w, offsets, out, err=None):
+    status = (_fast or fast()).grouped(1, dy, w, offsets, out, err)
+    if status:
+        raise MoEError(status, "moe_grouped_gemm_dx")
+
+
+def moe_grouped_gemm_dw(dy, x, offsets, out, accumulate: bool, err=None):
+    status = (_fast or fast()).grouped_dw(dy, x, offsets, out, accumulate, err)
+    if status:
+        raise MoEError(status, "moe_grouped_gemm_dw")
+
+
+def moe_swiglu(gate, up, weight, out):
+    status = (_fast or fast()).swiglu(gate, up, weight, out)
+    if status:
+        raise MoEError(status, "moe_swiglu")
+
+
+def moe_swiglu_grad(dh, gate, up, weight, dgate, dup, dweight):
+    status = (_fast or fast()).swiglu_grad(dh, gate, up, weight, dgate, dup, dweight)
+    if status:
+        raise MoEError(status, "moe_swiglu_grad")
+
+
+def moe_int4_quantize(x, codes, scales, zeros, cols: int, group: int):
+    status = (_fast or fast()).int4_quantize(x, codes, scales, zeros, cols, group)
+    if status:
+        raise MoEError(status, "moe_int4_quantize")
+
+
+def moe_int4_dequantize(codes, scales, zeros, cols: int, group: int, out):
+    status = (_fast or fast()).int4_dequantize(codes, scales, zeros, cols, group, out)
+    if status:
+        raise MoEError(status, "moe_int4_dequantize")
+
+
+def moe_int4_gemm(x, codes, scales, zeros, cols: int, group: int, offsets, out, err=None):
+    status = (_fast or fast()).int4_gemm(x, codes, scales, zeros, cols, group, offsets, out, err)
+    if status:
+        raise MoEError(status, "moe_int4_gemm")
 
 
 def moe_launch_count() -> int:

@@ -1157,6 +1157,254 @@ moe_status moe_mx_gemm(const uint8_t* a, const uint8_t* a_scale, const uint8_t* 
     return MOE_OK;
 }
 
+// ------------------------------------------------- experts' products
+
+namespace {
+moe_status current_sms(int* sms) {
+    int dev = 0;
+    MOE_CUDA(cudaGetDevice(&dev));
+    static const char key = 0;
+    MOE_CUDA(moe::per_device_value(&key, [dev](int* v) { return cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev); }, sms));
+    return MOE_OK;
+}
+
+moe_status check_groups(const int32_t* offsets, int32_t rows, int32_t G, int32_t N, int32_t K, const uint32_t* err) {
+    if (rows < 0 || G < 1 || N < 1 || K < 1) return arg_fail(MOE_ERR_INVALID_ARG, "rows < 0, or G, N or K < 1");
+    if (!offsets && G != 1) return arg_fail(MOE_ERR_INVALID_ARG, "offsets NULL with several groups");
+    if (G > moe::kProductMaxG || N > (1 << 20) || K > (1 << 20) || rows > (1 << 30))
+        return arg_fail(MOE_ERR_UNSUPPORTED, "G above 1025, N or K above 2^20 or rows above 2^30");
+    if (!aligned(offsets, 4) || !aligned(err, 4)) return arg_fail(MOE_ERR_INVALID_ARG, "offsets or err misaligned");
+    return MOE_OK;
+}
+
+moe_status run_product(moe::GroupProduct& g, int32_t dtype, int32_t out_dtype, void* stream) {
+    g.elem = float_elem(dtype);
+    g.out_elem = float_elem(out_dtype);
+    g.spin_ns = kDefaultSpinNs;
+    int sms = 0;
+    const moe_status st = current_sms(&sms);
+    if (st != MOE_OK) return st;
+    moe::PdlScope scope(true);
+    MOE_CUDA(moe::launch_product_simt(g, sms, (cudaStream_t)stream));
+    return MOE_OK;
+}
+
+// out = rows of `in` columns times the groups' weights, in `op`'s direction.
+moe_status rows_product(int op, const void* a, int64_t ld_a, int32_t in, const void* w, int32_t dtype, const int32_t* offsets, int32_t rows,
+                        int32_t G, int32_t N, int32_t K, void* out, int32_t out_dtype, int64_t ld_out, uint32_t* err, void* stream) {
+    const moe_status st = check_groups(offsets, rows, G, N, K, err);
+    if (st != MOE_OK) return st;
+    if (!float_type(dtype) || !float_type(out_dtype)) return arg_fail(MOE_ERR_UNSUPPORTED, "operands and out must be fp32 or bf16");
+    if (rows == 0) return MOE_OK;
+    if (!rows_ok(a, dtype, ld_a, in) || !rows_ok(w, dtype, K, K))
+        return arg_fail(MOE_ERR_INVALID_ARG, "operand NULL or misaligned, or a row stride below its columns");
+    if (!rows_ok(out, out_dtype, ld_out, N + K - in)) return arg_fail(MOE_ERR_INVALID_ARG, "out NULL or misaligned, or its row stride too small");
+    moe::GroupProduct g = {};
+    g.op = op;
+    g.a = a;
+    g.lda = ld_a;
+    g.b = w;
+    g.ldb = K;
+    g.offsets = offsets;
+    g.rows = rows;
+    g.G = G;
+    g.N = N;
+    g.K = K;
+    g.out = out;
+    g.ldo = ld_out;
+    g.err = err;
+    return run_product(g, dtype, out_dtype, stream);
+}
+}  // namespace
+
+moe_status moe_grouped_gemm(const void* x, int64_t ld_x, const void* w, int32_t dtype, const int32_t* offsets, int32_t rows, int32_t G,
+                            int32_t N, int32_t K, void* out, int32_t out_dtype, int64_t ld_out, uint32_t* err, void* stream) {
+    return rows_product(moe::kProductFwd, x, ld_x, K, w, dtype, offsets, rows, G, N, K, out, out_dtype, ld_out, err, stream);
+}
+
+moe_status moe_grouped_gemm_dx(const void* dy, int64_t ld_dy, const void* w, int32_t dtype, const int32_t* offsets, int32_t rows, int32_t G,
+                               int32_t N, int32_t K, void* dx, int32_t out_dtype, int64_t ld_dx, uint32_t* err, void* stream) {
+    return rows_product(moe::kProductDx, dy, ld_dy, N, w, dtype, offsets, rows, G, N, K, dx, out_dtype, ld_dx, err, stream);
+}
+
+moe_status moe_grouped_gemm_dw(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, int32_t dtype, const int32_t* offsets,
+                               int32_t rows, int32_t G, int32_t N, int32_t K, void* dw, int32_t out_dtype, int32_t accumulate, uint32_t* err,
+                               void* stream) {
+    const moe_status st = check_groups(offsets, rows, G, N, K, err);
+    if (st != MOE_OK) return st;
+    if (!float_type(dtype) || !float_type(out_dtype)) return arg_fail(MOE_ERR_UNSUPPORTED, "operands and dw must be fp32 or bf16");
+    if (rows > 0 && (!rows_ok(dy, dtype, ld_dy, N) || !rows_ok(x, dtype, ld_x, K)))
+        return arg_fail(MOE_ERR_INVALID_ARG, "dy or x NULL or misaligned, or a row stride below its columns");
+    if (!rows_ok(dw, out_dtype, K, K)) return arg_fail(MOE_ERR_INVALID_ARG, "dw NULL or misaligned");
+    moe::GroupProduct g = {};
+    g.op = moe::kProductDw;
+    g.a = dy;
+    g.lda = ld_dy;
+    g.b = x;
+    g.ldb = ld_x;
+    g.offsets = offsets;
+    g.rows = rows;
+    g.G = G;
+    g.N = N;
+    g.K = K;
+    g.out = dw;
+    g.ldo = K;
+    g.accumulate = accumulate != 0;
+    g.err = err;
+    return run_product(g, dtype, out_dtype, stream);
+}
+
+namespace {
+moe_status check_act(int32_t dtype, int32_t rows, int32_t I, const void* gate, int64_t ld_gate, const void* up, int64_t ld_up,
+                     const float* weight) {
+    if (rows < 0 || I < 1) return arg_fail(MOE_ERR_INVALID_ARG, "rows < 0 or I < 1");
+    if (I > (1 << 20)) return arg_fail(MOE_ERR_UNSUPPORTED, "I above 2^20");
+    if (!float_type(dtype)) return arg_fail(MOE_ERR_UNSUPPORTED, "gate and up must be fp32 or bf16");
+    if (rows == 0) return MOE_OK;
+    if (!rows_ok(gate, dtype, ld_gate, I) || !rows_ok(up, dtype, ld_up, I) || !aligned(weight, 4))
+        return arg_fail(MOE_ERR_INVALID_ARG, "gate or up NULL or misaligned, a row stride below I, or weight misaligned");
+    return MOE_OK;
+}
+}  // namespace
+
+moe_status moe_swiglu(const void* gate, int64_t ld_gate, const void* up, int64_t ld_up, int32_t dtype, const float* weight, int32_t rows,
+                      int32_t I, void* out, int32_t out_dtype, int64_t ld_out, void* stream) {
+    moe_status st = check_act(dtype, rows, I, gate, ld_gate, up, ld_up, weight);
+    if (st != MOE_OK) return st;
+    if (!float_type(out_dtype)) return arg_fail(MOE_ERR_UNSUPPORTED, "out must be fp32 or bf16");
+    if (rows == 0) return MOE_OK;
+    if (!rows_ok(out, out_dtype, ld_out, I)) return arg_fail(MOE_ERR_INVALID_ARG, "out NULL or misaligned, or its row stride below I");
+    moe::ActParams p = {};
+    p.rows = rows;
+    p.I = I;
+    p.elem = float_elem(dtype);
+    p.out_elem = float_elem(out_dtype);
+    p.gate = gate;
+    p.up = up;
+    p.ld_gate = ld_gate;
+    p.ld_up = ld_up;
+    p.weight = weight;
+    p.out = out;
+    p.ld_out = ld_out;
+    int sms = 0;
+    if ((st = current_sms(&sms)) != MOE_OK) return st;
+    moe::PdlScope scope(true);
+    MOE_CUDA(moe::launch_swiglu(p, sms, (cudaStream_t)stream));
+    return MOE_OK;
+}
+
+moe_status moe_swiglu_grad(const void* dh, int64_t ld_dh, const void* gate, int64_t ld_gate, const void* up, int64_t ld_up, int32_t dtype,
+                           const float* weight, int32_t rows, int32_t I, void* dgate, int64_t ld_dgate, void* dup, int64_t ld_dup,
+                           float* dweight, void* stream) {
+    moe_status st = check_act(dtype, rows, I, gate, ld_gate, up, ld_up, weight);
+    if (st != MOE_OK) return st;
+    if (rows == 0) return MOE_OK;
+    if (!rows_ok(dh, dtype, ld_dh, I) || !rows_ok(dgate, dtype, ld_dgate, I) || !rows_ok(dup, dtype, ld_dup, I) || !aligned(dweight, 4))
+        return arg_fail(MOE_ERR_INVALID_ARG, "dh, dgate or dup NULL or misaligned, a row stride below I, or dweight misaligned");
+    moe::ActParams p = {};
+    p.rows = rows;
+    p.I = I;
+    p.elem = p.out_elem = float_elem(dtype);
+    p.gate = gate;
+    p.up = up;
+    p.dh = dh;
+    p.ld_gate = ld_gate;
+    p.ld_up = ld_up;
+    p.ld_dh = ld_dh;
+    p.weight = weight;
+    p.dgate = dgate;
+    p.dup = dup;
+    p.ld_dgate = ld_dgate;
+    p.ld_dup = ld_dup;
+    p.dweight = dweight;
+    int sms = 0;
+    if ((st = current_sms(&sms)) != MOE_OK) return st;
+    moe::PdlScope scope(true);
+    MOE_CUDA(moe::launch_swiglu_grad(p, sms, (cudaStream_t)stream));
+    return MOE_OK;
+}
+
+namespace {
+// Codes of rows of cols columns (at least one row).
+moe_status check_int4(const uint8_t* codes, const void* scales, int32_t scale_dtype, int32_t group, int32_t cols, bool used) {
+    if (cols < 1) return arg_fail(MOE_ERR_INVALID_ARG, "columns < 1");
+    if (cols % 32 || cols > (1 << 20)) return arg_fail(MOE_ERR_UNSUPPORTED, "columns no multiple of 32, or above 2^20");
+    if (group != 32 && group != 64 && group != 128) return arg_fail(MOE_ERR_UNSUPPORTED, "groups of 32, 64 or 128 columns");
+    if (!float_type(scale_dtype)) return arg_fail(MOE_ERR_UNSUPPORTED, "scales must be fp32 or bf16");
+    if (used && (!ptr_ok(codes) || !rows_ok(scales, scale_dtype, 1, 1)))
+        return arg_fail(MOE_ERR_INVALID_ARG, "codes or scales NULL or misaligned");
+    return MOE_OK;
+}
+moe::Int4 int4_of(const uint8_t* codes, const void* scales, int32_t scale_dtype, const uint8_t* zeros, int32_t group) {
+    moe::Int4 q = {};
+    q.codes = codes;
+    q.scales = scales;
+    q.scale_elem = float_elem(scale_dtype);
+    q.zeros = zeros;
+    q.group = group;
+    return q;
+}
+}  // namespace
+
+moe_status moe_int4_quantize(const void* x, int32_t dtype, int64_t ld_x, int64_t rows, int32_t cols, int32_t group, uint8_t* codes,
+                             void* scales, int32_t scale_dtype, uint8_t* zeros, void* stream) {
+    if (rows < 0) return arg_fail(MOE_ERR_INVALID_ARG, "rows < 0");
+    const moe_status st = check_int4(codes, scales, scale_dtype, group, cols, rows > 0);
+    if (st != MOE_OK) return st;
+    if (!float_type(dtype)) return arg_fail(MOE_ERR_UNSUPPORTED, "values must be fp32 or bf16");
+    if (rows == 0) return MOE_OK;
+    if (!rows_ok(x, dtype, ld_x, cols)) return arg_fail(MOE_ERR_INVALID_ARG, "values NULL or misaligned, or a row stride below cols");
+    moe::PdlScope scope(true);
+    MOE_CUDA(moe::launch_int4_quantize(x, float_elem(dtype), ld_x, rows, cols, int4_of(codes, scales, scale_dtype, zeros, group),
+                                       (cudaStream_t)stream));
+    return MOE_OK;
+}
+
+moe_status moe_int4_dequantize(const uint8_t* codes, const void* scales, int32_t scale_dtype, const uint8_t* zeros, int32_t group,
+                               int64_t rows, int32_t cols, void* out, int32_t out_dtype, int64_t ld_out, void* stream) {
+    if (rows < 0) return arg_fail(MOE_ERR_INVALID_ARG, "rows < 0");
+    const moe_status st = check_int4(codes, scales, scale_dtype, group, cols, rows > 0);
+    if (st != MOE_OK) return st;
+    if (!float_type(out_dtype)) return arg_fail(MOE_ERR_UNSUPPORTED, "out must be fp32 or bf16");
+    if (rows == 0) return MOE_OK;
+    if (!rows_ok(out, out_dtype, ld_out, cols)) return arg_fail(MOE_ERR_INVALID_ARG, "out NULL or misaligned, or its row stride below cols");
+    moe::PdlScope scope(true);
+    MOE_CUDA(moe::launch_int4_dequantize(int4_of(codes, scales, scale_dtype, zeros, group), rows, cols, out, float_elem(out_dtype), ld_out,
+                                         (cudaStream_t)stream));
+    return MOE_OK;
+}
+
+moe_status moe_int4_gemm(const void* x, int32_t dtype, int64_t ld_x, const uint8_t* codes, const void* scales, int32_t scale_dtype,
+                         const uint8_t* zeros, int32_t group, const int32_t* offsets, int32_t rows, int32_t G, int32_t N, int32_t K,
+                         void* out, int32_t out_dtype, int64_t ld_out, uint32_t* err, void* stream) {
+    moe_status st = check_groups(offsets, rows, G, N, K, err);
+    if (st != MOE_OK || (st = check_int4(codes, scales, scale_dtype, group, K, rows > 0)) != MOE_OK) return st;
+    if (!float_type(dtype) || !float_type(out_dtype)) return arg_fail(MOE_ERR_UNSUPPORTED, "x and out must be fp32 or bf16");
+    if (rows == 0) return MOE_OK;
+    if (!rows_ok(x, dtype, ld_x, K)) return arg_fail(MOE_ERR_INVALID_ARG, "x NULL or misaligned, or its row stride below K");
+    if (!rows_ok(out, out_dtype, ld_out, N)) return arg_fail(MOE_ERR_INVALID_ARG, "out NULL or misaligned, or its row stride below N");
+    moe::Int4Product g = {};
+    g.x = x;
+    g.elem = float_elem(dtype);
+    g.ldx = ld_x;
+    g.w = int4_of(codes, scales, scale_dtype, zeros, group);
+    g.offsets = offsets;
+    g.rows = rows;
+    g.G = G;
+    g.N = N;
+    g.K = K;
+    g.out = out;
+    g.out_elem = float_elem(out_dtype);
+    g.ldo = ld_out;
+    g.err = err;
+    g.spin_ns = kDefaultSpinNs;
+    int sms = 0;
+    if ((st = current_sms(&sms)) != MOE_OK) return st;
+    moe::PdlScope scope(true);
+    MOE_CUDA(moe::launch_int4_simt(g, sms, (cudaStream_t)stream));
+    return MOE_OK;
+}
+
 moe_status moe_pointer_kind(const void* ptr, int32_t* kind) {
     if (!kind) return arg_fail(MOE_ERR_INVALID_ARG, "kind is NULL");
     *kind = 0;

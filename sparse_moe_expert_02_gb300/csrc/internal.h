@@ -284,4 +284,72 @@ bool few_fits(int dtype, int down_f16, int D, int I, int k);
 cudaError_t launch_few(const FewParams& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_selftest_timeout(uint32_t* err, int64_t limit_ns, cudaStream_t stream);
 
+// ------------------------------------------------- experts' products
+
+// Products of rows grouped by expert (moe_grouped_gemm and its gradients):
+//   kProductFwd  out[r][n] = sum_k a[r][k] w_g[n][k]
+//   kProductDx   out[r][k] = sum_n a[r][n] w_g[n][k]
+//   kProductDw   out_g[n][k] (+)= sum over the rows r of g of a[r][n] x[r][k]
+enum ProductOp : int { kProductFwd = 0, kProductDx = 1, kProductDw = 2 };
+struct GroupProduct {
+    int op;
+    int elem;                // of both operands: kF32 or kBF16
+    const void* a;           // x or dy, [rows, lda]
+    int64_t lda;
+    const void* b;           // kProductDw: x [rows, ldb]; else w [G, N, K]
+    int64_t ldb;
+    const int32_t* offsets;  // [G+1] device, or nullptr (G = 1: all rows)
+    int rows, G, N, K;
+    void* out;               // [rows, ldo], or [G, N, K]
+    int out_elem;
+    int64_t ldo;             // kProductDw: K
+    int accumulate;          // kProductDw: added to out
+    uint32_t* err;           // device error word or nullptr
+    int64_t spin_ns;
+};
+constexpr int kProductMaxG = 1025;
+cudaError_t launch_product_simt(const GroupProduct& p, int num_sms, cudaStream_t stream);
+
+// The experts' activation h = weight * silu(gate) * up and its gradient; rows
+// of I elements at the strides ld_*.
+struct ActParams {
+    int rows, I;
+    int elem, out_elem;          // of gate, up and dh, dgate, dup; of h
+    const void *gate, *up, *dh;  // dh: gradient only
+    int64_t ld_gate, ld_up, ld_dh;
+    const float* weight;         // [rows] or nullptr
+    void* out;                   // h
+    int64_t ld_out;
+    void *dgate, *dup;
+    int64_t ld_dgate, ld_dup;
+    float* dweight;              // [rows] or nullptr
+};
+cudaError_t launch_swiglu(const ActParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_swiglu_grad(const ActParams& p, int num_sms, cudaStream_t stream);
+
+// 4-bit codes with a scale and a zero point per group of columns.
+struct Int4 {
+    const uint8_t* codes;  // [rows, cols/2]
+    const void* scales;    // [rows, ceil(cols/group)]
+    int scale_elem;        // kF32 or kBF16
+    const uint8_t* zeros;  // [rows, ceil(cols/group)] or nullptr (8 everywhere)
+    int group;             // 32, 64 or 128
+};
+cudaError_t launch_int4_quantize(const void* x, int x_elem, int64_t ld, int64_t rows, int cols, const Int4& q, cudaStream_t stream);
+cudaError_t launch_int4_dequantize(const Int4& q, int64_t rows, int cols, void* out, int out_elem, int64_t ld, cudaStream_t stream);
+struct Int4Product {
+    const void* x;           // [rows, ldx]
+    int elem;
+    int64_t ldx;
+    Int4 w;                  // [G * N] rows of K columns
+    const int32_t* offsets;  // [G+1] device, or nullptr
+    int rows, G, N, K;
+    void* out;               // [rows, ldo]
+    int out_elem;
+    int64_t ldo;
+    uint32_t* err;
+    int64_t spin_ns;
+};
+cudaError_t launch_int4_simt(const Int4Product& p, int num_sms, cudaStream_t stream);
+
 }  // namespace moe
