@@ -1185,7 +1185,7 @@ moe_status run_product(moe::GroupProduct& g, int32_t dtype, int32_t out_dtype, v
     const moe_status st = current_sms(&sms);
     if (st != MOE_OK) return st;
     moe::PdlScope scope(true);
-    MOE_CUDA(moe::launch_product_simt(g, sms, (cudaStream_t)stream));
+    MOE_CUDA(g.elem == moe::kBF16 ? moe::launch_product_tc(g, sms, (cudaStream_t)stream) : moe::launch_product_simt(g, sms, (cudaStream_t)stream));
     return MOE_OK;
 }
 
@@ -1401,7 +1401,7 @@ moe_status moe_int4_gemm(const void* x, int32_t dtype, int64_t ld_x, const uint8
     int sms = 0;
     if ((st = current_sms(&sms)) != MOE_OK) return st;
     moe::PdlScope scope(true);
-    MOE_CUDA(moe::launch_int4_simt(g, sms, (cudaStream_t)stream));
+    MOE_CUDA(g.elem == moe::kBF16 && rows > 16 * (int64_t)G ? moe::launch_int4_tc(g, sms, (cudaStream_t)stream) : moe::launch_int4_simt(g, sms, (cudaStream_t)stream));
     return MOE_OK;
 }
 

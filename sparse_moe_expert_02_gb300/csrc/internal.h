@@ -309,6 +309,7 @@ struct GroupProduct {
 };
 constexpr int kProductMaxG = 1025;
 cudaError_t launch_product_simt(const GroupProduct& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_product_tc(const GroupProduct& p, int num_sms, cudaStream_t stream);  // bf16
 
 // The experts' activation h = weight * silu(gate) * up and its gradient; rows
 // of I elements at the strides ld_*.
@@ -351,5 +352,6 @@ struct Int4Product {
     int64_t spin_ns;
 };
 cudaError_t launch_int4_simt(const Int4Product& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_int4_tc(const Int4Product& p, int num_sms, cudaStream_t stream);  // bf16 rows
 
 }  // namespace moe

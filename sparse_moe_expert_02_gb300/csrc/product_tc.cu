@@ -1,0 +1,744 @@
+// Products of rows grouped by expert on the tensor cores, bf16 with fp32 sums
+// (moe_grouped_gemm and its gradients), and rows times 4-bit weights for many
+// rows (moe_int4_gemm).  One kernel, D[f][i] = sum_c F(f, c) R(i, c):
+//
+//            f (MMA M, 128 a tile)   i (MMA N)      c               F lies   R lies
+//   forward  features of w_g         rows of g      columns of x    along c  along c
+//   dx       columns of w_g          rows of g      features of w_g along f  along c
+//   dw       columns of x            columns of dy  rows of g       along f  along i
+//
+// f is what the output is contiguous along.  tcgen05 takes an operand that is
+// contiguous along M or N as readily as one along K, so nothing is transposed:
+// a stage holds 64 of c in 128-byte swizzled lines, of 64 c for each f or i,
+// or of 64 f or i for each c.  The rows of a group are the MMA's N side in
+// steps of 16, so a small group costs tensor time for its rows only.
+//
+// dw sums over a group's rows, which end anywhere: the lines of the last 16
+// that lie past the end hold the next group's rows, and the MMA warp writes
+// zeros over them in both operands (their values may be anything, and times
+// zero need not be zero).  Columns past a matrix's edge are filled with zeros
+// by TMA; w is mapped as [G][N][K], so that dx's sum ends with its own matrix.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "groups.cuh"
+#include "internal.h"
+#include "tc_ptx.cuh"
+#include "tc_warp.cuh"
+
+namespace moe {
+namespace tc {
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();  // gemm_tc.cu
+}
+namespace ptc {
+
+using namespace tc;
+
+// Where a stage's operands come from: TMA alone; or the line of an operand
+// that TMA cannot read (rows not aligned to 16 bytes) copied by eight warps;
+// or the F operand's 4-bit codes turned into bf16 by them (bf16 or fp32
+// scales), R by TMA or copied.
+enum Feed { kTma = 0, kCopy = 1, kCodes16 = 2, kCodes32 = 3 };
+
+constexpr int BF = 128, BK = 64, kMaxI = 256;  // f and c of a stage, i of a tile at most
+constexpr int kLine = 128;                     // bytes
+constexpr int kFBytes = BF * BK * 2;
+constexpr int kMaxStages = 8;
+constexpr int kEpiWarps = 8, kFeedWarps = 8;
+constexpr int kThreads = 32 * (2 + kEpiWarps), kThreadsFeed = kThreads + 32 * kFeedWarps;
+constexpr int kMaxSplit = 8;
+constexpr int kRing = 4 * (kFBytes + kMaxI * BK * 2);
+constexpr int kStWarp = 8 * 32 * 4;            // 8 row pairs x 32 features, two bf16 a word
+constexpr int kOffStage = kRing;
+constexpr int kOffBar = kOffStage + kEpiWarps * kStWarp;
+constexpr int kOffTab = kOffBar + 256;
+constexpr int kSmem = kOffTab + (int)sizeof(GroupTable);
+static_assert(kSmem <= 232448, "shared memory plan exceeds 227 KB");
+static_assert((2 * kMaxStages + 5) * 8 + 8 <= 256, "barrier block overflows");
+
+struct Args {
+    const int32_t* offsets;
+    int rows, G, N, K;
+    const bf16 *f, *r;  // operands F (w, or x for dw) and R
+    int64_t ldf, ldr;
+    Int4 w;             // F in 4 bits
+    void* out;
+    int out_elem, accumulate;
+    int64_t ldo;
+    uint32_t* err;
+    int64_t spin_ns;
+    int tile_i, stages, stage_bytes, split;
+    int f_copy, r_copy;    // operand copied by the feed warps: 0 no, 1 by elements, 2 by pairs
+};
+
+// Descriptor of an operand contiguous along M or N, 128-byte swizzle: lines
+// of 64 elements, eight lines (of eight c) 1024 bytes apart, the next 64
+// elements 64 lines on.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)((BK * kLine) >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)2 << 61;
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void st_shared16(uint32_t a, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+struct Unit {
+    int g;
+    int i0, n;   // first row (dw: column of dy) of the tile, and how many
+    int f0;
+    int c0, c1;  // range of the sum
+};
+
+template <int OP> __device__ __forceinline__ int f_size(const Args& p) { return OP == kProductFwd ? p.N : p.K; }
+
+template <int OP> __device__ __forceinline__ Unit unit_at(const Args& p, int u, int FB, int NB, const GroupTable& t) {
+    Unit r;
+    const int rt = u / FB;
+    r.f0 = (u - rt * FB) * BF;
+    if (OP == kProductDw) {
+        r.g = rt / NB;
+        r.i0 = (rt - r.g * NB) * p.tile_i;
+        r.n = min(p.tile_i, p.N - r.i0);
+        r.c0 = t.first[r.g];
+        r.c1 = t.last[r.g];
+    } else {
+        r.g = find_group_smem(t.tiles, p.G, rt);
+        r.i0 = t.first[r.g] + (rt - t.tiles[r.g]) * p.tile_i;
+        r.n = min(p.tile_i, t.last[r.g] - r.i0);
+        r.c0 = 0;
+        r.c1 = OP == kProductFwd ? p.K : p.N;
+    }
+    return r;
+}
+// Blocks of the sum that this rank of a split takes: [first, last).
+__device__ __forceinline__ int2 my_blocks(const Unit& u, int rank, int split) {
+    const int kb = (u.c1 - u.c0 + BK - 1) / BK;
+    return make_int2((int)((int64_t)kb * rank / split), (int)((int64_t)kb * (rank + 1) / split));
+}
+
+// 32 features (this warp's lanes) x 32 rows, packed two rows a word (w[j]:
+// rows 2j and 2j + 1 of feature `lane`), to out rows of 64 bytes.
+__device__ __forceinline__ void store_block(uint8_t* st, const uint32_t* w, bf16* out, int64_t ldo, int rows, int cols) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) *(uint32_t*)(st + j * 128 + lane * 4) = w[8 * h + j];
+        __syncwarp();
+        const int pr = lane >> 2, q = lane & 3, row = 16 * h + 2 * pr;  // row pair, eight features
+        const uint4 a = *(const uint4*)(st + pr * 128 + q * 32), b = *(const uint4*)(st + pr * 128 + q * 32 + 16);
+        const uint4 lo = make_uint4(__byte_perm(a.x, a.y, 0x5410), __byte_perm(a.z, a.w, 0x5410), __byte_perm(b.x, b.y, 0x5410),
+                                    __byte_perm(b.z, b.w, 0x5410));
+        const uint4 hi = make_uint4(__byte_perm(a.x, a.y, 0x7632), __byte_perm(a.z, a.w, 0x7632), __byte_perm(b.x, b.y, 0x7632),
+                                    __byte_perm(b.z, b.w, 0x7632));
+        if (q * 8 < cols) {
+            if (row < rows) *(uint4*)(out + (int64_t)row * ldo + q * 8) = lo;
+            if (row + 1 < rows) *(uint4*)(out + (int64_t)(row + 1) * ldo + q * 8) = hi;
+        }
+        __syncwarp();
+    }
+}
+
+// One line of an operand, 64 elements from p of which the first `valid` are
+// the matrix's: this lane's two, the rest zeros.
+template <int MODE> __device__ __forceinline__ uint32_t load_pair(const bf16* p, int valid, int lane) {
+    const uint16_t* q = (const uint16_t*)p + 2 * lane;
+    if (MODE == 2) {  // pairs lie on 4 bytes; a last odd element has its neighbour cleared
+        if (2 * lane + 1 < valid) return __ldg((const uint32_t*)q);
+        return 2 * lane < valid ? (uint32_t)__ldg(q) : 0u;
+    }
+    uint32_t lo = 0, hi = 0;
+    if (2 * lane < valid) lo = __ldg(q);
+    if (2 * lane + 1 < valid) hi = __ldg(q + 1);
+    return lo | hi << 16;
+}
+
+// Lines base, base + kFeedWarps, ... below `lines` of an operand to shared
+// memory at dst, kBatch of them in flight.  along_c: a line is 64 c of row
+// `line`; else 64 rows (columns of the tensor) of one c, 64 lines a block.
+template <int MODE>
+__device__ __forceinline__ void copy_lines(uint32_t dst, const bf16* src, int64_t ld, bool along_c, int lines, int valid_rows, int c_left,
+                                           int first, int c16, int lane) {
+    constexpr int kBatch = 16;
+    for (int l0 = first; l0 < lines; l0 += kBatch * kFeedWarps) {
+        uint32_t v[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int l = l0 + j * kFeedWarps;
+            v[j] = 0;
+            if (l >= lines) continue;
+            if (along_c) {
+                if (l < valid_rows) v[j] = load_pair<MODE>(src + (int64_t)l * ld, min(c_left, BK), lane);
+            } else {
+                const int c = l & (BK - 1), at = l - c;  // `at`: first of the block's 64 rows
+                if (c < c_left) v[j] = load_pair<MODE>(src + (int64_t)c * ld + at, min(max(valid_rows - at, 0), 64), lane);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int l = l0 + j * kFeedWarps;
+            if (l >= lines || (!along_c && (l & (BK - 1)) >= c16)) continue;
+            const uint32_t a = dst + l * kLine + (((lane >> 2) ^ (l & 7)) << 4) + ((lane & 3) << 2);
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v[j]) : "memory");
+        }
+    }
+}
+
+// Eight codes (a word, the first in the lowest four bits) as bf16 pairs of
+// code - zero; z: 128 + zero in both halves.  bf16 counts in ones from 128 to
+// 256, so 0x4300 + code is 128 + code, and the difference is exact.
+__device__ __forceinline__ void decode8(uint32_t w, __nv_bfloat162 z, __nv_bfloat162 (&o)[4]) {
+    const uint32_t h = w >> 4;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        // byte j of w and of w >> 4: their low halves are codes 2j and 2j + 1
+        const uint32_t v = (__byte_perm(w, h, (4 + j) << 8 | j) & 0x000F000Fu) | 0x43004300u;
+        o[j] = __hsub2(*(const __nv_bfloat162*)&v, z);
+    }
+}
+// Their values, rounded to bf16 once.
+template <int FEED> __device__ __forceinline__ uint4 values8(uint32_t w, __nv_bfloat162 z, float s) {
+    __nv_bfloat162 d[4];
+    decode8(w, z, d);
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        __nv_bfloat162 v;
+        if (FEED == kCodes16) {
+            const bf16 sb = __float2bfloat16_rn(s);  // exact: it was a bf16
+            v = __hmul2(d[j], __nv_bfloat162(sb, sb));
+        } else {
+            const float2 x = __bfloat1622float2(d[j]);
+            v = __floats2bfloat162_rn(x.x * s, x.y * s);
+        }
+        o[j] = *(const uint32_t*)&v;
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <int OP, int FEED, bool SPLIT>
+__global__ void __launch_bounds__(FEED == kTma ? kThreads : kThreadsFeed, 1)
+    product_tc_kernel(const __grid_constant__ CUtensorMap tm_f, const __grid_constant__ CUtensorMap tm_f16,
+                      const __grid_constant__ CUtensorMap tm_r, const __grid_constant__ CUtensorMap tm_r16, const Args p) {
+    constexpr bool kFAlongC = OP == kProductFwd, kRAlongC = OP != kProductDw;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint64_t* bars = (uint64_t*)(smem + kOffBar);
+    const int S = p.stages;
+    const uint32_t smem0 = smem_u32(smem);
+    const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + kMaxStages);
+    const uint32_t tfull0 = smem_u32(bars + 2 * kMaxStages), tempty0 = tfull0 + 16, drain = tfull0 + 32;
+    uint32_t* tmem_slot = (uint32_t*)(bars + 2 * kMaxStages + 5);
+    volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
+    GroupTable& tab = *(GroupTable*)(smem + kOffTab);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const bool f_tma = FEED == kTma || (FEED == kCopy && !p.f_copy), r_tma = FEED == kTma || !p.r_copy;
+    if (threadIdx.x == 0) {
+        const int feeders = (f_tma || r_tma ? 1 : 0) + (FEED == kTma ? 0 : kFeedWarps);
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full0 + 8 * s, feeders);
+            mbar_init(empty0 + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(tfull0 + 8 * b, 1);
+            mbar_init(tempty0 + 8 * b, kEpiWarps);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    pdl_wait();  // what an earlier kernel wrote
+    if (warp == 2) group_table(tab, p.offsets, p.G, p.rows, OP == kProductDw ? kMaxI : p.tile_i);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_release();  // (once tensor memory is ours)
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+    const int F = f_size<OP>(p), FB = (F + BF - 1) / BF, NB = (p.N + p.tile_i - 1) / p.tile_i;
+    const int units = (OP == kProductDw ? p.G * NB : tab.tiles[p.G]) * FB;
+    // Units of this CTA: u0, u0 + step, ...  Split: a cluster takes one unit or none.
+    const int rank = SPLIT ? (int)cluster_rank() : 0, cl = SPLIT ? p.split : 1;
+    const int u0 = (int)blockIdx.x / cl, step = (int)gridDim.x / cl;
+    const int64_t lim = p.spin_ns;
+
+    if (warp == 0) {
+        // -------------------------------------------------- TMA producer
+        if (f_tma || r_tma) {
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int u = u0; u < units && ok; u += step) {
+                const Unit un = unit_at<OP>(p, u, FB, NB, tab);
+                const int2 kb = my_blocks(un, rank, cl);
+                const int n16 = __shfl_sync(0xffffffffu, (un.n + 15) >> 4, 0), slabs = (n16 + 3) >> 2;
+                const int i0 = __shfl_sync(0xffffffffu, un.i0, 0), f0 = __shfl_sync(0xffffffffu, un.f0, 0);
+                const int g = __shfl_sync(0xffffffffu, un.g, 0);
+                for (int k = kb.x; k < kb.y; ++k) {
+                    ok = warp_wait(empty0 + 8 * stage, phase ^ 1, lim, abort_flag, p.err, 61);
+                    if (!ok) break;
+                    const int c = __shfl_sync(0xffffffffu, un.c0 + k * BK, 0);
+                    // dw: sixteens of this block's rows; the others read whole blocks, zeros past the edge
+                    const int c16 = OP == kProductDw ? __shfl_sync(0xffffffffu, min(4, (un.c1 - c + 15) >> 4), 0) : 4;
+                    if (elect_one()) {
+                        const uint32_t fb = full0 + 8 * stage, fs = smem0 + stage * p.stage_bytes, rs = fs + kFBytes;
+                        const int rlines = kRAlongC ? n16 * 16 : slabs * c16 * 16, flines = kFAlongC ? BF : 2 * c16 * 16;
+                        mbar_expect_tx(fb, (f_tma ? flines * kLine : 0) + (r_tma ? rlines * kLine : 0));
+                        if (f_tma) {
+                            if (OP == kProductFwd) {
+                                tma_load_3d(fs, &tm_f, fb, c, f0, g);
+                            } else if (OP == kProductDx) {
+                                tma_load_3d(fs, &tm_f, fb, f0, c, g);
+                                tma_load_3d(fs + BK * kLine, &tm_f, fb, f0 + 64, c, g);
+                            } else {
+                                for (int s = 0; s < 2; ++s) {
+                                    if (c16 == 4) tma_load_2d(fs + s * BK * kLine, &tm_f, fb, f0 + 64 * s, c);
+                                    else
+                                        for (int j = 0; j < c16; ++j)
+                                            tma_load_2d(fs + s * BK * kLine + j * 16 * kLine, &tm_f16, fb, f0 + 64 * s, c + 16 * j);
+                                }
+                            }
+                        }
+                        if (r_tma) {
+                            if (kRAlongC) {
+                                const int n64 = n16 >> 2;
+                                for (int j = 0; j < n64; ++j) tma_load_2d(rs + j * 64 * kLine, &tm_r, fb, c, i0 + j * 64);
+                                for (int j = 4 * n64; j < n16; ++j) tma_load_2d(rs + j * 16 * kLine, &tm_r16, fb, c, i0 + j * 16);
+                            } else {
+                                for (int s = 0; s < slabs; ++s) {
+                                    if (c16 == 4) tma_load_2d(rs + s * BK * kLine, &tm_r, fb, i0 + 64 * s, c);
+                                    else
+                                        for (int j = 0; j < c16; ++j)
+                                            tma_load_2d(rs + s * BK * kLine + j * 16 * kLine, &tm_r16, fb, i0 + 64 * s, c + 16 * j);
+                                }
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            if (!ok) sleep_ns(200000);  // copies already issued land before the CTA leaves
+        }
+    } else if (warp == 1) {
+        // --------------------------------------------------- MMA issuer
+        int stage = 0, acc = 0;
+        uint32_t phase = 0, acc_phase = 0;
+        bool ok = true;
+        for (int u = u0; u < units && ok; u += step) {
+            const Unit un = unit_at<OP>(p, u, FB, NB, tab);
+            const int2 kb = my_blocks(un, rank, cl);
+            if (kb.x == kb.y) continue;  // nothing to sum: the epilogue knows
+            const int n = __shfl_sync(0xffffffffu, (un.n + 15) & ~15, 0);
+            const uint32_t id = idesc_bf16(BF, n) | (kFAlongC ? 0u : 1u << 15) | (kRAlongC ? 0u : 1u << 16);
+            ok = warp_wait(tempty0 + 8 * acc, acc_phase ^ 1, lim, abort_flag, p.err, 62);
+            if (!ok) break;
+            const uint32_t d = tmem + acc * kMaxI;
+            for (int k = kb.x; k < kb.y; ++k) {
+                ok = warp_wait(full0 + 8 * stage, phase, lim, abort_flag, p.err, 63);
+                if (!ok) break;
+                const uint32_t fs = smem0 + stage * p.stage_bytes, rs = fs + kFBytes;
+                const int left = un.c1 - un.c0 - k * BK;
+                const int steps = __shfl_sync(0xffffffffu, min(4, (left + 15) >> 4), 0);
+                if (OP == kProductDw && left < BK && (left & 15)) {
+                    const int slabs = 2 + (n + 63) / 64, per = (16 - (left & 15)) * 8;  // 16-byte pieces of a slab
+                    for (int e = lane; e < slabs * per; e += 32) {
+                        const int s = e / per;
+                        st_shared16(fs + s * BK * kLine + left * kLine + (e - s * per) * 16, make_uint4(0, 0, 0, 0));
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                }
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t fd = kFAlongC ? umma_desc(fs) : desc_mn(fs), rd = kRAlongC ? umma_desc(rs) : desc_mn(rs);
+                    constexpr uint64_t fstep = (kFAlongC ? 32 : 16 * kLine) >> 4, rstep = (kRAlongC ? 32 : 16 * kLine) >> 4;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        if (kk < steps) umma_bf16(d, fd + kk * fstep, rd + kk * rstep, id, k != kb.x || kk != 0);
+                    umma_commit(empty0 + 8 * stage);
+                    if (k + 1 == kb.y) umma_commit(tfull0 + 8 * acc);
+                }
+                __syncwarp();
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1;
+        }
+        if (elect_one()) umma_commit(drain);  // everything issued is done before tensor memory is freed
+        __syncwarp();
+        volatile int never = 0;
+        mbar_wait(drain, 0, 1000000000LL, &never);
+    } else if (FEED != kTma && warp >= 2 + kEpiWarps) {
+        // -------------------------------------------- copied or coded operands
+        const int fw = warp - 2 - kEpiWarps, t = threadIdx.x - kThreads;
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int u = u0; u < units && ok; u += step) {
+            const Unit un = unit_at<OP>(p, u, FB, NB, tab);
+            const int2 kb = my_blocks(un, rank, cl);
+            // codes: thread t takes half a line (32 codes, one scale) of feature t / 2
+            const int64_t wrow = (int64_t)un.g * p.N + un.f0 + (t >> 1);
+            const bool in = un.f0 + (t >> 1) < p.N;
+            const int nbk = (p.K + p.w.group - 1) / p.w.group;
+            constexpr int kAhead = 3;
+            uint4 q[kAhead];
+            float sc[kAhead];
+            int zp[kAhead];
+            auto fetch = [&](int k, uint4& v, float& s, int& z) {
+                const int c = k * BK + 32 * (t & 1);
+                v = make_uint4(0, 0, 0, 0);
+                s = 0.0f;
+                z = 0;
+                if (!in || k >= kb.y || c >= p.K) return;
+                v = __ldg((const uint4*)(p.w.codes + wrow * (p.K / 2) + c / 2));
+                const int64_t at = wrow * nbk + c / p.w.group;
+                s = FEED == kCodes16 ? to_f32(((const bf16*)p.w.scales)[at]) : ((const float*)p.w.scales)[at];
+                z = p.w.zeros ? p.w.zeros[at] : 8;
+            };
+            if (FEED >= kCodes16) {
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) fetch(kb.x + i, q[i], sc[i], zp[i]);
+            }
+            for (int k0 = kb.x; k0 < kb.y && ok; k0 += kAhead) {
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    const int k = k0 + i;
+                    if (k >= kb.y || !ok) break;
+                    ok = __all_sync(0xffffffffu, mbar_wait(empty0 + 8 * stage, phase ^ 1, lim, abort_flag));
+                    if (!ok) break;
+                    const int c = un.c0 + k * BK, left = un.c1 - c, c16 = min(4, (left + 15) >> 4) * 16;
+                    const uint32_t fs = smem0 + stage * p.stage_bytes, rs = fs + kFBytes;
+                    if (FEED >= kCodes16) {
+                        const uint32_t row = fs + (t >> 1) * kLine;
+                        const bf16 zb = __int2bfloat16_rn(128 + zp[i]);
+                        const __nv_bfloat162 z = __nv_bfloat162(zb, zb);
+                        const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint4 v = values8<FEED>(w[j], z, sc[i]);
+                            if (c + 32 * (t & 1) >= p.K) v = make_uint4(0, 0, 0, 0);
+                            st_shared16(row + (((4 * (t & 1) + j) ^ ((t >> 1) & 7)) << 4), v);
+                        }
+                        fetch(k + kAhead, q[i], sc[i], zp[i]);
+                    } else if (p.f_copy) {
+                        const bf16* src = OP == kProductFwd   ? p.f + ((int64_t)un.g * p.N + un.f0) * p.ldf + c
+                                          : OP == kProductDx ? p.f + ((int64_t)un.g * p.N + c) * p.ldf + un.f0
+                                                             : p.f + (int64_t)c * p.ldf + un.f0;
+                        if (p.f_copy == 2) copy_lines<2>(fs, src, p.ldf, kFAlongC, BF, F - un.f0, left, fw, c16, lane);
+                        else copy_lines<1>(fs, src, p.ldf, kFAlongC, BF, F - un.f0, left, fw, c16, lane);
+                    }
+                    if (p.r_copy) {
+                        const bf16* src = kRAlongC ? p.r + (int64_t)un.i0 * p.ldr + c : p.r + (int64_t)c * p.ldr + un.i0;
+                        const int lines = kRAlongC ? (un.n + 15) & ~15 : ((un.n + 63) & ~63);
+                        if (p.r_copy == 2) copy_lines<2>(rs, src, p.ldr, kRAlongC, lines, un.n, left, fw, c16, lane);
+                        else copy_lines<1>(rs, src, p.ldr, kRAlongC, lines, un.n, left, fw, c16, lane);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full0 + 8 * stage);
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+        }
+    }
+    // ---------------------------------------------------------- epilogue
+    // Lanes are f, columns i.
+    const int ew = warp - 2, sub = warp & 3, half = ew >> 2;  // lane quarter, column half
+    const bool epi = ew >= 0 && ew < kEpiWarps;
+    if (!SPLIT && epi) {
+        uint8_t* st = smem + kOffStage + ew * kStWarp;
+        const bool vec = F % 8 == 0 && p.ldo % 8 == 0 && ((uintptr_t)p.out & 15) == 0;
+        const bool add = OP == kProductDw && p.accumulate;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        for (int u = u0; u < units; u += step) {
+            const Unit un = unit_at<OP>(p, u, FB, NB, tab);
+            const bool any = un.c1 > un.c0;
+            const uint32_t taddr = tmem + acc * kMaxI + ((uint32_t)(sub * 32) << 16);
+            const uint32_t te = tempty0 + 8 * acc;
+            if (any) {
+                const bool ok = mbar_wait(tfull0 + 8 * acc, acc_phase, lim, abort_flag);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    if (lane == 0 && !*abort_flag) {
+                        record_error(p.err, MOE_ERR_DEVICE_TIMEOUT, 64, blockIdx.x, u);
+                        *abort_flag = 1;
+                    }
+                    break;
+                }
+                tc_fence_after();
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1;
+            } else if (add) {
+                continue;
+            }
+            const int f = un.f0 + sub * 32, cols = F - f;  // this warp's f inside the matrix
+            const int64_t row0 = OP == kProductDw ? (int64_t)un.g * p.N + un.i0 : (int64_t)un.i0;
+            // this half's 32-row blocks: 0, 2, 4, 6 or 1, 3, 5, 7
+#pragma unroll 1
+            for (int c = half * 32; c < un.n; c += 64) {
+                uint32_t v[32];
+                if (any) {
+                    tmem_ld32(taddr + c, v);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0;
+                }
+                const int rows = un.n - c;
+                const int64_t at = (row0 + c) * p.ldo + f;
+                if (p.out_elem == kF32) {
+                    float* o = (float*)p.out + at + lane;
+                    if (lane < cols) {
+                        if (add) {
+                            const float* q = o;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j, q += p.ldo)
+                                if (j < rows) v[j] = __float_as_uint(*q + __uint_as_float(v[j]));
+                        }
+#pragma unroll
+                        for (int j = 0; j < 32; ++j, o += p.ldo)
+                            if (j < rows) *o = __uint_as_float(v[j]);
+                    }
+                } else if (vec && !add) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                        pk[j] = *(const uint32_t*)&h;
+                    }
+                    store_block(st, pk, (bf16*)p.out + at, p.ldo, rows, cols);
+                } else if (lane < cols) {
+                    bf16* o = (bf16*)p.out + at + lane;
+                    if (add) {
+                        const bf16* q = o;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j, q += p.ldo)
+                            if (j < rows) v[j] = __float_as_uint(to_f32(*q) + __uint_as_float(v[j]));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; ++j, o += p.ldo)
+                        if (j < rows) *o = __float2bfloat16_rn(__uint_as_float(v[j]));
+                }
+            }
+            if (any) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(te);
+            }
+        }
+    }
+    if (SPLIT) {
+        // One unit a cluster.  Rank q sums rows q, q + split, ... of the tile
+        // in blocks of four: every rank sends it its partial sums, [rank][slot
+        // of four rows][feature], into the ring, which is idle by then.
+        __syncwarp();
+        cluster_sync();  // every CTA's loads and MMAs are done
+        const bool has = u0 < units;
+        const Unit un = has ? unit_at<OP>(p, u0, FB, NB, tab) : Unit{};
+        const int2 kb = my_blocks(un, rank, cl);
+        const int quads = (un.n + 3) >> 2, per = (quads + cl - 1) / cl;  // four-row slots, of each rank
+        const uint32_t part = (uint32_t)(per * BF * 16);                 // bytes a rank sends another
+        if (has && epi) {
+            tc_fence_after();  // the accumulator was committed before the barrier
+            const uint32_t taddr = tmem + ((uint32_t)(sub * 32) << 16);
+            const uint32_t mine = smem0 + rank * part + (uint32_t)((sub * 32 + lane) * 16);
+#pragma unroll 1
+            for (int c = half * 16; c < un.n; c += 32) {
+                uint32_t v[16];
+                if (kb.x < kb.y) {
+                    tmem_ld16(taddr + c, v);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = 0;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int qd = c / 4 + j;
+                    if (qd < quads) {
+                        const float4 x = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]), __uint_as_float(v[4 * j + 2]),
+                                                     __uint_as_float(v[4 * j + 3]));
+                        st_cluster(mapa_shared(mine + (uint32_t)(qd / cl) * BF * 16, (uint32_t)(qd % cl)), x);
+                    }
+                }
+            }
+            tc_fence_before();
+        }
+        __syncwarp();
+        cluster_sync();
+        const bool add = OP == kProductDw && p.accumulate;
+        if (has && epi && !(add && un.c0 == un.c1)) {
+            const int e = threadIdx.x - 64, feat = un.f0 + (e & 127);
+            const int64_t row0 = OP == kProductDw ? (int64_t)un.g * p.N + un.i0 : (int64_t)un.i0;
+            for (int i = e >> 7; i < per; i += 2) {
+                const int row = (i * cl + rank) * 4;
+                if (row >= un.n) break;
+                float s[4] = {0, 0, 0, 0};
+                for (int k = 0; k < cl; ++k) {
+                    const float4 x = *(const float4*)(smem + k * part + i * BF * 16 + (e & 127) * 16);
+                    s[0] += x.x; s[1] += x.y; s[2] += x.z; s[3] += x.w;
+                }
+                if (feat < F) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (row + j < un.n) {
+                            const int64_t at = (row0 + row + j) * p.ldo + feat;
+                            if (p.out_elem == kF32) {
+                                float* o = (float*)p.out + at;
+                                *o = add ? *o + s[j] : s[j];
+                            } else {
+                                bf16* o = (bf16*)p.out + at;
+                                *o = __float2bfloat16_rn(add ? to_f32(*o) + s[j] : s[j]);
+                            }
+                        }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+}
+
+// bf16 [d2][d1][d0] (d2 = 0: two dimensions), boxes of a 128-byte line by box1.
+bool line_map(CUtensorMap* m, const void* base, int64_t d0, int64_t d1, int64_t d2, int64_t ld, int box1) {
+    const cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2}, strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)(ld * d1) * 2};
+    const cuuint32_t box[3] = {BK, (cuuint32_t)box1, 1}, es[3] = {1, 1, 1};
+    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d2 ? 3 : 2, const_cast<void*>(base), dims, strides, box, es,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// How the feed warps would copy an operand.
+int copy_mode(const void* base, int64_t ld) { return ((uintptr_t)base & 3) == 0 && ld % 2 == 0 ? 2 : 1; }
+
+struct Maps {
+    CUtensorMap f, f16, r, r16;
+};
+
+template <int OP, int FEED, bool SPLIT> cudaError_t launch(const Maps& m, const Args& a, int grid, cudaStream_t s) {
+    cudaError_t e = ensure_smem_attr((const void*)product_tc_kernel<OP, FEED, SPLIT>, kSmem);
+    if (e != cudaSuccess) return e;
+    e = launch_kernel(product_tc_kernel<OP, FEED, SPLIT>, dim3(grid), dim3(FEED == kTma ? kThreads : kThreadsFeed), kSmem, s,
+                      SPLIT ? a.split : 1, m.f, m.f16, m.r, m.r16, a);
+    count_launches(1);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Tiles, stages, split and grid; the launch.
+template <int OP> cudaError_t plan_and_launch(const Maps& m, Args& a, int feed, int num_sms, cudaStream_t s) {
+    // i of a tile: as many as the groups fill (F is read once per tile), fewer
+    // where they do not, for more stages in flight.
+    const int64_t avg = OP == kProductDw ? a.N : cdiv(a.rows, a.G);
+    a.tile_i = avg > 128 ? 256 : avg > (OP == kProductDw ? 64 : 32) ? 128 : 64;
+    a.stage_bytes = kFBytes + a.tile_i * BK * 2;
+    a.stages = std::min(kMaxStages, kRing / a.stage_bytes);
+    const int F = OP == kProductFwd ? a.N : a.K;
+    const int64_t fb = cdiv(F, BF);
+    const int64_t tiles = OP == kProductDw ? a.G * cdiv(a.N, a.tile_i) : cdiv(a.rows, a.tile_i) + std::min(a.G - 1, a.rows);
+    const int64_t units = tiles * fb;  // at most
+    const int64_t kb = cdiv(OP == kProductFwd ? a.K : OP == kProductDx ? a.N : cdiv(a.rows, a.G), BK);
+    a.split = 1;
+    while (a.split < kMaxSplit && units * a.split * 2 <= num_sms && kb >= 4 * a.split) a.split *= 2;
+    const int grid = a.split > 1 ? (int)units * a.split : (int)std::min<int64_t>(units, num_sms);
+#define MOE_PTC(FEED) (a.split > 1 ? launch<OP, FEED, true>(m, a, grid, s) : launch<OP, FEED, false>(m, a, grid, s))
+    if (feed == kTma) return MOE_PTC(kTma);
+    if constexpr (OP == kProductFwd) {
+        if (feed == kCodes16) return MOE_PTC(kCodes16);
+        if (feed == kCodes32) return MOE_PTC(kCodes32);
+    }
+    return MOE_PTC(kCopy);
+#undef MOE_PTC
+}
+
+}  // namespace ptc
+
+cudaError_t launch_product_tc(const GroupProduct& g, int num_sms, cudaStream_t stream) {
+    using namespace ptc;
+    if (!tc::encode_fn()) return cudaErrorNotSupported;
+    Maps m = {};
+    Args a = {};
+    a.offsets = g.offsets;
+    a.rows = g.rows;
+    a.G = g.G;
+    a.N = g.N;
+    a.K = g.K;
+    a.f = (const bf16*)g.b;
+    a.r = (const bf16*)g.a;
+    a.ldf = g.op == kProductDw ? g.ldb : g.K;
+    a.ldr = g.lda;
+    a.out = g.out;
+    a.out_elem = g.out_elem;
+    a.accumulate = g.accumulate;
+    a.ldo = g.ldo;
+    a.err = g.err;
+    a.spin_ns = g.spin_ns;
+    const int64_t r0 = g.op == kProductFwd ? g.K : g.N;  // columns of R
+    // one row: its stride is of no account, and must not keep TMA from it
+    if (g.rows == 1) {
+        a.ldr = cdiv(r0, 8) * 8;
+        if (g.op == kProductDw) a.ldf = cdiv(g.K, 8) * 8;
+    }
+    // (no rows, dw: the maps are not read from, only zeros are written)
+    if (g.rows == 0) {
+        a.f_copy = a.r_copy = 1;
+    } else {
+        if (g.op == kProductDw) {
+            if (!line_map(&m.f, g.b, g.K, g.rows, 0, a.ldf, 64) || !line_map(&m.f16, g.b, g.K, g.rows, 0, a.ldf, 16))
+                a.f_copy = copy_mode(g.b, a.ldf);
+        } else if (!line_map(&m.f, g.b, g.K, g.N, g.G, g.K, g.op == kProductFwd ? BF : 64)) {
+            a.f_copy = copy_mode(g.b, g.K);
+        }
+        if (!line_map(&m.r, g.a, r0, g.rows, 0, a.ldr, 64) || !line_map(&m.r16, g.a, r0, g.rows, 0, a.ldr, 16))
+            a.r_copy = copy_mode(g.a, a.ldr);
+    }
+    const int feed = a.f_copy || a.r_copy ? kCopy : kTma;
+    if (g.op == kProductFwd) return plan_and_launch<kProductFwd>(m, a, feed, num_sms, stream);
+    if (g.op == kProductDx) return plan_and_launch<kProductDx>(m, a, feed, num_sms, stream);
+    return plan_and_launch<kProductDw>(m, a, feed, num_sms, stream);
+}
+
+cudaError_t launch_int4_tc(const Int4Product& g, int num_sms, cudaStream_t stream) {
+    using namespace ptc;
+    if (!tc::encode_fn()) return cudaErrorNotSupported;
+    Maps m = {};
+    Args a = {};
+    a.offsets = g.offsets;
+    a.rows = g.rows;
+    a.G = g.G;
+    a.N = g.N;
+    a.K = g.K;
+    a.w = g.w;
+    a.r = (const bf16*)g.x;
+    a.ldr = g.rows == 1 ? g.K : g.ldx;
+    a.out = g.out;
+    a.out_elem = g.out_elem;
+    a.ldo = g.ldo;
+    a.err = g.err;
+    a.spin_ns = g.spin_ns;
+    if (!line_map(&m.r, g.x, g.K, g.rows, 0, a.ldr, 64) || !line_map(&m.r16, g.x, g.K, g.rows, 0, a.ldr, 16)) a.r_copy = copy_mode(g.x, a.ldr);
+    return plan_and_launch<kProductFwd>(m, a, g.w.scale_elem == kF32 ? kCodes32 : kCodes16, num_sms, stream);
+}
+
+}  // namespace moe
