@@ -1177,6 +1177,9 @@ moe_status check_groups(const int32_t* offsets, int32_t rows, int32_t G, int32_t
     return MOE_OK;
 }
 
+// Few rows a group: bound by the weights' bytes.
+bool few_rows(int64_t rows, int64_t G) { return rows <= 16 * G; }
+
 moe_status run_product(moe::GroupProduct& g, int32_t dtype, int32_t out_dtype, void* stream) {
     g.elem = float_elem(dtype);
     g.out_elem = float_elem(out_dtype);
@@ -1185,7 +1188,11 @@ moe_status run_product(moe::GroupProduct& g, int32_t dtype, int32_t out_dtype, v
     const moe_status st = current_sms(&sms);
     if (st != MOE_OK) return st;
     moe::PdlScope scope(true);
-    MOE_CUDA(g.elem == moe::kBF16 ? moe::launch_product_tc(g, sms, (cudaStream_t)stream) : moe::launch_product_simt(g, sms, (cudaStream_t)stream));
+    cudaError_t e = cudaErrorNotSupported;
+    if (few_rows(g.rows, g.G)) e = moe::launch_product_few(g, sms, (cudaStream_t)stream);
+    if (e == cudaErrorNotSupported)
+        e = g.elem == moe::kBF16 ? moe::launch_product_tc(g, sms, (cudaStream_t)stream) : moe::launch_product_simt(g, sms, (cudaStream_t)stream);
+    MOE_CUDA(e);
     return MOE_OK;
 }
 
@@ -1401,7 +1408,9 @@ moe_status moe_int4_gemm(const void* x, int32_t dtype, int64_t ld_x, const uint8
     int sms = 0;
     if ((st = current_sms(&sms)) != MOE_OK) return st;
     moe::PdlScope scope(true);
-    MOE_CUDA(g.elem == moe::kBF16 && rows > 16 * (int64_t)G ? moe::launch_int4_tc(g, sms, (cudaStream_t)stream) : moe::launch_int4_simt(g, sms, (cudaStream_t)stream));
+    MOE_CUDA(few_rows(rows, G)          ? moe::launch_int4_few(g, sms, (cudaStream_t)stream)
+             : g.elem == moe::kBF16 ? moe::launch_int4_tc(g, sms, (cudaStream_t)stream)
+                                    : moe::launch_int4_simt(g, sms, (cudaStream_t)stream));
     return MOE_OK;
 }
 

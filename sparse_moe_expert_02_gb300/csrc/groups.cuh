@@ -20,14 +20,15 @@ struct GroupTable {
 // end lies before its start has none.
 __device__ __forceinline__ int2 group_rows(const int32_t* offsets, int g, int rows) {
     if (!offsets) return make_int2(0, rows);
-    const int lo = min(max(offsets[g], 0), rows);
-    return make_int2(lo, min(max(offsets[g + 1], lo), rows));
+    const int lo = min(max(__ldg(offsets + g), 0), rows);
+    return make_int2(lo, min(max(__ldg(offsets + g + 1), lo), rows));
 }
 
 // By one converged warp; the block synchronises afterwards.
 __device__ __forceinline__ void group_table(GroupTable& t, const int32_t* offsets, int G, int rows, int tile_rows) {
     const int lane = threadIdx.x & 31;
     int base = 0;
+#pragma unroll 4
     for (int g0 = 0; g0 < G; g0 += 32) {
         const int g = g0 + lane;
         int n = 0;

@@ -310,6 +310,8 @@ struct GroupProduct {
 constexpr int kProductMaxG = 1025;
 cudaError_t launch_product_simt(const GroupProduct& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_product_tc(const GroupProduct& p, int num_sms, cudaStream_t stream);  // bf16
+// kProductFwd, bf16, K a multiple of 8, w aligned to 16 bytes (else cudaErrorNotSupported).
+cudaError_t launch_product_few(const GroupProduct& p, int num_sms, cudaStream_t stream);
 
 // The experts' activation h = weight * silu(gate) * up and its gradient; rows
 // of I elements at the strides ld_*.
@@ -353,5 +355,6 @@ struct Int4Product {
 };
 cudaError_t launch_int4_simt(const Int4Product& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_int4_tc(const Int4Product& p, int num_sms, cudaStream_t stream);  // bf16 rows
+cudaError_t launch_int4_few(const Int4Product& p, int num_sms, cudaStream_t stream);
 
 }  // namespace moe

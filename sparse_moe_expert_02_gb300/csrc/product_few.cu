@@ -1,0 +1,400 @@
+// Products of a few rows with their groups' weights, bf16 or 4-bit
+// (moe_grouped_gemm, moe_int4_gemm): out[r][n] = sum_k x[r][k] w_g[n][k].
+//
+// Bound by the bytes of the weights, so they go from memory to registers and
+// straight into mma.sync (m16n8k16: 16 features by 8 rows), with nothing
+// between: a tensor-memory kernel would write what it decodes to shared memory
+// first, for tiles of 128 features that a few rows do not fill.  A block takes
+// 16 features of a group at a time, its eight warps a piece of the columns
+// each; a warp has the loads of its next 512 columns in flight while it
+// multiplies.  The order of the columns within a sum is free as long as x
+// follows it, so a lane loads 16 bytes of a row and hands them to successive
+// MMAs.  Eight partial sums meet in shared memory.  How the columns are
+// divided depends on K alone, so a row's result does not depend on the other
+// rows and groups.
+//
+// 4 bits: the MMAs sum code - zero, exact in bf16, over one group of columns;
+// the fp32 sum is then multiplied by the scale.  Groups of 32 and 64 columns
+// need the four lanes that share an MMA's columns to hold codes of the same
+// group: they exchange words first.  fp32 rows go in as three bf16 parts,
+// which hold all 24 bits.  A group's sum may overflow where its product with
+// the scale does not, so what comes out as no finite number is summed again
+// with the weights' values.
+#include <algorithm>
+#include <type_traits>
+
+#include "common.cuh"
+#include "groups.cuh"
+#include "int4.cuh"
+#include "internal.h"
+
+namespace moe {
+namespace few_rows {
+
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kF = 16, kRows = 16;  // features and rows of a tile
+constexpr int kChunk = 128;         // columns a warp takes at a time
+constexpr int kPitch = 20;          // floats between the rows of a partial tile: lanes hit different banks
+
+struct Args {
+    const int32_t* offsets;
+    int rows, G, N, K;
+    const void* x;
+    int64_t ldx;
+    bool xv;  // 16-byte loads of x
+    const bf16* w;
+    Int4 q;
+    void* out;
+    int out_elem;
+    int64_t ldo;
+};
+
+// Codes in groups of 2^LG columns; LG = 0: bf16 weights.
+template <int LG> struct Chunk {  // a lane's share: 32 codes of feature rows g and g + 8
+    uint4 w[2];
+    float s[2];
+    int z[2];
+};
+template <> struct Chunk<0> {  // 32 bf16 of each
+    uint4 w[2][4];
+};
+
+struct Unit {
+    int g, f0, row0, n;
+};
+__device__ __forceinline__ Unit unit_at(const Args& p, int u, int FB, const GroupTable& t) {
+    Unit r;
+    const int rt = u / FB;
+    r.f0 = (u - rt * FB) * kF;
+    r.g = 0;
+    if (!p.offsets) {
+        r.row0 = rt * kRows;
+        r.n = min(kRows, p.rows - r.row0);
+        return r;
+    }
+    r.g = find_group_smem(t.tiles, p.G, rt);
+    r.row0 = t.first[r.g] + (rt - t.tiles[r.g]) * kRows;
+    r.n = min(kRows, t.last[r.g] - r.row0);
+    return r;
+}
+
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Weights are read once: no place in L1, which x keeps.
+__device__ __forceinline__ uint4 load_once(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+// Eight columns of x as the parts of MMA operands: one for bf16; for fp32
+// three, each the leading eight bits of what the ones before leave, the second
+// times 2^8 and the third times 2^16: within range for the largest numbers,
+// and no bits lost below bf16's smallest for the smallest.
+template <typename T> struct Parts { static constexpr int n = sizeof(T) == 4 ? 3 : 1; uint32_t v[n][4]; };
+
+__device__ __forceinline__ void load_x(const bf16* x, bool vec, Parts<bf16>& o) {
+    if (vec) {
+        const uint4 v = __ldg((const uint4*)x);
+        o.v[0][0] = v.x; o.v[0][1] = v.y; o.v[0][2] = v.z; o.v[0][3] = v.w;
+    } else {
+        const uint16_t* h = (const uint16_t*)x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o.v[0][j] = (uint32_t)__ldg(h + 2 * j) | (uint32_t)__ldg(h + 2 * j + 1) << 16;
+    }
+}
+__device__ __forceinline__ void load_x(const float* x, bool vec, Parts<float>& o) {
+    float f[8];
+    if (vec) {
+        *(float4*)f = __ldg((const float4*)x);
+        *(float4*)(f + 4) = __ldg((const float4*)x + 1);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = __ldg(x + j);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t part[3][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float v = f[2 * j + h];
+            const uint32_t u = __float_as_uint(v);
+            const bool odd = (u & 0x7F800000u) == 0x7F800000u;  // an infinity or a NaN goes whole into the first part
+            part[0][h] = odd && (u & 0x007FFFFFu) ? 0x7FC00000u : u & 0xFFFF0000u;
+            const float r1 = odd ? 0.0f : v - __uint_as_float(part[0][h]);
+            const float r2 = r1 * 256.0f;
+            part[1][h] = __float_as_uint(r2) & 0xFFFF0000u;
+            part[2][h] = __float_as_uint((r2 - __uint_as_float(part[1][h])) * 256.0f);
+        }
+#pragma unroll
+        for (int i = 0; i < 3; ++i) o.v[i][j] = __byte_perm(part[i][0], part[i][1], 0x7632);
+    }
+}
+
+// Words of four lanes exchanged so that word i of every lane is of column
+// group i (groups of 32) or i / 2 (of 64).
+template <int LG> __device__ __forceinline__ void exchange(uint32_t (&w)[4], int t) {
+    if (LG == 5) {
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, t & 1 ? w[i] : w[i + 1], 1);
+            if (t & 1) w[i] = got;
+            else w[i + 1] = got;
+        }
+    }
+    if (LG == 5 || LG == 6) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, t & 2 ? w[i] : w[i + 2], 2);
+            if (t & 2) w[i] = got;
+            else w[i + 2] = got;
+        }
+    }
+}
+// First column, within a chunk, of the eight in word i of lane t.
+template <int LG> __device__ __forceinline__ int column(int i, int t) {
+    if (LG == 7) return 32 * t + 8 * i;
+    if (LG == 6) return 64 * (i >> 1) + 32 * (t & 1) + 16 * (t >> 1) + 8 * (i & 1);
+    return 32 * i + 8 * t;
+}
+
+template <int LG, typename T>
+__global__ void __launch_bounds__(kThreads, 2) product_few_kernel(const Args p) {
+    constexpr int kDepth = LG ? 4 : 2;
+    __shared__ GroupTable tab;
+    __shared__ float part[2][kWarps][kRows * kPitch];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    pdl_wait();
+    if (p.offsets) {
+        if (warp == 0) group_table(tab, p.offsets, p.G, p.rows, kRows);
+        __syncthreads();
+    }
+    pdl_release();
+    const int FB = (p.N + kF - 1) / kF;
+    const int units = (p.offsets ? tab.tiles[p.G] : (p.rows + kRows - 1) / kRows) * FB;
+    const int chunks = (p.K + kChunk - 1) / kChunk;
+    const int k0 = chunks * warp / kWarps, nk = chunks * (warp + 1) / kWarps - k0, batches = (nk + kDepth - 1) / kDepth;
+    const int step = gridDim.x;
+    const int nb = LG ? (p.K + (1 << LG) - 1) >> LG : 0;
+
+    Chunk<LG> q[kDepth];
+    int fu = blockIdx.x, fb = 0;  // next batch to load
+    int64_t frow[2];
+    bool fin[2];
+    auto locate = [&](int u) {
+        if (u >= units) return;
+        const Unit un = unit_at(p, u, FB, tab);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            fin[h] = un.f0 + g + 8 * h < p.N;
+            frow[h] = (int64_t)un.g * p.N + un.f0 + g + 8 * h;
+        }
+    };
+    auto fetch = [&](int i, Chunk<LG>& v) {  // slot i of the batch (fu, fb)
+        const int k = fb * kDepth + i, c = (k0 + k) * kChunk;
+        const bool on = fu < units && k < nk;
+        if constexpr (LG == 0) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int col = c + column<0>(j, t);
+                    v.w[h][j] = on && fin[h] && col < p.K ? load_once(p.w + frow[h] * p.K + col) : make_uint4(0, 0, 0, 0);
+                }
+        } else {
+            const int col = c + 32 * t;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                v.w[h] = make_uint4(0, 0, 0, 0);
+                v.s[h] = 0.0f;
+                v.z[h] = 0;
+                if (on && fin[h] && col < p.K) v.w[h] = load_once(p.q.codes + frow[h] * (p.K / 2) + col / 2);
+                if (on && fin[h] && (LG == 7 || col < p.K)) {  // (a group of 128 is the chunk: all four lanes need its scale)
+                    const int64_t at = frow[h] * nb + (col >> LG);
+                    v.s[h] = p.q.scale_elem == kF32 ? __ldg((const float*)p.q.scales + at) : to_f32(((const bf16*)p.q.scales)[at]);
+                    v.z[h] = p.q.zeros ? __ldg(p.q.zeros + at) : 8;
+                }
+            }
+        }
+    };
+    locate(fu);
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i) fetch(i, q[i]);
+
+    int buf = 0;
+    for (int u = blockIdx.x; u < units; u += step, buf ^= 1) {
+        const Unit un = unit_at(p, u, FB, tab);
+        const bool two = un.n > 8;
+        float acc[2][4] = {};
+        // rows past the tile: the last one's, their sums are not stored
+        const T* x0 = (const T*)p.x + (int64_t)(un.row0 + min(g, un.n - 1)) * p.ldx;
+        const T* x1 = (const T*)p.x + (int64_t)(un.row0 + min(g + 8, un.n - 1)) * p.ldx;
+        for (int b = 0; b < batches; ++b) {
+            if (++fb == batches) {
+                fb = 0;
+                fu += step;
+            }
+            if (fb == 0) locate(fu);
+#pragma unroll
+            for (int i = 0; i < kDepth; ++i) {
+                const int k = b * kDepth + i, c = (k0 + k) * kChunk;
+                if (k < nk) {
+                    if constexpr (LG == 0) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int col = c + column<0>(j, t);
+                            const uint4 a = q[i].w[0][j], e = q[i].w[1][j];
+                            Parts<T> x = {};
+                            if (col < p.K) load_x(x0 + col, p.xv, x);
+                            mma(acc[0], a.x, e.x, a.y, e.y, x.v[0][0], x.v[0][1]);
+                            mma(acc[0], a.z, e.z, a.w, e.w, x.v[0][2], x.v[0][3]);
+                            if (two) {
+                                Parts<T> y = {};
+                                if (col < p.K) load_x(x1 + col, p.xv, y);
+                                mma(acc[1], a.x, e.x, a.y, e.y, y.v[0][0], y.v[0][1]);
+                                mma(acc[1], a.z, e.z, a.w, e.w, y.v[0][2], y.v[0][3]);
+                            }
+                        }
+                    } else {
+                        constexpr int kGroups = 1 << (7 - LG), kWords = 4 / kGroups;  // column groups of a chunk, words of each
+                        uint32_t w0[4] = {q[i].w[0].x, q[i].w[0].y, q[i].w[0].z, q[i].w[0].w};
+                        uint32_t w1[4] = {q[i].w[1].x, q[i].w[1].y, q[i].w[1].z, q[i].w[1].w};
+                        exchange<LG>(w0, t);
+                        exchange<LG>(w1, t);
+#pragma unroll
+                        for (int gr = 0; gr < kGroups; ++gr) {
+                            float s[2];
+                            __nv_bfloat162 z[2];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {  // (the group's columns are lanes gr * kWords .. of the four)
+                                const int from = (lane & ~3) | (gr * kWords);
+                                s[h] = LG == 7 ? q[i].s[h] : __shfl_sync(0xffffffffu, q[i].s[h], from);
+                                z[h] = int4_zero(LG == 7 ? q[i].z[h] : __shfl_sync(0xffffffffu, q[i].z[h], from));
+                            }
+                            float sum[Parts<T>::n][2][4] = {};
+#pragma unroll
+                            for (int j = 0; j < kWords; ++j) {
+                                const int wi = gr * kWords + j, col = c + column<LG>(wi, t);
+                                uint32_t a[4], e[4];
+                                int4_pairs(w0[wi], z[0], a);
+                                int4_pairs(w1[wi], z[1], e);
+                                Parts<T> x = {};
+                                if (col < p.K) load_x(x0 + col, p.xv, x);
+#pragma unroll
+                                for (int m = 0; m < Parts<T>::n; ++m) {
+                                    mma(sum[m][0], a[0], e[0], a[1], e[1], x.v[m][0], x.v[m][1]);
+                                    mma(sum[m][0], a[2], e[2], a[3], e[3], x.v[m][2], x.v[m][3]);
+                                }
+                                if (two) {
+                                    Parts<T> y = {};
+                                    if (col < p.K) load_x(x1 + col, p.xv, y);
+#pragma unroll
+                                    for (int m = 0; m < Parts<T>::n; ++m) {
+                                        mma(sum[m][1], a[0], e[0], a[1], e[1], y.v[m][0], y.v[m][1]);
+                                        mma(sum[m][1], a[2], e[2], a[3], e[3], y.v[m][2], y.v[m][3]);
+                                    }
+                                }
+                            }
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int m = 0; m < 4; ++m) {
+                                    float v = sum[0][h][m];
+                                    if constexpr (Parts<T>::n == 3)
+                                        v += fmaf(sum[2][h][m], 0x1p-16f, sum[1][h][m] * 0x1p-8f);
+                                    acc[h][m] = fmaf(s[m >> 1], v, acc[h][m]);
+                                }
+                        }
+                    }
+                }
+                fetch(i, q[i]);
+            }
+        }
+        // D(g, 2t), D(g, 2t + 1), D(g + 8, 2t), D(g + 8, 2t + 1): feature, row
+        float* mine = part[buf][warp];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) mine[(8 * h + 2 * t + (m & 1)) * kPitch + g + 8 * (m >> 1)] = acc[h][m];
+        __syncthreads();
+        const int f = threadIdx.x & (kF - 1), r = threadIdx.x / kF;
+        if (r < un.n && un.f0 + f < p.N) {
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) v += part[buf][w][r * kPitch + f];
+            if constexpr (LG != 0) {
+                if (!isfinite(v)) {  // a group's sum may have overflown before its scale
+                    const T* x = (const T*)p.x + (int64_t)(un.row0 + r) * p.ldx;
+                    const int64_t row = (int64_t)un.g * p.N + un.f0 + f;
+                    v = 0.0f;
+                    for (int k = 0; k < p.K; ++k) {
+                        const int64_t at = row * nb + (k >> LG);
+                        const int cd = (p.q.codes[row * (p.K / 2) + (k >> 1)] >> (4 * (k & 1))) & 15;
+                        const float s = p.q.scale_elem == kF32 ? ((const float*)p.q.scales)[at] : to_f32(((const bf16*)p.q.scales)[at]);
+                        v = fmaf(to_f32(x[k]), (float)(cd - (p.q.zeros ? p.q.zeros[at] : 8)) * s, v);
+                    }
+                }
+            }
+            const int64_t at = (int64_t)(un.row0 + r) * p.ldo + un.f0 + f;
+            if (p.out_elem == kF32) ((float*)p.out)[at] = v;
+            else ((bf16*)p.out)[at] = __float2bfloat16_rn(v);
+        }
+    }
+}
+
+template <int LG, typename T> cudaError_t launch(const Args& a, int num_sms, cudaStream_t s) {
+    const int64_t tiles = cdiv(a.rows, kRows) + (a.offsets ? std::min(a.G - 1, a.rows) : 0), units = tiles * cdiv(a.N, kF);  // at most
+    const cudaError_t e = launch_kernel(product_few_kernel<LG, T>, dim3((unsigned)std::min<int64_t>(units, 2 * num_sms)), dim3(kThreads), 0, s, 1, a);
+    count_launches(1);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+bool aligned16(const void* p, int64_t ld, int elem) { return ((uintptr_t)p & 15) == 0 && ld * (elem == kF32 ? 4 : 2) % 16 == 0; }
+
+}  // namespace few_rows
+
+cudaError_t launch_product_few(const GroupProduct& g, int num_sms, cudaStream_t stream) {
+    using namespace few_rows;
+    if (g.op != kProductFwd || g.elem != kBF16 || g.K % 8 || ((uintptr_t)g.b & 15)) return cudaErrorNotSupported;
+    Args a = {};
+    a.offsets = g.offsets;
+    a.rows = g.rows;
+    a.G = g.G;
+    a.N = g.N;
+    a.K = g.K;
+    a.x = g.a;
+    a.ldx = g.lda;
+    a.xv = aligned16(g.a, g.rows > 1 ? g.lda : 0, kBF16);
+    a.w = (const bf16*)g.b;
+    a.out = g.out;
+    a.out_elem = g.out_elem;
+    a.ldo = g.ldo;
+    return launch<0, bf16>(a, num_sms, stream);
+}
+
+cudaError_t launch_int4_few(const Int4Product& g, int num_sms, cudaStream_t stream) {
+    using namespace few_rows;
+    Args a = {};
+    a.offsets = g.offsets;
+    a.rows = g.rows;
+    a.G = g.G;
+    a.N = g.N;
+    a.K = g.K;
+    a.x = g.x;
+    a.ldx = g.ldx;
+    a.xv = aligned16(g.x, g.rows > 1 ? g.ldx : 0, g.elem);
+    a.q = g.w;
+    a.out = g.out;
+    a.out_elem = g.out_elem;
+    a.ldo = g.ldo;
+    const bool f32 = g.elem == kF32;
+    if (g.w.group == 32) return f32 ? launch<5, float>(a, num_sms, stream) : launch<5, bf16>(a, num_sms, stream);
+    if (g.w.group == 64) return f32 ? launch<6, float>(a, num_sms, stream) : launch<6, bf16>(a, num_sms, stream);
+    return f32 ? launch<7, float>(a, num_sms, stream) : launch<7, bf16>(a, num_sms, stream);
+}
+
+}  // namespace moe

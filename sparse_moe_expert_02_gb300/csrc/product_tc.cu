@@ -24,6 +24,7 @@
 
 #include "common.cuh"
 #include "groups.cuh"
+#include "int4.cuh"
 #include "internal.h"
 #include "tc_ptx.cuh"
 #include "tc_warp.cuh"
@@ -192,31 +193,19 @@ __device__ __forceinline__ void copy_lines(uint32_t dst, const bf16* src, int64_
     }
 }
 
-// Eight codes (a word, the first in the lowest four bits) as bf16 pairs of
-// code - zero; z: 128 + zero in both halves.  bf16 counts in ones from 128 to
-// 256, so 0x4300 + code is 128 + code, and the difference is exact.
-__device__ __forceinline__ void decode8(uint32_t w, __nv_bfloat162 z, __nv_bfloat162 (&o)[4]) {
-    const uint32_t h = w >> 4;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        // byte j of w and of w >> 4: their low halves are codes 2j and 2j + 1
-        const uint32_t v = (__byte_perm(w, h, (4 + j) << 8 | j) & 0x000F000Fu) | 0x43004300u;
-        o[j] = __hsub2(*(const __nv_bfloat162*)&v, z);
-    }
-}
-// Their values, rounded to bf16 once.
+// Eight codes' values, rounded to bf16 once.
 template <int FEED> __device__ __forceinline__ uint4 values8(uint32_t w, __nv_bfloat162 z, float s) {
-    __nv_bfloat162 d[4];
-    decode8(w, z, d);
     uint32_t o[4];
+    int4_pairs(w, z, o);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 d = *(const __nv_bfloat162*)&o[j];
         __nv_bfloat162 v;
         if (FEED == kCodes16) {
             const bf16 sb = __float2bfloat16_rn(s);  // exact: it was a bf16
-            v = __hmul2(d[j], __nv_bfloat162(sb, sb));
+            v = __hmul2(d, __nv_bfloat162(sb, sb));
         } else {
-            const float2 x = __bfloat1622float2(d[j]);
+            const float2 x = __bfloat1622float2(d);
             v = __floats2bfloat162_rn(x.x * s, x.y * s);
         }
         o[j] = *(const uint32_t*)&v;
@@ -428,8 +417,7 @@ __global__ void __launch_bounds__(FEED == kTma ? kThreads : kThreadsFeed, 1)
                     const uint32_t fs = smem0 + stage * p.stage_bytes, rs = fs + kFBytes;
                     if (FEED >= kCodes16) {
                         const uint32_t row = fs + (t >> 1) * kLine;
-                        const bf16 zb = __int2bfloat16_rn(128 + zp[i]);
-                        const __nv_bfloat162 z = __nv_bfloat162(zb, zb);
+                        const __nv_bfloat162 z = int4_zero(zp[i]);
                         const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
