@@ -1191,7 +1191,7 @@ moe_status run_product(moe::GroupProduct& g, int32_t dtype, int32_t out_dtype, v
     cudaError_t e = cudaErrorNotSupported;
     if (few_rows(g.rows, g.G)) e = moe::launch_product_few(g, sms, (cudaStream_t)stream);
     if (e == cudaErrorNotSupported)
-        e = g.elem == moe::kBF16 ? moe::launch_product_tc(g, sms, (cudaStream_t)stream) : moe::launch_product_simt(g, sms, (cudaStream_t)stream);
+        e = g.elem == moe::kBF16 ? moe::launch_product_tc(g, sms, (cudaStream_t)stream) : moe::launch_product_f32(g, sms, (cudaStream_t)stream);
     MOE_CUDA(e);
     return MOE_OK;
 }
@@ -1408,9 +1408,8 @@ moe_status moe_int4_gemm(const void* x, int32_t dtype, int64_t ld_x, const uint8
     int sms = 0;
     if ((st = current_sms(&sms)) != MOE_OK) return st;
     moe::PdlScope scope(true);
-    MOE_CUDA(few_rows(rows, G)          ? moe::launch_int4_few(g, sms, (cudaStream_t)stream)
-             : g.elem == moe::kBF16 ? moe::launch_int4_tc(g, sms, (cudaStream_t)stream)
-                                    : moe::launch_int4_simt(g, sms, (cudaStream_t)stream));
+    MOE_CUDA(g.elem == moe::kBF16 && !few_rows(rows, G) ? moe::launch_int4_tc(g, sms, (cudaStream_t)stream)
+                                                       : moe::launch_int4_few(g, sms, (cudaStream_t)stream));
     return MOE_OK;
 }
 

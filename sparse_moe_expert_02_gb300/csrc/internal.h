@@ -308,7 +308,7 @@ struct GroupProduct {
     int64_t spin_ns;
 };
 constexpr int kProductMaxG = 1025;
-cudaError_t launch_product_simt(const GroupProduct& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_product_f32(const GroupProduct& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_product_tc(const GroupProduct& p, int num_sms, cudaStream_t stream);  // bf16
 // kProductFwd, bf16, K a multiple of 8, w aligned to 16 bytes (else cudaErrorNotSupported).
 cudaError_t launch_product_few(const GroupProduct& p, int num_sms, cudaStream_t stream);
@@ -353,7 +353,6 @@ struct Int4Product {
     uint32_t* err;
     int64_t spin_ns;
 };
-cudaError_t launch_int4_simt(const Int4Product& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_int4_tc(const Int4Product& p, int num_sms, cudaStream_t stream);  // bf16 rows
 cudaError_t launch_int4_few(const Int4Product& p, int num_sms, cudaStream_t stream);
 

@@ -1,0 +1,172 @@
+// Products of rows grouped by expert in fp32 arithmetic, on the CUDA cores:
+// out[m][n] = sum_k A(m, k) B(n, k) with the operands of ProductOp.
+//
+// Tiles of BM x BM, K in steps through a ring of kStages steps in shared
+// memory.  Elements come by cp.async one by one, along whichever dimension is
+// contiguous, to where the products read them: any strides and alignment, and
+// zeros beyond the edges, without registers between.  Tiles of 128 where they
+// fill the GPU twice (a thread's 8 x 8 sums need the fewest reads of shared
+// memory), of 64 or 32 where there are fewer: a short call is bound by one
+// block's way through K.
+#include <algorithm>
+
+#include "common.cuh"
+#include "groups.cuh"
+#include "internal.h"
+#include "tc_ptx.cuh"
+
+namespace moe {
+namespace f32 {
+
+constexpr int kThreads = 256;
+
+template <int BM> struct Tile {
+    static constexpr int BK = BM == 32 ? 32 : 16, kStages = BM == 128 ? 3 : 4, TM = BM / 16, LD = BM + 4;
+    static constexpr int V = TM < 4 ? TM : 4;  // floats of a read
+    static constexpr int kBytes = kStages * 2 * BK * LD * 4;
+    static constexpr int kBlocks = BM == 128 ? 2 : 4;  // an SM
+    // the thread's i-th row or column
+    __device__ __forceinline__ static int at(int i, int t) { return (i / V) * 16 * V + t * V + i % V; }
+};
+
+// Four bytes to shared memory, or zeros.
+__device__ __forceinline__ void copy4(uint32_t dst, const float* src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void wait_all_but() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+template <int OP, int BM>
+__global__ void __launch_bounds__(kThreads, Tile<BM>::kBlocks) product_f32_kernel(const GroupProduct p) {
+    using T = Tile<BM>;
+    constexpr int TM = T::TM, BK = T::BK, LD = T::LD, kEach = BM * BK / kThreads;
+    constexpr bool kAK = OP != kProductDw, kBK = OP == kProductFwd;  // contiguous along the sum
+    extern __shared__ __align__(16) float ring[];                    // [stage][A, B][BK][LD]
+    __shared__ GroupTable tab;
+    const float *a = (const float*)p.a, *b = (const float*)p.b;
+    const int64_t ldb = OP == kProductDw ? p.ldb : p.K;
+    pdl_wait();
+    if (threadIdx.x < 32) group_table(tab, p.offsets, p.G, p.rows, BM);
+    __syncthreads();
+    pdl_release();
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int cols = OP == kProductFwd ? p.N : p.K;  // of the output
+    const int cb = (cols + BM - 1) / BM, nb = (p.N + BM - 1) / BM;
+    const int64_t units = OP == kProductDw ? (int64_t)p.G * nb * cb : (int64_t)tab.tiles[p.G] * cb;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int t = (int)(u / cb), c0 = (int)(u - (int64_t)t * cb) * BM;
+        int g, i0, i1, k0, k1;  // rows of the tile [i0, i1), the sum's range
+        if (OP == kProductDw) {
+            g = t / nb;
+            i0 = (t - g * nb) * BM;
+            i1 = p.N;
+            k0 = tab.first[g];
+            k1 = tab.last[g];
+        } else {
+            g = find_group_smem(tab.tiles, p.G, t);
+            i0 = tab.first[g] + (t - tab.tiles[g]) * BM;
+            i1 = tab.last[g];
+            k0 = 0;
+            k1 = OP == kProductFwd ? p.K : p.N;
+        }
+        const int64_t brow = OP == kProductDw ? 0 : (int64_t)g * p.N;  // row of B that its index 0 is
+        auto fetch = [&](int step) {
+            const int k = k0 + step * BK;
+            if (k < k1) {
+                const uint32_t sa = tc::smem_u32(ring) + (step % T::kStages) * (2 * BK * LD * 4), sb = sa + BK * LD * 4;
+#pragma unroll
+                for (int j = 0; j < kEach; ++j) {
+                    const int e = tid + j * kThreads;
+                    const int ai = kAK ? e / BK : e % BM, ak = kAK ? e % BK : e / BM;
+                    const int bi = kBK ? e / BK : e % BM, bk = kBK ? e % BK : e / BM;
+                    const bool ain = i0 + ai < i1 && k + ak < k1, bin = c0 + bi < cols && k + bk < k1;
+                    const int64_t aat = kAK ? (int64_t)(i0 + ai) * p.lda + k + ak : (int64_t)(k + ak) * p.lda + i0 + ai;
+                    const int64_t bat = kBK ? (brow + c0 + bi) * ldb + k + bk : (brow + k + bk) * ldb + c0 + bi;
+                    copy4(sa + (ak * LD + ai) * 4, ain ? a + aat : a, ain);
+                    copy4(sb + (bk * LD + bi) * 4, bin ? b + bat : b, bin);
+                }
+            }
+            commit();  // (a group a step, empty past the end)
+        };
+        float acc[TM][TM] = {};
+        const int steps = (k1 - k0 + BK - 1) / BK;
+        for (int s = 0; s < T::kStages - 1; ++s) fetch(s);
+        for (int s = 0; s < steps; ++s) {
+            wait_all_but<T::kStages - 2>();
+            __syncthreads();  // the step is here for everyone, and everyone is done with the one before
+            fetch(s + T::kStages - 1);
+            const float* sa = ring + (s % T::kStages) * (2 * BK * LD);
+            const float* sb = sa + BK * LD;
+#pragma unroll
+            for (int kk = 0; kk < BK; ++kk) {
+                float x[TM], y[TM];
+#pragma unroll
+                for (int h = 0; h < TM / T::V; ++h) {
+                    const float *px = sa + kk * LD + T::at(h * T::V, ty), *py = sb + kk * LD + T::at(h * T::V, tx);
+                    if constexpr (T::V == 4) {
+                        *(float4*)(x + 4 * h) = *(const float4*)px;
+                        *(float4*)(y + 4 * h) = *(const float4*)py;
+                    } else {
+                        *(float2*)x = *(const float2*)px;
+                        *(float2*)y = *(const float2*)py;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+#pragma unroll
+                    for (int j = 0; j < TM; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+            }
+        }
+        wait_all_but<0>();
+        __syncthreads();  // the ring is free for the next unit
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const int r = i0 + T::at(i, ty);
+            if (r >= i1) continue;
+            const int64_t at = (OP == kProductDw ? (int64_t)g * p.N + r : (int64_t)r) * p.ldo;
+#pragma unroll
+            for (int j = 0; j < TM; ++j) {
+                const int c = c0 + T::at(j, tx);
+                if (c >= cols) continue;
+                float v = acc[i][j];
+                if (p.out_elem == kF32) {
+                    float* o = (float*)p.out + at + c;
+                    *o = OP == kProductDw && p.accumulate ? *o + v : v;
+                } else {
+                    bf16* o = (bf16*)p.out + at + c;
+                    *o = __float2bfloat16_rn(OP == kProductDw && p.accumulate ? to_f32(*o) + v : v);
+                }
+            }
+        }
+    }
+}
+
+template <int OP, int BM> cudaError_t launch(const GroupProduct& g, int64_t units, int num_sms, cudaStream_t s) {
+    cudaError_t e = ensure_smem_attr((const void*)product_f32_kernel<OP, BM>, Tile<BM>::kBytes);
+    if (e != cudaSuccess) return e;
+    e = launch_kernel(product_f32_kernel<OP, BM>, dim3((unsigned)std::min<int64_t>(units, Tile<BM>::kBlocks * num_sms)), dim3(kThreads),
+                      Tile<BM>::kBytes, s, 1, g);
+    count_launches(1);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int OP> cudaError_t launch_op(const GroupProduct& g, int num_sms, cudaStream_t s) {
+    const int64_t cols = OP == kProductFwd ? g.N : g.K;
+    auto units = [&](int64_t bm) {  // at most
+        if (OP == kProductDw) return g.G * cdiv(g.N, bm) * cdiv(cols, bm);
+        return (cdiv(g.rows, bm) + std::min(g.G - 1, g.rows)) * cdiv(cols, bm);
+    };
+    if (units(128) >= 2 * num_sms) return launch<OP, 128>(g, units(128), num_sms, s);
+    if (units(64) >= 2 * num_sms) return launch<OP, 64>(g, units(64), num_sms, s);
+    return launch<OP, 32>(g, units(32), num_sms, s);
+}
+
+}  // namespace f32
+
+cudaError_t launch_product_f32(const GroupProduct& g, int num_sms, cudaStream_t stream) {
+    if (g.op == kProductFwd) return f32::launch_op<kProductFwd>(g, num_sms, stream);
+    if (g.op == kProductDx) return f32::launch_op<kProductDx>(g, num_sms, stream);
+    return f32::launch_op<kProductDw>(g, num_sms, stream);
+}
+
+}  // namespace moe

@@ -72,7 +72,7 @@ template <int LG, typename TS> __device__ __forceinline__ float scale_of(const C
 
 // Units are (row tile, feature tile).  list: group and tile within it of each
 // row tile, so that a block finds its next unit without a search.
-constexpr int kMaxTiles = 2 * kProductMaxG;  // rows <= 16 G
+constexpr int kMaxTiles = 2 * kProductMaxG;  // (16 rows a group; fp32 rows may be more)
 struct Tables {
     GroupTable groups;
     uint32_t list[kMaxTiles];
@@ -81,13 +81,18 @@ struct Tables {
 struct Unit {
     int g, f0, row0, n;  // group, first feature, first row of the tile and how many
 };
-__device__ __forceinline__ Unit unit_at(int u, int FB, const Tables& t) {
+__device__ __forceinline__ Unit unit_at(int u, int FB, int G, const Tables& t) {
     Unit r;
     const int rt = u / FB;
     r.f0 = (u - rt * FB) * kF;
-    const uint32_t e = t.list[rt];
-    r.g = (int)(e & 2047u);
-    r.row0 = t.groups.first[r.g] + (int)(e >> 11) * kRows;
+    if (t.groups.tiles[G] <= kMaxTiles) {
+        const uint32_t e = t.list[rt];
+        r.g = (int)(e & 2047u);
+        r.row0 = t.groups.first[r.g] + (int)(e >> 11) * kRows;
+    } else {
+        r.g = find_group_smem(t.groups.tiles, G, rt);
+        r.row0 = t.groups.first[r.g] + (rt - t.groups.tiles[r.g]) * kRows;
+    }
     r.n = min(kRows, t.groups.last[r.g] - r.row0);
     return r;
 }
@@ -187,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, MOE_FEW_BLOCKS) product_few_kernel(c
     if (warp == 0) group_table(tab.groups, p.offsets, p.G, p.rows, kRows);
     __syncthreads();
     pdl_release();
-    for (int i = threadIdx.x; i < p.G; i += kThreads)
+    for (int i = threadIdx.x; i < p.G && tab.groups.tiles[p.G] <= kMaxTiles; i += kThreads)
         for (int j = tab.groups.tiles[i], n = 0; j < tab.groups.tiles[i + 1]; ++j, ++n) tab.list[j] = (uint32_t)i | (uint32_t)n << 11;
     __syncthreads();
     const int FB = (p.N + kF - 1) / kF, units = tab.groups.tiles[p.G] * FB, step = gridDim.x;
@@ -203,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, MOE_FEW_BLOCKS) product_few_kernel(c
     const uint8_t* wp[2];                   // its part of the batch's first chunk
     int64_t sp[2];                          // first scale of that chunk
     const int lane_k = LG ? (p.K - 32 * t + kChunk - 1) / kChunk - k0 : nk;  // chunks with a code of this lane
-    Unit fc = unit_at(fu, FB, tab), cur = fc;
+    Unit fc = unit_at(fu, FB, p.G, tab), cur = fc;
     auto locate = [&]() {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -275,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, MOE_FEW_BLOCKS) product_few_kernel(c
         for (int b = 0; b < batches; ++b) {
             if (++fb == batches) {
                 fb = 0;
-                if ((fu += step) < units) fc = unit_at(fu, FB, tab);
+                if ((fu += step) < units) fc = unit_at(fu, FB, p.G, tab);
                 locate();
             } else {
 #pragma unroll
@@ -398,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, MOE_FEW_BLOCKS) product_few_kernel(c
             else ((bf16*)p.out)[at] = __float2bfloat16_rn(v);
         }
         if (u + step < units) {
-            cur = batches ? fc : unit_at(u + step, FB, tab);
+            cur = batches ? fc : unit_at(u + step, FB, p.G, tab);
             rows_at();
         }
     }
@@ -442,7 +447,6 @@ cudaError_t launch_product_few(const GroupProduct& g, int num_sms, cudaStream_t 
 
 cudaError_t launch_int4_few(const Int4Product& g, int num_sms, cudaStream_t stream) {
     using namespace few_rows;
-    if (g.rows > kRows * (int64_t)g.G) return cudaErrorNotSupported;
     Args a = {};
     a.offsets = g.offsets;
     a.rows = g.rows;

@@ -47,7 +47,7 @@ constexpr int BF = 128, BK = 64, kMaxI = 256;  // f and c of a stage, i of a til
 constexpr int kLine = 128;                     // bytes
 constexpr int kFBytes = BF * BK * 2;
 constexpr int kMaxStages = 8;
-constexpr int kEpiWarps = 8, kFeedWarps = 8;
+constexpr int kEpiWarps = 8, kFeedWarps = 8, kFeedGroup = 4;  // feed warps; those that fill one stage
 constexpr int kThreads = 32 * (2 + kEpiWarps), kThreadsFeed = kThreads + 32 * kFeedWarps;
 constexpr int kMaxSplit = 8;
 constexpr int kRing = 4 * (kFBytes + kMaxI * BK * 2);
@@ -162,18 +162,18 @@ template <int MODE> __device__ __forceinline__ uint32_t load_pair(const bf16* p,
     return lo | hi << 16;
 }
 
-// Lines base, base + kFeedWarps, ... below `lines` of an operand to shared
+// Lines first, first + kFeedGroup, ... below `lines` of an operand to shared
 // memory at dst, kBatch of them in flight.  along_c: a line is 64 c of row
 // `line`; else 64 rows (columns of the tensor) of one c, 64 lines a block.
 template <int MODE>
 __device__ __forceinline__ void copy_lines(uint32_t dst, const bf16* src, int64_t ld, bool along_c, int lines, int valid_rows, int c_left,
                                            int first, int c16, int lane) {
     constexpr int kBatch = 16;
-    for (int l0 = first; l0 < lines; l0 += kBatch * kFeedWarps) {
+    for (int l0 = first; l0 < lines; l0 += kBatch * kFeedGroup) {
         uint32_t v[kBatch];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-            const int l = l0 + j * kFeedWarps;
+            const int l = l0 + j * kFeedGroup;
             v[j] = 0;
             if (l >= lines) continue;
             if (along_c) {
@@ -185,7 +185,7 @@ __device__ __forceinline__ void copy_lines(uint32_t dst, const bf16* src, int64_
         }
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-            const int l = l0 + j * kFeedWarps;
+            const int l = l0 + j * kFeedGroup;
             if (l >= lines || (!along_c && (l & (BK - 1)) >= c16)) continue;
             const uint32_t a = dst + l * kLine + (((lane >> 2) ^ (l & 7)) << 4) + ((lane & 3) << 2);
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v[j]) : "memory");
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(FEED == kTma ? kThreads : kThreadsFeed, 1)
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const bool f_tma = FEED == kTma || (FEED == kCopy && !p.f_copy), r_tma = FEED == kTma || !p.r_copy;
     if (threadIdx.x == 0) {
-        const int feeders = (f_tma || r_tma ? 1 : 0) + (FEED == kTma ? 0 : kFeedWarps);
+        const int feeders = (f_tma || r_tma ? 1 : 0) + (FEED == kTma ? 0 : kFeedGroup);
         for (int s = 0; s < S; ++s) {
             mbar_init(full0 + 8 * s, feeders);
             mbar_init(empty0 + 8 * s, 1);
@@ -376,72 +376,86 @@ __global__ void __launch_bounds__(FEED == kTma ? kThreads : kThreadsFeed, 1)
         mbar_wait(drain, 0, 1000000000LL, &never);
     } else if (FEED != kTma && warp >= 2 + kEpiWarps) {
         // -------------------------------------------- copied or coded operands
-        const int fw = warp - 2 - kEpiWarps, t = threadIdx.x - kThreads;
-        int stage = 0;
+        // Two groups of four warps fill stages in turn, so that one's latency
+        // (a wait, loads, a proxy fence, an arrival) passes beside the other's.
+        const int fw = (warp - 2 - kEpiWarps) & (kFeedGroup - 1), mine = (warp - 2 - kEpiWarps) / kFeedGroup;
+        const int t = (threadIdx.x - kThreads) & (32 * kFeedGroup - 1);
+        int stage = 0, turn = 0;
         uint32_t phase = 0;
         bool ok = true;
         for (int u = u0; u < units && ok; u += step) {
             const Unit un = unit_at<OP>(p, u, FB, NB, tab);
             const int2 kb = my_blocks(un, rank, cl);
-            // codes: thread t takes half a line (32 codes, one scale) of feature t / 2
-            const int64_t wrow = (int64_t)un.g * p.N + un.f0 + (t >> 1);
-            const bool in = un.f0 + (t >> 1) < p.N;
+            // codes: thread t takes the line (64 codes, a scale or two) of feature t
+            const int64_t wrow = (int64_t)un.g * p.N + un.f0 + t;
+            const bool in = un.f0 + t < p.N;
             const int nbk = (p.K + p.w.group - 1) / p.w.group;
-            constexpr int kAhead = 3;
-            uint4 q[kAhead];
-            float sc[kAhead];
-            int zp[kAhead];
-            auto fetch = [&](int k, uint4& v, float& s, int& z) {
-                const int c = k * BK + 32 * (t & 1);
-                v = make_uint4(0, 0, 0, 0);
-                s = 0.0f;
-                z = 0;
-                if (!in || k >= kb.y || c >= p.K) return;
-                v = __ldg((const uint4*)(p.w.codes + wrow * (p.K / 2) + c / 2));
-                const int64_t at = wrow * nbk + c / p.w.group;
-                s = FEED == kCodes16 ? to_f32(((const bf16*)p.w.scales)[at]) : ((const float*)p.w.scales)[at];
-                z = p.w.zeros ? p.w.zeros[at] : 8;
+            constexpr int kAhead = 2;
+            uint4 q[kAhead][2];
+            float sc[kAhead][2];
+            int zp[kAhead][2];
+            auto fetch = [&](int k, uint4 (&v)[2], float (&s)[2], int (&z)[2]) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int c = k * BK + 32 * h;
+                    v[h] = make_uint4(0, 0, 0, 0);
+                    s[h] = 0.0f;
+                    z[h] = 0;
+                    if (!in || k >= kb.y || c >= p.K) continue;
+                    v[h] = __ldg((const uint4*)(p.w.codes + wrow * (p.K / 2) + c / 2));
+                    const int64_t at = wrow * nbk + c / p.w.group;
+                    s[h] = FEED == kCodes16 ? to_f32(((const bf16*)p.w.scales)[at]) : ((const float*)p.w.scales)[at];
+                    z[h] = p.w.zeros ? p.w.zeros[at] : 8;
+                }
             };
+            const int first = kb.x + (turn ^ mine);  // this group's first block of the unit
             if (FEED >= kCodes16) {
 #pragma unroll
-                for (int i = 0; i < kAhead; ++i) fetch(kb.x + i, q[i], sc[i], zp[i]);
+                for (int i = 0; i < kAhead; ++i) fetch(first + 2 * i, q[i], sc[i], zp[i]);
             }
-            for (int k0 = kb.x; k0 < kb.y && ok; k0 += kAhead) {
+            for (int k0 = kb.x; k0 < kb.y && ok; k0 += 2 * kAhead) {
 #pragma unroll
-                for (int i = 0; i < kAhead; ++i) {
+                for (int i = 0; i < 2 * kAhead; ++i) {
                     const int k = k0 + i;
                     if (k >= kb.y || !ok) break;
-                    ok = __all_sync(0xffffffffu, mbar_wait(empty0 + 8 * stage, phase ^ 1, lim, abort_flag));
-                    if (!ok) break;
-                    const int c = un.c0 + k * BK, left = un.c1 - c, c16 = min(4, (left + 15) >> 4) * 16;
-                    const uint32_t fs = smem0 + stage * p.stage_bytes, rs = fs + kFBytes;
-                    if (FEED >= kCodes16) {
-                        const uint32_t row = fs + (t >> 1) * kLine;
-                        const __nv_bfloat162 z = int4_zero(zp[i]);
-                        const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+                    if (turn == mine) {
+                        ok = __all_sync(0xffffffffu, mbar_wait(empty0 + 8 * stage, phase ^ 1, lim, abort_flag));
+                        if (!ok) break;
+                        const int c = un.c0 + k * BK, left = un.c1 - c, c16 = min(4, (left + 15) >> 4) * 16;
+                        const uint32_t fs = smem0 + stage * p.stage_bytes, rs = fs + kFBytes;
+                        if (FEED >= kCodes16) {
+                            const uint32_t row = fs + t * kLine;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint4 v = values8<FEED>(w[j], z, sc[i]);
-                            if (c + 32 * (t & 1) >= p.K) v = make_uint4(0, 0, 0, 0);
-                            st_shared16(row + (((4 * (t & 1) + j) ^ ((t >> 1) & 7)) << 4), v);
+                            for (int h = 0; h < 2; ++h) {
+                                const uint4 v = q[i / 2][h];
+                                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                                const __nv_bfloat162 z = int4_zero(zp[i / 2][h]);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    uint4 o = values8<FEED>(w[j], z, sc[i / 2][h]);
+                                    if (c + 32 * h >= p.K) o = make_uint4(0, 0, 0, 0);
+                                    st_shared16(row + (((4 * h + j) ^ (t & 7)) << 4), o);
+                                }
+                            }
+                            fetch(k + 2 * kAhead, q[i / 2], sc[i / 2], zp[i / 2]);
+                        } else if (p.f_copy) {
+                            const bf16* src = OP == kProductFwd   ? p.f + ((int64_t)un.g * p.N + un.f0) * p.ldf + c
+                                              : OP == kProductDx ? p.f + ((int64_t)un.g * p.N + c) * p.ldf + un.f0
+                                                                 : p.f + (int64_t)c * p.ldf + un.f0;
+                            if (p.f_copy == 2) copy_lines<2>(fs, src, p.ldf, kFAlongC, BF, F - un.f0, left, fw, c16, lane);
+                            else copy_lines<1>(fs, src, p.ldf, kFAlongC, BF, F - un.f0, left, fw, c16, lane);
                         }
-                        fetch(k + kAhead, q[i], sc[i], zp[i]);
-                    } else if (p.f_copy) {
-                        const bf16* src = OP == kProductFwd   ? p.f + ((int64_t)un.g * p.N + un.f0) * p.ldf + c
-                                          : OP == kProductDx ? p.f + ((int64_t)un.g * p.N + c) * p.ldf + un.f0
-                                                             : p.f + (int64_t)c * p.ldf + un.f0;
-                        if (p.f_copy == 2) copy_lines<2>(fs, src, p.ldf, kFAlongC, BF, F - un.f0, left, fw, c16, lane);
-                        else copy_lines<1>(fs, src, p.ldf, kFAlongC, BF, F - un.f0, left, fw, c16, lane);
+                        if (p.r_copy) {
+                            const bf16* src = kRAlongC ? p.r + (int64_t)un.i0 * p.ldr + c : p.r + (int64_t)c * p.ldr + un.i0;
+                            const int lines = kRAlongC ? (un.n + 15) & ~15 : ((un.n + 63) & ~63);
+                            if (p.r_copy == 2) copy_lines<2>(rs, src, p.ldr, kRAlongC, lines, un.n, left, fw, c16, lane);
+                            else copy_lines<1>(rs, src, p.ldr, kRAlongC, lines, un.n, left, fw, c16, lane);
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(full0 + 8 * stage);
                     }
-                    if (p.r_copy) {
-                        const bf16* src = kRAlongC ? p.r + (int64_t)un.i0 * p.ldr + c : p.r + (int64_t)c * p.ldr + un.i0;
-                        const int lines = kRAlongC ? (un.n + 15) & ~15 : ((un.n + 63) & ~63);
-                        if (p.r_copy == 2) copy_lines<2>(rs, src, p.ldr, kRAlongC, lines, un.n, left, fw, c16, lane);
-                        else copy_lines<1>(rs, src, p.ldr, kRAlongC, lines, un.n, left, fw, c16, lane);
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(full0 + 8 * stage);
+                    turn ^= 1;
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1;
@@ -639,17 +653,25 @@ template <int OP> cudaError_t plan_and_launch(const Maps& m, Args& a, int feed, 
     // i of a tile: as many as the groups fill (F is read once per tile), fewer
     // where they do not, for more stages in flight.
     const int64_t avg = OP == kProductDw ? a.N : cdiv(a.rows, a.G);
-    a.tile_i = avg > 128 ? 256 : avg > (OP == kProductDw ? 64 : 32) ? 128 : 64;
-    a.stage_bytes = kFBytes + a.tile_i * BK * 2;
-    a.stages = std::min(kMaxStages, kRing / a.stage_bytes);
     const int F = OP == kProductFwd ? a.N : a.K;
     const int64_t fb = cdiv(F, BF);
-    const int64_t tiles = OP == kProductDw ? a.G * cdiv(a.N, a.tile_i) : cdiv(a.rows, a.tile_i) + std::min(a.G - 1, a.rows);
-    const int64_t units = tiles * fb;  // at most
-    const int64_t kb = cdiv(OP == kProductFwd ? a.K : OP == kProductDx ? a.N : cdiv(a.rows, a.G), BK);
+    auto units = [&](int ti) {  // at most
+        return (OP == kProductDw ? a.G * cdiv(a.N, ti) : cdiv(a.rows, ti) + std::min(a.G - 1, a.rows)) * fb;
+    };
+    a.tile_i = avg > 128 ? 256 : avg > (OP == kProductDw ? 64 : 32) ? 128 : 64;
+    while (a.tile_i > 64 && units(a.tile_i) * 2 <= num_sms) a.tile_i /= 2;  // (few tiles: smaller ones on more SMs)
+    if (OP != kProductDw && a.G == 1 && a.tile_i == 256) {
+        // One matrix: as many tiles as the same number of rounds holds, of equal size.
+        const int64_t tiles = cdiv(units(256), num_sms) * num_sms / fb;
+        if (tiles > 0) a.tile_i = (int)std::min<int64_t>(256, cdiv(cdiv(a.rows, tiles), 16) * 16);
+    }
+    a.stage_bytes = kFBytes + (int)cdiv(a.tile_i, 64) * 64 * BK * 2;
+    a.stages = std::min(kMaxStages, kRing / a.stage_bytes);
+    // dw: a group's rows, at most (an average would leave the largest to one CTA)
+    const int64_t kb = cdiv(OP == kProductFwd ? a.K : OP == kProductDx ? a.N : a.rows, BK);
     a.split = 1;
-    while (a.split < kMaxSplit && units * a.split * 2 <= num_sms && kb >= 4 * a.split) a.split *= 2;
-    const int grid = a.split > 1 ? (int)units * a.split : (int)std::min<int64_t>(units, num_sms);
+    while (a.split < kMaxSplit && units(a.tile_i) * a.split * 2 <= num_sms && kb >= 4 * a.split) a.split *= 2;
+    const int grid = a.split > 1 ? (int)units(a.tile_i) * a.split : (int)std::min<int64_t>(units(a.tile_i), num_sms);
 #define MOE_PTC(FEED) (a.split > 1 ? launch<OP, FEED, true>(m, a, grid, s) : launch<OP, FEED, false>(m, a, grid, s))
     if (feed == kTma) return MOE_PTC(kTma);
     if constexpr (OP == kProductFwd) {
