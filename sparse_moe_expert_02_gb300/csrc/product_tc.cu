@@ -37,8 +37,8 @@ namespace ptc {
 
 using namespace tc;
 
-// Where a stage's operands come from: TMA alone; or the line of an operand
-// that TMA cannot read (rows not aligned to 16 bytes) copied by eight warps;
+// Where a stage's operands come from: TMA alone; or the lines of an
+// operand that TMA cannot read (rows not aligned to 16 bytes) copied by warps;
 // or the F operand's 4-bit codes turned into bf16 by them (bf16 or fp32
 // scales), R by TMA or copied.
 enum Feed { kTma = 0, kCopy = 1, kCodes16 = 2, kCodes32 = 3 };
@@ -47,8 +47,12 @@ constexpr int BF = 128, BK = 64, kMaxI = 256;  // f and c of a stage, i of a til
 constexpr int kLine = 128;                     // bytes
 constexpr int kFBytes = BF * BK * 2;
 constexpr int kMaxStages = 8;
-constexpr int kEpiWarps = 8, kFeedWarps = 8, kFeedGroup = 4;  // feed warps; those that fill one stage
-constexpr int kThreads = 32 * (2 + kEpiWarps), kThreadsFeed = kThreads + 32 * kFeedWarps;
+// Epilogue warps, and groups of four warps that feed stages: codes take many
+// instructions, so four groups, and fewer epilogue warps for their registers.
+constexpr int kEpiWarps = 8, kFeedGroup = 4;
+__host__ __device__ constexpr int epi_warps(int feed) { return feed >= kCodes16 ? 4 : kEpiWarps; }
+__host__ __device__ constexpr int feed_groups(int feed) { return feed >= kCodes16 ? 4 : feed == kCopy ? 2 : 0; }
+__host__ __device__ constexpr int threads_for(int feed) { return 32 * (2 + epi_warps(feed) + kFeedGroup * feed_groups(feed)); }
 constexpr int kMaxSplit = 8;
 constexpr int kRing = 4 * (kFBytes + kMaxI * BK * 2);
 constexpr int kStWarp = 8 * 32 * 4;            // 8 row pairs x 32 features, two bf16 a word
@@ -193,8 +197,8 @@ __device__ __forceinline__ void copy_lines(uint32_t dst, const bf16* src, int64_
     }
 }
 
-// Eight codes' values, rounded to bf16 once.
-template <int FEED> __device__ __forceinline__ uint4 values8(uint32_t w, __nv_bfloat162 z, float s) {
+// Eight codes' values, rounded to bf16 once.  s: the scale's bits.
+template <int FEED> __device__ __forceinline__ uint4 values8(uint32_t w, __nv_bfloat162 z, uint32_t s) {
     uint32_t o[4];
     int4_pairs(w, z, o);
 #pragma unroll
@@ -202,11 +206,11 @@ template <int FEED> __device__ __forceinline__ uint4 values8(uint32_t w, __nv_bf
         const __nv_bfloat162 d = *(const __nv_bfloat162*)&o[j];
         __nv_bfloat162 v;
         if (FEED == kCodes16) {
-            const bf16 sb = __float2bfloat16_rn(s);  // exact: it was a bf16
-            v = __hmul2(d, __nv_bfloat162(sb, sb));
+            const uint32_t ss = s * 0x10001u;
+            v = __hmul2(d, *(const __nv_bfloat162*)&ss);
         } else {
             const float2 x = __bfloat1622float2(d);
-            v = __floats2bfloat162_rn(x.x * s, x.y * s);
+            v = __floats2bfloat162_rn(x.x * __uint_as_float(s), x.y * __uint_as_float(s));
         }
         o[j] = *(const uint32_t*)&v;
     }
@@ -214,10 +218,11 @@ template <int FEED> __device__ __forceinline__ uint4 values8(uint32_t w, __nv_bf
 }
 
 template <int OP, int FEED, bool SPLIT>
-__global__ void __launch_bounds__(FEED == kTma ? kThreads : kThreadsFeed, 1)
+__global__ void __launch_bounds__(threads_for(FEED), 1)
     product_tc_kernel(const __grid_constant__ CUtensorMap tm_f, const __grid_constant__ CUtensorMap tm_f16,
                       const __grid_constant__ CUtensorMap tm_r, const __grid_constant__ CUtensorMap tm_r16, const Args p) {
     constexpr bool kFAlongC = OP == kProductFwd, kRAlongC = OP != kProductDw;
+    constexpr int kEpi = epi_warps(FEED), kHalves = kEpi / 4;  // warps for each lane quarter
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* bars = (uint64_t*)(smem + kOffBar);
     const int S = p.stages;
@@ -237,7 +242,7 @@ __global__ void __launch_bounds__(FEED == kTma ? kThreads : kThreadsFeed, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull0 + 8 * b, 1);
-            mbar_init(tempty0 + 8 * b, kEpiWarps);
+            mbar_init(tempty0 + 8 * b, kEpi);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -374,14 +379,14 @@ __global__ void __launch_bounds__(FEED == kTma ? kThreads : kThreadsFeed, 1)
         __syncwarp();
         volatile int never = 0;
         mbar_wait(drain, 0, 1000000000LL, &never);
-    } else if (FEED != kTma && warp >= 2 + kEpiWarps) {
+    } else if (FEED != kTma && warp >= 2 + kEpi) {
         // -------------------------------------------- copied or coded operands
-        // Two groups of four warps fill stages in turn, so that one's latency
-        // (a wait, loads, a proxy fence, an arrival) passes beside the other's.
-        const int fw = (warp - 2 - kEpiWarps) & (kFeedGroup - 1), mine = (warp - 2 - kEpiWarps) / kFeedGroup;
-        const int t = (threadIdx.x - kThreads) & (32 * kFeedGroup - 1);
-        int stage = 0, turn = 0;
-        uint32_t phase = 0;
+        // Groups of four warps fill stages in turn, so that one's latency (a
+        // wait, loads, a proxy fence, an arrival) passes beside the others'.
+        constexpr int kGroups = feed_groups(FEED);
+        const int fw = (warp - 2 - kEpi) & (kFeedGroup - 1), mine = (warp - 2 - kEpi) / kFeedGroup;
+        const int t = (threadIdx.x - 32 * (2 + kEpi)) & (32 * kFeedGroup - 1);
+        int64_t done = 0;  // blocks of the units before
         bool ok = true;
         for (int u = u0; u < units && ok; u += step) {
             const Unit un = unit_at<OP>(p, u, FB, NB, tab);
@@ -390,76 +395,63 @@ __global__ void __launch_bounds__(FEED == kTma ? kThreads : kThreadsFeed, 1)
             const int64_t wrow = (int64_t)un.g * p.N + un.f0 + t;
             const bool in = un.f0 + t < p.N;
             const int nbk = (p.K + p.w.group - 1) / p.w.group;
-            constexpr int kAhead = 2;
-            uint4 q[kAhead][2];
-            float sc[kAhead][2];
-            int zp[kAhead][2];
-            auto fetch = [&](int k, uint4 (&v)[2], float (&s)[2], int (&z)[2]) {
+            uint4 q[2];
+            uint32_t sc[2], zp[2];  // as loaded: converting would wait for the load
+            auto fetch = [&](int k) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int c = k * BK + 32 * h;
-                    v[h] = make_uint4(0, 0, 0, 0);
-                    s[h] = 0.0f;
-                    z[h] = 0;
+                    q[h] = make_uint4(0, 0, 0, 0);
+                    sc[h] = zp[h] = 0;  // (0 - 0) * 0
                     if (!in || k >= kb.y || c >= p.K) continue;
-                    v[h] = __ldg((const uint4*)(p.w.codes + wrow * (p.K / 2) + c / 2));
+                    q[h] = __ldg((const uint4*)(p.w.codes + wrow * (p.K / 2) + c / 2));
                     const int64_t at = wrow * nbk + c / p.w.group;
-                    s[h] = FEED == kCodes16 ? to_f32(((const bf16*)p.w.scales)[at]) : ((const float*)p.w.scales)[at];
-                    z[h] = p.w.zeros ? p.w.zeros[at] : 8;
+                    sc[h] = FEED == kCodes16 ? __ldg((const uint16_t*)p.w.scales + at) : __ldg((const uint32_t*)p.w.scales + at);
+                    zp[h] = 8;
+                    if (p.w.zeros) zp[h] = __ldg(p.w.zeros + at);
                 }
             };
-            const int first = kb.x + (turn ^ mine);  // this group's first block of the unit
-            if (FEED >= kCodes16) {
+            const int skip = (mine - (int)(done % kGroups) + kGroups) % kGroups;  // to this group's first block
+            const int64_t at0 = done + skip;
+            int stage = (int)(at0 % S);
+            uint32_t phase = (uint32_t)(at0 / S) & 1;
+            done += kb.y - kb.x;
+            if (FEED >= kCodes16) fetch(kb.x + skip);
+            for (int k = kb.x + skip; k < kb.y; k += kGroups) {
+                ok = __all_sync(0xffffffffu, mbar_wait(empty0 + 8 * stage, phase ^ 1, lim, abort_flag));
+                if (!ok) break;
+                const int c = un.c0 + k * BK, left = un.c1 - c, c16 = min(4, (left + 15) >> 4) * 16;
+                const uint32_t fs = smem0 + stage * p.stage_bytes, rs = fs + kFBytes;
+                if (FEED >= kCodes16) {
+                    const uint32_t row = fs + t * kLine;
 #pragma unroll
-                for (int i = 0; i < kAhead; ++i) fetch(first + 2 * i, q[i], sc[i], zp[i]);
-            }
-            for (int k0 = kb.x; k0 < kb.y && ok; k0 += 2 * kAhead) {
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t w[4] = {q[h].x, q[h].y, q[h].z, q[h].w};
+                        const __nv_bfloat162 z = int4_zero((int)zp[h]);
 #pragma unroll
-                for (int i = 0; i < 2 * kAhead; ++i) {
-                    const int k = k0 + i;
-                    if (k >= kb.y || !ok) break;
-                    if (turn == mine) {
-                        ok = __all_sync(0xffffffffu, mbar_wait(empty0 + 8 * stage, phase ^ 1, lim, abort_flag));
-                        if (!ok) break;
-                        const int c = un.c0 + k * BK, left = un.c1 - c, c16 = min(4, (left + 15) >> 4) * 16;
-                        const uint32_t fs = smem0 + stage * p.stage_bytes, rs = fs + kFBytes;
-                        if (FEED >= kCodes16) {
-                            const uint32_t row = fs + t * kLine;
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const uint4 v = q[i / 2][h];
-                                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                                const __nv_bfloat162 z = int4_zero(zp[i / 2][h]);
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    uint4 o = values8<FEED>(w[j], z, sc[i / 2][h]);
-                                    if (c + 32 * h >= p.K) o = make_uint4(0, 0, 0, 0);
-                                    st_shared16(row + (((4 * h + j) ^ (t & 7)) << 4), o);
-                                }
-                            }
-                            fetch(k + 2 * kAhead, q[i / 2], sc[i / 2], zp[i / 2]);
-                        } else if (p.f_copy) {
-                            const bf16* src = OP == kProductFwd   ? p.f + ((int64_t)un.g * p.N + un.f0) * p.ldf + c
-                                              : OP == kProductDx ? p.f + ((int64_t)un.g * p.N + c) * p.ldf + un.f0
-                                                                 : p.f + (int64_t)c * p.ldf + un.f0;
-                            if (p.f_copy == 2) copy_lines<2>(fs, src, p.ldf, kFAlongC, BF, F - un.f0, left, fw, c16, lane);
-                            else copy_lines<1>(fs, src, p.ldf, kFAlongC, BF, F - un.f0, left, fw, c16, lane);
-                        }
-                        if (p.r_copy) {
-                            const bf16* src = kRAlongC ? p.r + (int64_t)un.i0 * p.ldr + c : p.r + (int64_t)c * p.ldr + un.i0;
-                            const int lines = kRAlongC ? (un.n + 15) & ~15 : ((un.n + 63) & ~63);
-                            if (p.r_copy == 2) copy_lines<2>(rs, src, p.ldr, kRAlongC, lines, un.n, left, fw, c16, lane);
-                            else copy_lines<1>(rs, src, p.ldr, kRAlongC, lines, un.n, left, fw, c16, lane);
-                        }
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(full0 + 8 * stage);
+                        for (int j = 0; j < 4; ++j) st_shared16(row + (((4 * h + j) ^ (t & 7)) << 4), values8<FEED>(w[j], z, sc[h]));
                     }
-                    turn ^= 1;
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
+                    fetch(k + kGroups);
+                } else if (p.f_copy) {
+                    const bf16* src = OP == kProductFwd   ? p.f + ((int64_t)un.g * p.N + un.f0) * p.ldf + c
+                                      : OP == kProductDx ? p.f + ((int64_t)un.g * p.N + c) * p.ldf + un.f0
+                                                         : p.f + (int64_t)c * p.ldf + un.f0;
+                    if (p.f_copy == 2) copy_lines<2>(fs, src, p.ldf, kFAlongC, BF, F - un.f0, left, fw, c16, lane);
+                    else copy_lines<1>(fs, src, p.ldf, kFAlongC, BF, F - un.f0, left, fw, c16, lane);
+                }
+                if (p.r_copy) {
+                    const bf16* src = kRAlongC ? p.r + (int64_t)un.i0 * p.ldr + c : p.r + (int64_t)c * p.ldr + un.i0;
+                    const int lines = kRAlongC ? (un.n + 15) & ~15 : ((un.n + 63) & ~63);
+                    if (p.r_copy == 2) copy_lines<2>(rs, src, p.ldr, kRAlongC, lines, un.n, left, fw, c16, lane);
+                    else copy_lines<1>(rs, src, p.ldr, kRAlongC, lines, un.n, left, fw, c16, lane);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full0 + 8 * stage);
+                stage += kGroups;
+                if (stage >= S) {
+                    stage -= S;
+                    phase ^= 1;
                 }
             }
         }
@@ -467,7 +459,7 @@ __global__ void __launch_bounds__(FEED == kTma ? kThreads : kThreadsFeed, 1)
     // ---------------------------------------------------------- epilogue
     // Lanes are f, columns i.
     const int ew = warp - 2, sub = warp & 3, half = ew >> 2;  // lane quarter, column half
-    const bool epi = ew >= 0 && ew < kEpiWarps;
+    const bool epi = ew >= 0 && ew < kEpi;
     if (!SPLIT && epi) {
         uint8_t* st = smem + kOffStage + ew * kStWarp;
         const bool vec = F % 8 == 0 && p.ldo % 8 == 0 && ((uintptr_t)p.out & 15) == 0;
@@ -496,9 +488,9 @@ __global__ void __launch_bounds__(FEED == kTma ? kThreads : kThreadsFeed, 1)
             }
             const int f = un.f0 + sub * 32, cols = F - f;  // this warp's f inside the matrix
             const int64_t row0 = OP == kProductDw ? (int64_t)un.g * p.N + un.i0 : (int64_t)un.i0;
-            // this half's 32-row blocks: 0, 2, 4, 6 or 1, 3, 5, 7
+            // this warp's 32-row blocks: of two halves 0, 2, 4, 6 or 1, 3, 5, 7
 #pragma unroll 1
-            for (int c = half * 32; c < un.n; c += 64) {
+            for (int c = half * 32; c < un.n; c += 32 * kHalves) {
                 uint32_t v[32];
                 if (any) {
                     tmem_ld32(taddr + c, v);
@@ -566,7 +558,7 @@ __global__ void __launch_bounds__(FEED == kTma ? kThreads : kThreadsFeed, 1)
             const uint32_t taddr = tmem + ((uint32_t)(sub * 32) << 16);
             const uint32_t mine = smem0 + rank * part + (uint32_t)((sub * 32 + lane) * 16);
 #pragma unroll 1
-            for (int c = half * 16; c < un.n; c += 32) {
+            for (int c = half * 16; c < un.n; c += 16 * kHalves) {
                 uint32_t v[16];
                 if (kb.x < kb.y) {
                     tmem_ld16(taddr + c, v);
@@ -593,7 +585,7 @@ __global__ void __launch_bounds__(FEED == kTma ? kThreads : kThreadsFeed, 1)
         if (has && epi && !(add && un.c0 == un.c1)) {
             const int e = threadIdx.x - 64, feat = un.f0 + (e & 127);
             const int64_t row0 = OP == kProductDw ? (int64_t)un.g * p.N + un.i0 : (int64_t)un.i0;
-            for (int i = e >> 7; i < per; i += 2) {
+            for (int i = e >> 7; i < per; i += kHalves) {
                 const int row = (i * cl + rank) * 4;
                 if (row >= un.n) break;
                 float s[4] = {0, 0, 0, 0};
@@ -642,7 +634,7 @@ struct Maps {
 template <int OP, int FEED, bool SPLIT> cudaError_t launch(const Maps& m, const Args& a, int grid, cudaStream_t s) {
     cudaError_t e = ensure_smem_attr((const void*)product_tc_kernel<OP, FEED, SPLIT>, kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_kernel(product_tc_kernel<OP, FEED, SPLIT>, dim3(grid), dim3(FEED == kTma ? kThreads : kThreadsFeed), kSmem, s,
+    e = launch_kernel(product_tc_kernel<OP, FEED, SPLIT>, dim3(grid), dim3(threads_for(FEED)), kSmem, s,
                       SPLIT ? a.split : 1, m.f, m.f16, m.r, m.r16, a);
     count_launches(1);
     return e != cudaSuccess ? e : cudaGetLastError();
