@@ -52,16 +52,21 @@ constexpr int kMaxStages = 8;
 constexpr int kEpiWarps = 8, kFeedGroup = 4;
 __host__ __device__ constexpr int epi_warps(int feed) { return feed >= kCodes16 ? 4 : kEpiWarps; }
 __host__ __device__ constexpr int feed_groups(int feed) { return feed >= kCodes16 ? 4 : feed == kCopy ? 2 : 0; }
-__host__ __device__ constexpr int threads_for(int feed) { return 32 * (2 + epi_warps(feed) + kFeedGroup * feed_groups(feed)); }
+__host__ __device__ constexpr int threads_for(int feed) {  // (codes: and a warp that loads them)
+    return 32 * (2 + epi_warps(feed) + kFeedGroup * feed_groups(feed) + (feed >= kCodes16 ? 1 : 0));
+}
 constexpr int kMaxSplit = 8;
 constexpr int kRing = 4 * (kFBytes + kMaxI * BK * 2);
 constexpr int kStWarp = 8 * 32 * 4;            // 8 row pairs x 32 features, two bf16 a word
-constexpr int kOffStage = kRing;
-constexpr int kOffBar = kOffStage + kEpiWarps * kStWarp;
-constexpr int kOffTab = kOffBar + 256;
-constexpr int kSmem = kOffTab + (int)sizeof(GroupTable);
-static_assert(kSmem <= 232448, "shared memory plan exceeds 227 KB");
-static_assert((2 * kMaxStages + 5) * 8 + 8 <= 256, "barrier block overflows");
+// shared memory: ring, barriers, codes (BF rows of 32 bytes a slot, a slot a stage), epilogue staging, groups' table
+constexpr int kOffBar = kRing;
+constexpr int kCodeSlots = 4, kCodeBytes = BF * BK / 2;
+constexpr int kOffCodes = kOffBar + 256;
+__host__ __device__ constexpr int off_stage(int feed) { return kOffCodes + (feed >= kCodes16 ? kCodeSlots * kCodeBytes : 0); }
+__host__ __device__ constexpr int off_table(int feed) { return off_stage(feed) + epi_warps(feed) * kStWarp; }
+__host__ __device__ constexpr int smem_bytes(int feed) { return off_table(feed) + (int)sizeof(GroupTable); }
+static_assert(smem_bytes(kTma) <= 232448 && smem_bytes(kCodes16) <= 232448, "shared memory plan exceeds 227 KB");
+static_assert((2 * kMaxStages + 5 + 2 * kCodeSlots) * 8 + 8 <= 256, "barrier block overflows");
 
 struct Args {
     const int32_t* offsets;
@@ -229,9 +234,10 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
     const uint32_t smem0 = smem_u32(smem);
     const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + kMaxStages);
     const uint32_t tfull0 = smem_u32(bars + 2 * kMaxStages), tempty0 = tfull0 + 16, drain = tfull0 + 32;
-    uint32_t* tmem_slot = (uint32_t*)(bars + 2 * kMaxStages + 5);
+    const uint32_t cfull0 = drain + 8, cempty0 = cfull0 + 8 * kCodeSlots;  // codes
+    uint32_t* tmem_slot = (uint32_t*)(bars + 2 * kMaxStages + 5 + 2 * kCodeSlots);
     volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
-    GroupTable& tab = *(GroupTable*)(smem + kOffTab);
+    GroupTable& tab = *(GroupTable*)(smem + off_table(FEED));
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const bool f_tma = FEED == kTma || (FEED == kCopy && !p.f_copy), r_tma = FEED == kTma || !p.r_copy;
     if (threadIdx.x == 0) {
@@ -243,6 +249,10 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull0 + 8 * b, 1);
             mbar_init(tempty0 + 8 * b, kEpi);
+        }
+        for (int s = 0; s < kCodeSlots; ++s) {
+            mbar_init(cfull0 + 8 * s, 1);
+            mbar_init(cempty0 + 8 * s, kFeedGroup);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -379,6 +389,30 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
         __syncwarp();
         volatile int never = 0;
         mbar_wait(drain, 0, 1000000000LL, &never);
+    } else if (FEED >= kCodes16 && warp == threads_for(FEED) / 32 - 1) {
+        // ------------------------------------------------- loads of codes
+        int slot = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int u = u0; u < units && ok; u += step) {
+            const Unit un = unit_at<OP>(p, u, FB, NB, tab);
+            const int2 kb = my_blocks(un, rank, cl);
+            const int row = __shfl_sync(0xffffffffu, un.g * p.N + un.f0, 0);
+            for (int k = kb.x; k < kb.y; ++k) {
+                ok = warp_wait(cempty0 + 8 * slot, phase ^ 1, lim, abort_flag, p.err, 65);
+                if (!ok) break;
+                if (elect_one()) {
+                    mbar_expect_tx(cfull0 + 8 * slot, kCodeBytes);
+                    tma_load_2d(smem0 + kOffCodes + slot * kCodeBytes, &tm_f, cfull0 + 8 * slot, k * (BK / 2), row);
+                }
+                __syncwarp();
+                if (++slot == kCodeSlots) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        if (!ok) sleep_ns(200000);
     } else if (FEED != kTma && warp >= 2 + kEpi) {
         // -------------------------------------------- copied or coded operands
         // Groups of four warps fill stages in turn, so that one's latency (a
@@ -387,6 +421,7 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
         const int fw = (warp - 2 - kEpi) & (kFeedGroup - 1), mine = (warp - 2 - kEpi) / kFeedGroup;
         const int t = (threadIdx.x - 32 * (2 + kEpi)) & (32 * kFeedGroup - 1);
         int64_t done = 0;  // blocks of the units before
+        uint32_t turn = 0;  // this group's
         bool ok = true;
         for (int u = u0; u < units && ok; u += step) {
             const Unit un = unit_at<OP>(p, u, FB, NB, tab);
@@ -395,16 +430,18 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
             const int64_t wrow = (int64_t)un.g * p.N + un.f0 + t;
             const bool in = un.f0 + t < p.N;
             const int nbk = (p.K + p.w.group - 1) / p.w.group;
-            uint4 q[2];
             uint32_t sc[2], zp[2];  // as loaded: converting would wait for the load
             auto fetch = [&](int k) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int c = k * BK + 32 * h;
-                    q[h] = make_uint4(0, 0, 0, 0);
-                    sc[h] = zp[h] = 0;  // (0 - 0) * 0
+                    if (h && p.w.group > 32 && c < p.K) {  // one for both halves
+                        sc[1] = sc[0];
+                        zp[1] = zp[0];
+                        continue;
+                    }
+                    sc[h] = zp[h] = 0;  // (past the edge)
                     if (!in || k >= kb.y || c >= p.K) continue;
-                    q[h] = __ldg((const uint4*)(p.w.codes + wrow * (p.K / 2) + c / 2));
                     const int64_t at = wrow * nbk + c / p.w.group;
                     sc[h] = FEED == kCodes16 ? __ldg((const uint16_t*)p.w.scales + at) : __ldg((const uint32_t*)p.w.scales + at);
                     zp[h] = 8;
@@ -418,6 +455,19 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
             done += kb.y - kb.x;
             if (FEED >= kCodes16) fetch(kb.x + skip);
             for (int k = kb.x + skip; k < kb.y; k += kGroups) {
+                uint4 q[2];
+                if (FEED >= kCodes16) {
+                    static_assert(FEED < kCodes16 || kGroups == kCodeSlots, "a group reads one slot");
+                    ok = __all_sync(0xffffffffu, mbar_wait(cfull0 + 8 * mine, turn & 1, lim, abort_flag));
+                    if (!ok) break;
+                    ++turn;
+                    // 32 bytes a line, their halves exchanged by TMA in every other four lines
+                    const uint8_t* line = smem + kOffCodes + mine * kCodeBytes + t * 32;
+                    q[0] = *(const uint4*)(line + ((t >> 2) & 1) * 16);
+                    q[1] = *(const uint4*)(line + (~(t >> 2) & 1) * 16);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(cempty0 + 8 * mine);
+                }
                 ok = __all_sync(0xffffffffu, mbar_wait(empty0 + 8 * stage, phase ^ 1, lim, abort_flag));
                 if (!ok) break;
                 const int c = un.c0 + k * BK, left = un.c1 - c, c16 = min(4, (left + 15) >> 4) * 16;
@@ -461,7 +511,7 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
     const int ew = warp - 2, sub = warp & 3, half = ew >> 2;  // lane quarter, column half
     const bool epi = ew >= 0 && ew < kEpi;
     if (!SPLIT && epi) {
-        uint8_t* st = smem + kOffStage + ew * kStWarp;
+        uint8_t* st = smem + off_stage(FEED) + ew * kStWarp;
         const bool vec = F % 8 == 0 && p.ldo % 8 == 0 && ((uintptr_t)p.out & 15) == 0;
         const bool add = OP == kProductDw && p.accumulate;
         int acc = 0;
@@ -624,6 +674,13 @@ bool line_map(CUtensorMap* m, const void* base, int64_t d0, int64_t d1, int64_t 
                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+// Codes, boxes of 32 bytes of BF rows.
+bool code_map(CUtensorMap* m, const void* base, int64_t rows, int64_t bytes) {
+    const cuuint64_t dims[2] = {(cuuint64_t)bytes, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)bytes};
+    const cuuint32_t box[2] = {BK / 2, BF}, es[2] = {1, 1};
+    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 // How the feed warps would copy an operand.
 int copy_mode(const void* base, int64_t ld) { return ((uintptr_t)base & 3) == 0 && ld % 2 == 0 ? 2 : 1; }
 
@@ -632,9 +689,9 @@ struct Maps {
 };
 
 template <int OP, int FEED, bool SPLIT> cudaError_t launch(const Maps& m, const Args& a, int grid, cudaStream_t s) {
-    cudaError_t e = ensure_smem_attr((const void*)product_tc_kernel<OP, FEED, SPLIT>, kSmem);
+    cudaError_t e = ensure_smem_attr((const void*)product_tc_kernel<OP, FEED, SPLIT>, smem_bytes(FEED));
     if (e != cudaSuccess) return e;
-    e = launch_kernel(product_tc_kernel<OP, FEED, SPLIT>, dim3(grid), dim3(threads_for(FEED)), kSmem, s,
+    e = launch_kernel(product_tc_kernel<OP, FEED, SPLIT>, dim3(grid), dim3(threads_for(FEED)), smem_bytes(FEED), s,
                       SPLIT ? a.split : 1, m.f, m.f16, m.r, m.r16, a);
     count_launches(1);
     return e != cudaSuccess ? e : cudaGetLastError();
@@ -739,6 +796,7 @@ cudaError_t launch_int4_tc(const Int4Product& g, int num_sms, cudaStream_t strea
     a.ldo = g.ldo;
     a.err = g.err;
     a.spin_ns = g.spin_ns;
+    if (!code_map(&m.f, g.w.codes, (int64_t)g.G * g.N, g.K / 2)) return cudaErrorNotSupported;
     if (!line_map(&m.r, g.x, g.K, g.rows, 0, a.ldr, 64) || !line_map(&m.r16, g.x, g.K, g.rows, 0, a.ldr, 16)) a.r_copy = copy_mode(g.x, a.ldr);
     return plan_and_launch<kProductFwd>(m, a, g.w.scale_elem == kF32 ? kCodes32 : kCodes16, num_sms, stream);
 }
