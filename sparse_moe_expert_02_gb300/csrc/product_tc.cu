@@ -47,11 +47,11 @@ constexpr int BF = 128, BK = 64, kMaxI = 256;  // f and c of a stage, i of a til
 constexpr int kLine = 128;                     // bytes
 constexpr int kFBytes = BF * BK * 2;
 constexpr int kMaxStages = 8;
-// Epilogue warps, and groups of four warps that feed stages: codes take many
-// instructions, so four groups, and fewer epilogue warps for their registers.
-constexpr int kEpiWarps = 8, kFeedGroup = 4;
-__host__ __device__ constexpr int epi_warps(int feed) { return feed >= kCodes16 ? 4 : kEpiWarps; }
-__host__ __device__ constexpr int feed_groups(int feed) { return feed >= kCodes16 ? 4 : feed == kCopy ? 2 : 0; }
+// Epilogue warps, and groups of four warps that feed stages: a stage is a long
+// way for one group, so four, and fewer epilogue warps for their registers.
+constexpr int kFeedGroup = 4;
+__host__ __device__ constexpr int epi_warps(int feed) { return feed == kTma ? 8 : 4; }
+__host__ __device__ constexpr int feed_groups(int feed) { return feed == kTma ? 0 : 4; }
 __host__ __device__ constexpr int threads_for(int feed) {  // (codes: and a warp that loads them)
     return 32 * (2 + epi_warps(feed) + kFeedGroup * feed_groups(feed) + (feed >= kCodes16 ? 1 : 0));
 }
@@ -157,47 +157,39 @@ __device__ __forceinline__ void store_block(uint8_t* st, const uint32_t* w, bf16
     }
 }
 
-// One line of an operand, 64 elements from p of which the first `valid` are
-// the matrix's: this lane's two, the rest zeros.
-template <int MODE> __device__ __forceinline__ uint32_t load_pair(const bf16* p, int valid, int lane) {
-    const uint16_t* q = (const uint16_t*)p + 2 * lane;
-    if (MODE == 2) {  // pairs lie on 4 bytes; a last odd element has its neighbour cleared
-        if (2 * lane + 1 < valid) return __ldg((const uint32_t*)q);
-        return 2 * lane < valid ? (uint32_t)__ldg(q) : 0u;
-    }
-    uint32_t lo = 0, hi = 0;
-    if (2 * lane < valid) lo = __ldg(q);
-    if (2 * lane + 1 < valid) hi = __ldg(q + 1);
-    return lo | hi << 16;
-}
-
-// Lines first, first + kFeedGroup, ... below `lines` of an operand to shared
-// memory at dst, kBatch of them in flight.  along_c: a line is 64 c of row
-// `line`; else 64 rows (columns of the tensor) of one c, 64 lines a block.
+// Lines of an operand to shared memory at dst by a group of four warps, 64 at
+// a time, all of a warp's sixteen in flight.  along_c: a line is 64 c of a row,
+// c_left of them the matrix's, and rows_left rows are; else 64 rows (columns
+// of the tensor) of one c.  What lies outside becomes zeros.  A lane takes two
+// elements of a line: MODE 2, where pairs lie on 4 bytes, with one load.
 template <int MODE>
-__device__ __forceinline__ void copy_lines(uint32_t dst, const bf16* src, int64_t ld, bool along_c, int lines, int valid_rows, int c_left,
-                                           int first, int c16, int lane) {
-    constexpr int kBatch = 16;
-    for (int l0 = first; l0 < lines; l0 += kBatch * kFeedGroup) {
-        uint32_t v[kBatch];
+__device__ __forceinline__ void copy_lines(uint32_t dst, const bf16* src, int64_t ld, bool along_c, int lines, int rows_left, int c_left,
+                                           int c16, int warp, int lane) {
+    constexpr int kEach = BK / kFeedGroup;
+    const uint16_t* q = (const uint16_t*)src + warp * ld + 2 * lane;
+    dst += warp * kLine + ((lane & 3) << 2);
+    for (int l0 = 0; l0 < lines; l0 += BK) {
+        const int in = along_c ? c_left : rows_left - l0;           // elements of a line
+        const int some = along_c ? rows_left - l0 : c_left;         // lines that have any
+        const bool lo = 2 * lane < in, hi = 2 * lane + 1 < in;
+        const uint16_t* b = q + (along_c ? l0 * ld : (int64_t)l0);
+        uint32_t v[kEach], w[kEach];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const int l = l0 + j * kFeedGroup;
-            v[j] = 0;
-            if (l >= lines) continue;
-            if (along_c) {
-                if (l < valid_rows) v[j] = load_pair<MODE>(src + (int64_t)l * ld, min(c_left, BK), lane);
-            } else {
-                const int c = l & (BK - 1), at = l - c;  // `at`: first of the block's 64 rows
-                if (c < c_left) v[j] = load_pair<MODE>(src + (int64_t)c * ld + at, min(max(valid_rows - at, 0), 64), lane);
-            }
+        for (int j = 0; j < kEach; ++j, b += kFeedGroup * ld) {
+            v[j] = w[j] = 0;
+            if (warp + kFeedGroup * j >= some) continue;
+            if (MODE == 2 && hi) v[j] = __ldg((const uint32_t*)b);
+            if (MODE == 2 && lo && !hi) v[j] = __ldg(b);
+            if (MODE == 1 && lo) v[j] = __ldg(b);
+            if (MODE == 1 && hi) w[j] = __ldg(b + 1);
         }
+        const int put = along_c ? lines - l0 : c16;
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const int l = l0 + j * kFeedGroup;
-            if (l >= lines || (!along_c && (l & (BK - 1)) >= c16)) continue;
-            const uint32_t a = dst + l * kLine + (((lane >> 2) ^ (l & 7)) << 4) + ((lane & 3) << 2);
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v[j]) : "memory");
+        for (int j = 0; j < kEach; ++j) {
+            const int l = warp + kFeedGroup * j;
+            if (l >= put) continue;
+            const uint32_t a = dst + (l0 + kFeedGroup * j) * kLine + (((lane >> 2) ^ (l & 7)) << 4);
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(MODE == 1 ? v[j] | w[j] << 16 : v[j]) : "memory");
         }
     }
 }
@@ -486,14 +478,14 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
                     const bf16* src = OP == kProductFwd   ? p.f + ((int64_t)un.g * p.N + un.f0) * p.ldf + c
                                       : OP == kProductDx ? p.f + ((int64_t)un.g * p.N + c) * p.ldf + un.f0
                                                          : p.f + (int64_t)c * p.ldf + un.f0;
-                    if (p.f_copy == 2) copy_lines<2>(fs, src, p.ldf, kFAlongC, BF, F - un.f0, left, fw, c16, lane);
-                    else copy_lines<1>(fs, src, p.ldf, kFAlongC, BF, F - un.f0, left, fw, c16, lane);
+                    if (p.f_copy == 2) copy_lines<2>(fs, src, p.ldf, kFAlongC, BF, F - un.f0, left, c16, fw, lane);
+                    else copy_lines<1>(fs, src, p.ldf, kFAlongC, BF, F - un.f0, left, c16, fw, lane);
                 }
                 if (p.r_copy) {
                     const bf16* src = kRAlongC ? p.r + (int64_t)un.i0 * p.ldr + c : p.r + (int64_t)c * p.ldr + un.i0;
                     const int lines = kRAlongC ? (un.n + 15) & ~15 : ((un.n + 63) & ~63);
-                    if (p.r_copy == 2) copy_lines<2>(rs, src, p.ldr, kRAlongC, lines, un.n, left, fw, c16, lane);
-                    else copy_lines<1>(rs, src, p.ldr, kRAlongC, lines, un.n, left, fw, c16, lane);
+                    if (p.r_copy == 2) copy_lines<2>(rs, src, p.ldr, kRAlongC, lines, un.n, left, c16, fw, lane);
+                    else copy_lines<1>(rs, src, p.ldr, kRAlongC, lines, un.n, left, c16, fw, lane);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
@@ -668,6 +660,7 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
 
 // bf16 [d2][d1][d0] (d2 = 0: two dimensions), boxes of a 128-byte line by box1.
 bool line_map(CUtensorMap* m, const void* base, int64_t d0, int64_t d1, int64_t d2, int64_t ld, int box1) {
+    if (((uintptr_t)base & 15) || ld % 8) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2}, strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)(ld * d1) * 2};
     const cuuint32_t box[3] = {BK, (cuuint32_t)box1, 1}, es[3] = {1, 1, 1};
     return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d2 ? 3 : 2, const_cast<void*>(base), dims, strides, box, es,
