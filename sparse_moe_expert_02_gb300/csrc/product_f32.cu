@@ -69,22 +69,28 @@ __global__ void __launch_bounds__(kThreads, Tile<BM>::kBlocks) product_f32_kerne
             k0 = 0;
             k1 = OP == kProductFwd ? p.K : p.N;
         }
+        // An operand's elements of a step, kEach a thread: along the sum one place for all of them and every
+        // kThreads / BK-th row, or one row and every kThreads / BM-th place.
+        const int ak = kAK ? tid % BK : tid / BM, ai = kAK ? tid / BK : tid % BM;
+        const int bk = kBK ? tid % BK : tid / BM, bi = kBK ? tid / BK : tid % BM;
+        constexpr int kNextI = kThreads / BK, kNextK = kThreads / BM;
+        const float* pa = kAK ? a + (int64_t)(i0 + ai) * p.lda + k0 + ak : a + (int64_t)(k0 + ak) * p.lda + i0 + ai;
         const int64_t brow = OP == kProductDw ? 0 : (int64_t)g * p.N;  // row of B that its index 0 is
+        const float* pb = kBK ? b + (brow + c0 + bi) * ldb + k0 + bk : b + (brow + k0 + bk) * ldb + c0 + bi;
+        const uint32_t da = tc::smem_u32(ring) + (ak * LD + ai) * 4, db = tc::smem_u32(ring) + (BK * LD + bk * LD + bi) * 4;
         auto fetch = [&](int step) {
-            const int k = k0 + step * BK;
-            if (k < k1) {
-                const uint32_t sa = tc::smem_u32(ring) + (step % T::kStages) * (2 * BK * LD * 4), sb = sa + BK * LD * 4;
+            const int left = k1 - k0 - step * BK;
+            if (left > 0) {
+                const uint32_t at = (step % T::kStages) * (2 * BK * LD * 4);
 #pragma unroll
                 for (int j = 0; j < kEach; ++j) {
-                    const int e = tid + j * kThreads;
-                    const int ai = kAK ? e / BK : e % BM, ak = kAK ? e % BK : e / BM;
-                    const int bi = kBK ? e / BK : e % BM, bk = kBK ? e % BK : e / BM;
-                    const bool ain = i0 + ai < i1 && k + ak < k1, bin = c0 + bi < cols && k + bk < k1;
-                    const int64_t aat = kAK ? (int64_t)(i0 + ai) * p.lda + k + ak : (int64_t)(k + ak) * p.lda + i0 + ai;
-                    const int64_t bat = kBK ? (brow + c0 + bi) * ldb + k + bk : (brow + k + bk) * ldb + c0 + bi;
-                    copy4(sa + (ak * LD + ai) * 4, ain ? a + aat : a, ain);
-                    copy4(sb + (bk * LD + bi) * 4, bin ? b + bat : b, bin);
+                    const bool ain = kAK ? ak < left && i0 + ai + j * kNextI < i1 : ak + j * kNextK < left && i0 + ai < i1;
+                    const bool bin = kBK ? bk < left && c0 + bi + j * kNextI < cols : bk + j * kNextK < left && c0 + bi < cols;
+                    copy4(da + at + j * (kAK ? kNextI : kNextK * LD) * 4, ain ? pa + j * (kAK ? kNextI : kNextK) * p.lda : a, ain);
+                    copy4(db + at + j * (kBK ? kNextI : kNextK * LD) * 4, bin ? pb + j * (kBK ? kNextI : kNextK) * ldb : b, bin);
                 }
+                pa += kAK ? BK : BK * p.lda;
+                pb += kBK ? BK : BK * ldb;
             }
             commit();  // (a group a step, empty past the end)
         };

@@ -61,12 +61,19 @@ constexpr int kStWarp = 8 * 32 * 4;            // 8 row pairs x 32 features, two
 // shared memory: ring, barriers, codes (BF rows of 32 bytes a slot, a slot a stage), epilogue staging, groups' table
 constexpr int kOffBar = kRing;
 constexpr int kCodeSlots = 4, kCodeBytes = BF * BK / 2;
-constexpr int kOffCodes = kOffBar + 256;
+constexpr int kOffCodes = kOffBar + 512;
 __host__ __device__ constexpr int off_stage(int feed) { return kOffCodes + (feed >= kCodes16 ? kCodeSlots * kCodeBytes : 0); }
 __host__ __device__ constexpr int off_table(int feed) { return off_stage(feed) + epi_warps(feed) * kStWarp; }
 __host__ __device__ constexpr int smem_bytes(int feed) { return off_table(feed) + (int)sizeof(GroupTable); }
 static_assert(smem_bytes(kTma) <= 232448 && smem_bytes(kCodes16) <= 232448, "shared memory plan exceeds 227 KB");
-static_assert((2 * kMaxStages + 5 + 2 * kCodeSlots) * 8 + 8 <= 256, "barrier block overflows");
+static_assert((3 * kMaxStages + 5 + 2 * kCodeSlots) * 8 + 8 <= 512, "barrier block overflows");
+
+// What a cluster is for: nothing; a split of one unit's sum over its CTAs; a
+// pair of CTAs that multiply 256 f by a tile's rows together (cta_group::2).
+// Each of a pair holds 128 f and half of the rows of a stage, so that a stage
+// takes 32 KB instead of 48 for the same time of MMAs: less to bring from L2,
+// and six stages on the way instead of four.
+enum Cluster { kSingle = 0, kSplit = 1, kPair = 2 };
 
 struct Args {
     const int32_t* offsets;
@@ -96,6 +103,25 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
+// Loads; of a pair, bar may be the other CTA's (a cluster address).
+template <bool PAIR> __device__ __forceinline__ void load2(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+    if (PAIR) tma_load_2d_pair(dst, map, bar, x, y);
+    else tma_load_2d(dst, map, bar, x, y);
+}
+template <bool PAIR> __device__ __forceinline__ void load3(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+    if (!PAIR) {
+        tma_load_3d(dst, map, bar, x, y, z);
+    } else {
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+            : "memory");
+    }
+}
+// Arrival at another CTA's barrier that orders nothing before it.
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 __device__ __forceinline__ void st_shared16(uint32_t a, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -109,10 +135,10 @@ struct Unit {
 
 template <int OP> __device__ __forceinline__ int f_size(const Args& p) { return OP == kProductFwd ? p.N : p.K; }
 
-template <int OP> __device__ __forceinline__ Unit unit_at(const Args& p, int u, int FB, int NB, const GroupTable& t) {
+template <int OP, int UF> __device__ __forceinline__ Unit unit_at(const Args& p, int u, int FB, int NB, const GroupTable& t) {
     Unit r;
     const int rt = u / FB;
-    r.f0 = (u - rt * FB) * BF;
+    r.f0 = (u - rt * FB) * UF;
     if (OP == kProductDw) {
         r.g = rt / NB;
         r.i0 = (rt - r.g * NB) * p.tile_i;
@@ -214,33 +240,37 @@ template <int FEED> __device__ __forceinline__ uint4 values8(uint32_t w, __nv_bf
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-template <int OP, int FEED, bool SPLIT>
+template <int OP, int FEED, int CL>
 __global__ void __launch_bounds__(threads_for(FEED), 1)
     product_tc_kernel(const __grid_constant__ CUtensorMap tm_f, const __grid_constant__ CUtensorMap tm_f16,
                       const __grid_constant__ CUtensorMap tm_r, const __grid_constant__ CUtensorMap tm_r16, const Args p) {
     constexpr bool kFAlongC = OP == kProductFwd, kRAlongC = OP != kProductDw;
     constexpr int kEpi = epi_warps(FEED), kHalves = kEpi / 4;  // warps for each lane quarter
+    constexpr bool SPLIT = CL == kSplit, PAIR = CL == kPair;
+    static_assert(!PAIR || FEED == kTma, "pairs load by TMA alone");
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* bars = (uint64_t*)(smem + kOffBar);
     const int S = p.stages;
     const uint32_t smem0 = smem_u32(smem);
     const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + kMaxStages);
     const uint32_t tfull0 = smem_u32(bars + 2 * kMaxStages), tempty0 = tfull0 + 16, drain = tfull0 + 32;
-    const uint32_t cfull0 = drain + 8, cempty0 = cfull0 + 8 * kCodeSlots;  // codes
-    uint32_t* tmem_slot = (uint32_t*)(bars + 2 * kMaxStages + 5 + 2 * kCodeSlots);
+    const uint32_t tail0 = drain + 8, cfull0 = tail0 + 8 * kMaxStages, cempty0 = cfull0 + 8 * kCodeSlots;  // codes
+    uint32_t* tmem_slot = (uint32_t*)(bars + 3 * kMaxStages + 5 + 2 * kCodeSlots);
     volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
     GroupTable& tab = *(GroupTable*)(smem + off_table(FEED));
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const bool f_tma = FEED == kTma || (FEED == kCopy && !p.f_copy), r_tma = FEED == kTma || !p.r_copy;
     if (threadIdx.x == 0) {
-        const int feeders = (f_tma || r_tma ? 1 : 0) + (FEED == kTma ? 0 : kFeedGroup);
+        // (pair, dw: the leader's are told by the other CTA's loads as well)
+        const int feeders = (f_tma || r_tma ? 1 : 0) + (FEED == kTma ? 0 : kFeedGroup) + (PAIR && OP == kProductDw ? 1 : 0);
         for (int s = 0; s < S; ++s) {
             mbar_init(full0 + 8 * s, feeders);
             mbar_init(empty0 + 8 * s, 1);
+            mbar_init(tail0 + 8 * s, 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull0 + 8 * b, 1);
-            mbar_init(tempty0 + 8 * b, kEpi);
+            mbar_init(tempty0 + 8 * b, PAIR ? 2 * kEpi : kEpi);
         }
         for (int s = 0; s < kCodeSlots; ++s) {
             mbar_init(cfull0 + 8 * s, 1);
@@ -250,7 +280,9 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 1) {
+    if (PAIR && warp == 1) {
+        tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    } else if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -258,15 +290,28 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
     if (warp == 2) group_table(tab, p.offsets, p.G, p.rows, OP == kProductDw ? kMaxI : p.tile_i);
     tc_fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();  // both CTAs' barriers and tensor memory exist before either uses the other's
     tc_fence_after();
     pdl_release();  // (once tensor memory is ours)
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-    const int F = f_size<OP>(p), FB = (F + BF - 1) / BF, NB = (p.N + p.tile_i - 1) / p.tile_i;
+    constexpr int kUnitF = PAIR ? 2 * BF : BF;
+    const int F = f_size<OP>(p), FB = (F + kUnitF - 1) / kUnitF, NB = (p.N + p.tile_i - 1) / p.tile_i;
     const int units = (OP == kProductDw ? p.G * NB : tab.tiles[p.G]) * FB;
     // Units of this CTA: u0, u0 + step, ...  Split: a cluster takes one unit or none.
     const int rank = SPLIT ? (int)cluster_rank() : 0, cl = SPLIT ? p.split : 1;
-    const int u0 = (int)blockIdx.x / cl, step = (int)gridDim.x / cl;
+    const int crank = PAIR ? (int)cluster_rank() : 0, per = PAIR ? 2 : cl;  // of a pair: 0 leads (issues the MMAs)
+    const int u0 = (int)blockIdx.x / per, step = (int)gridDim.x / per;
     const int64_t lim = p.spin_ns;
+    auto wait = [&](uint32_t bar, uint32_t parity, int where) {
+        const bool ok = warp_wait(bar, parity, lim, abort_flag, p.err, where);
+        if (PAIR && !ok && elect_one()) raise_abort_pair(abort_flag, (uint32_t)crank);
+        return ok;
+    };
+    auto at_unit = [&](int u) {
+        Unit un = unit_at<OP, kUnitF>(p, u, FB, NB, tab);
+        if (PAIR) un.f0 += crank * BF;
+        return un;
+    };
 
     if (warp == 0) {
         // -------------------------------------------------- TMA producer
@@ -275,47 +320,66 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
             uint32_t phase = 0;
             bool ok = true;
             for (int u = u0; u < units && ok; u += step) {
-                const Unit un = unit_at<OP>(p, u, FB, NB, tab);
+                const Unit un = at_unit(u);
                 const int2 kb = my_blocks(un, rank, cl);
-                const int n16 = __shfl_sync(0xffffffffu, (un.n + 15) >> 4, 0), slabs = (n16 + 3) >> 2;
-                const int i0 = __shfl_sync(0xffffffffu, un.i0, 0), f0 = __shfl_sync(0xffffffffu, un.f0, 0);
+                // sixteens of i that this CTA loads, from i0 on
+                const int n16 = __shfl_sync(0xffffffffu, PAIR ? (un.n + 31) >> 5 : (un.n + 15) >> 4, 0), slabs = (n16 + 3) >> 2;
+                const int i0 = __shfl_sync(0xffffffffu, un.i0 + crank * n16 * 16, 0), f0 = __shfl_sync(0xffffffffu, un.f0, 0);
                 const int g = __shfl_sync(0xffffffffu, un.g, 0);
                 for (int k = kb.x; k < kb.y; ++k) {
-                    ok = warp_wait(empty0 + 8 * stage, phase ^ 1, lim, abort_flag, p.err, 61);
+                    ok = wait(empty0 + 8 * stage, phase ^ 1, 61);
                     if (!ok) break;
                     const int c = __shfl_sync(0xffffffffu, un.c0 + k * BK, 0);
                     // dw: sixteens of this block's rows; the others read whole blocks, zeros past the edge
                     const int c16 = OP == kProductDw ? __shfl_sync(0xffffffffu, min(4, (un.c1 - c + 15) >> 4), 0) : 4;
                     if (elect_one()) {
-                        const uint32_t fb = full0 + 8 * stage, fs = smem0 + stage * p.stage_bytes, rs = fs + kFBytes;
+                        uint32_t fb = full0 + 8 * stage;
+                        const uint32_t fs = smem0 + stage * p.stage_bytes, rs = fs + kFBytes;
                         const int rlines = kRAlongC ? n16 * 16 : slabs * c16 * 16, flines = kFAlongC ? BF : 2 * c16 * 16;
-                        mbar_expect_tx(fb, (f_tma ? flines * kLine : 0) + (r_tma ? rlines * kLine : 0));
+                        const uint32_t bytes = (f_tma ? flines * kLine : 0) + (r_tma ? rlines * kLine : 0);
+                        if (!PAIR) {
+                            mbar_expect_tx(fb, bytes);
+                        } else {
+                            // Both CTAs' loads count at the leader.  dw's last block, where zeros have to be written
+                            // over lines: the other's at its own barrier, and its MMA warp tells the leader.
+                            const bool ragged = OP == kProductDw && un.c1 - c < BK && ((un.c1 - c) & 15);
+                            if (crank == 0) {
+                                mbar_expect_tx(fb, ragged ? bytes : 2 * bytes);
+                            } else if (ragged) {
+                                fb = tail0 + 8 * stage;
+                                mbar_expect_tx(fb, bytes);
+                            } else if (OP == kProductDw) {
+                                mbar_arrive_relaxed(mapa_shared(fb, 0));
+                            }
+                            if (!ragged) fb = mapa_shared(fb, 0);
+                            else fb = mapa_shared(fb, (uint32_t)crank);
+                        }
                         if (f_tma) {
                             if (OP == kProductFwd) {
-                                tma_load_3d(fs, &tm_f, fb, c, f0, g);
+                                load3<PAIR>(fs, &tm_f, fb, c, f0, g);
                             } else if (OP == kProductDx) {
-                                tma_load_3d(fs, &tm_f, fb, f0, c, g);
-                                tma_load_3d(fs + BK * kLine, &tm_f, fb, f0 + 64, c, g);
+                                load3<PAIR>(fs, &tm_f, fb, f0, c, g);
+                                load3<PAIR>(fs + BK * kLine, &tm_f, fb, f0 + 64, c, g);
                             } else {
                                 for (int s = 0; s < 2; ++s) {
-                                    if (c16 == 4) tma_load_2d(fs + s * BK * kLine, &tm_f, fb, f0 + 64 * s, c);
+                                    if (c16 == 4) load2<PAIR>(fs + s * BK * kLine, &tm_f, fb, f0 + 64 * s, c);
                                     else
                                         for (int j = 0; j < c16; ++j)
-                                            tma_load_2d(fs + s * BK * kLine + j * 16 * kLine, &tm_f16, fb, f0 + 64 * s, c + 16 * j);
+                                            load2<PAIR>(fs + s * BK * kLine + j * 16 * kLine, &tm_f16, fb, f0 + 64 * s, c + 16 * j);
                                 }
                             }
                         }
                         if (r_tma) {
                             if (kRAlongC) {
                                 const int n64 = n16 >> 2;
-                                for (int j = 0; j < n64; ++j) tma_load_2d(rs + j * 64 * kLine, &tm_r, fb, c, i0 + j * 64);
-                                for (int j = 4 * n64; j < n16; ++j) tma_load_2d(rs + j * 16 * kLine, &tm_r16, fb, c, i0 + j * 16);
+                                for (int j = 0; j < n64; ++j) load2<PAIR>(rs + j * 64 * kLine, &tm_r, fb, c, i0 + j * 64);
+                                for (int j = 4 * n64; j < n16; ++j) load2<PAIR>(rs + j * 16 * kLine, &tm_r16, fb, c, i0 + j * 16);
                             } else {
                                 for (int s = 0; s < slabs; ++s) {
-                                    if (c16 == 4) tma_load_2d(rs + s * BK * kLine, &tm_r, fb, i0 + 64 * s, c);
+                                    if (c16 == 4) load2<PAIR>(rs + s * BK * kLine, &tm_r, fb, i0 + 64 * s, c);
                                     else
                                         for (int j = 0; j < c16; ++j)
-                                            tma_load_2d(rs + s * BK * kLine + j * 16 * kLine, &tm_r16, fb, i0 + 64 * s, c + 16 * j);
+                                            load2<PAIR>(rs + s * BK * kLine + j * 16 * kLine, &tm_r16, fb, i0 + 64 * s, c + 16 * j);
                                 }
                             }
                         }
@@ -331,42 +395,70 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
         }
     } else if (warp == 1) {
         // --------------------------------------------------- MMA issuer
+        // dw: zeros over the lines of a last block's last sixteen that lie past the end.
+        auto clear = [&](uint32_t fs, int left, int rslabs) {
+            const int slabs = 2 + rslabs, each = (16 - (left & 15)) * 8;  // 16-byte pieces of a slab
+            for (int e = lane; e < slabs * each; e += 32) {
+                const int s = e / each;
+                st_shared16(fs + s * BK * kLine + left * kLine + (e - s * each) * 16, make_uint4(0, 0, 0, 0));
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+        };
         int stage = 0, acc = 0;
-        uint32_t phase = 0, acc_phase = 0;
+        uint32_t phase = 0, acc_phase = 0, tail_phase = 0;  // (a bit a stage)
         bool ok = true;
         for (int u = u0; u < units && ok; u += step) {
-            const Unit un = unit_at<OP>(p, u, FB, NB, tab);
+            const Unit un = at_unit(u);
             const int2 kb = my_blocks(un, rank, cl);
             if (kb.x == kb.y) continue;  // nothing to sum: the epilogue knows
-            const int n = __shfl_sync(0xffffffffu, (un.n + 15) & ~15, 0);
-            const uint32_t id = idesc_bf16(BF, n) | (kFAlongC ? 0u : 1u << 15) | (kRAlongC ? 0u : 1u << 16);
-            ok = warp_wait(tempty0 + 8 * acc, acc_phase ^ 1, lim, abort_flag, p.err, 62);
+            const int n = __shfl_sync(0xffffffffu, PAIR ? (un.n + 31) & ~31 : (un.n + 15) & ~15, 0);
+            const int rslabs = ((PAIR ? n / 2 : n) + 63) / 64;
+            if (PAIR && crank) {  // only the other CTA's last block of dw is of concern here
+                if (OP != kProductDw) break;
+                const int left = (un.c1 - un.c0) & (BK - 1);
+                stage = (stage + kb.y - 1) % S;
+                if (left & 15) {
+                    ok = wait(tail0 + 8 * stage, tail_phase >> stage & 1, 66);
+                    if (!ok) break;
+                    tail_phase ^= 1u << stage;
+                    clear(smem0 + stage * p.stage_bytes, left, rslabs);
+                    if (elect_one()) mbar_arrive_cluster(mapa_shared(full0 + 8 * stage, 0));
+                    __syncwarp();
+                }
+                stage = (stage + 1) % S;
+                continue;
+            }
+            const uint32_t id = idesc_bf16(PAIR ? 2 * BF : BF, n) | (kFAlongC ? 0u : 1u << 15) | (kRAlongC ? 0u : 1u << 16);
+            ok = wait(tempty0 + 8 * acc, acc_phase ^ 1, 62);
             if (!ok) break;
             const uint32_t d = tmem + acc * kMaxI;
             for (int k = kb.x; k < kb.y; ++k) {
-                ok = warp_wait(full0 + 8 * stage, phase, lim, abort_flag, p.err, 63);
+                ok = wait(full0 + 8 * stage, phase, 63);
                 if (!ok) break;
                 const uint32_t fs = smem0 + stage * p.stage_bytes, rs = fs + kFBytes;
                 const int left = un.c1 - un.c0 - k * BK;
                 const int steps = __shfl_sync(0xffffffffu, min(4, (left + 15) >> 4), 0);
                 if (OP == kProductDw && left < BK && (left & 15)) {
-                    const int slabs = 2 + (n + 63) / 64, per = (16 - (left & 15)) * 8;  // 16-byte pieces of a slab
-                    for (int e = lane; e < slabs * per; e += 32) {
-                        const int s = e / per;
-                        st_shared16(fs + s * BK * kLine + left * kLine + (e - s * per) * 16, make_uint4(0, 0, 0, 0));
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
+                    if (PAIR) asm volatile("fence.acq_rel.cluster;" ::: "memory");  // the other CTA's zeros
+                    clear(fs, left, rslabs);
                 }
                 tc_fence_after();
                 if (elect_one()) {
                     const uint64_t fd = kFAlongC ? umma_desc(fs) : desc_mn(fs), rd = kRAlongC ? umma_desc(rs) : desc_mn(rs);
                     constexpr uint64_t fstep = (kFAlongC ? 32 : 16 * kLine) >> 4, rstep = (kRAlongC ? 32 : 16 * kLine) >> 4;
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        if (kk < steps) umma_bf16(d, fd + kk * fstep, rd + kk * rstep, id, k != kb.x || kk != 0);
-                    umma_commit(empty0 + 8 * stage);
-                    if (k + 1 == kb.y) umma_commit(tfull0 + 8 * acc);
+                    for (int kk = 0; kk < 4; ++kk) {
+                        if (kk >= steps) break;
+                        if (PAIR) umma_bf16_pair(d, fd + kk * fstep, rd + kk * rstep, id, k != kb.x || kk != 0);
+                        else umma_bf16(d, fd + kk * fstep, rd + kk * rstep, id, k != kb.x || kk != 0);
+                    }
+                    if (PAIR) umma_commit_pair(empty0 + 8 * stage);
+                    else umma_commit(empty0 + 8 * stage);
+                    if (k + 1 == kb.y) {
+                        if (PAIR) umma_commit_pair(tfull0 + 8 * acc);
+                        else umma_commit(tfull0 + 8 * acc);
+                    }
                 }
                 __syncwarp();
                 if (++stage == S) {
@@ -377,17 +469,23 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1;
         }
-        if (elect_one()) umma_commit(drain);  // everything issued is done before tensor memory is freed
-        __syncwarp();
-        volatile int never = 0;
-        mbar_wait(drain, 0, 1000000000LL, &never);
+        // everything issued is done before tensor memory is freed
+        if (!PAIR || crank == 0) {
+            if (elect_one()) {
+                if (PAIR) umma_commit_pair(drain);
+                else umma_commit(drain);
+            }
+            __syncwarp();
+            volatile int never = 0;
+            mbar_wait(drain, 0, 1000000000LL, &never);
+        }
     } else if (FEED >= kCodes16 && warp == threads_for(FEED) / 32 - 1) {
         // ------------------------------------------------- loads of codes
         int slot = 0;
         uint32_t phase = 0;
         bool ok = true;
         for (int u = u0; u < units && ok; u += step) {
-            const Unit un = unit_at<OP>(p, u, FB, NB, tab);
+            const Unit un = at_unit(u);
             const int2 kb = my_blocks(un, rank, cl);
             const int row = __shfl_sync(0xffffffffu, un.g * p.N + un.f0, 0);
             for (int k = kb.x; k < kb.y; ++k) {
@@ -416,7 +514,7 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
         uint32_t turn = 0;  // this group's
         bool ok = true;
         for (int u = u0; u < units && ok; u += step) {
-            const Unit un = unit_at<OP>(p, u, FB, NB, tab);
+            const Unit un = at_unit(u);
             const int2 kb = my_blocks(un, rank, cl);
             // codes: thread t takes the line (64 codes, a scale or two) of feature t
             const int64_t wrow = (int64_t)un.g * p.N + un.f0 + t;
@@ -509,7 +607,7 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int u = u0; u < units; u += step) {
-            const Unit un = unit_at<OP>(p, u, FB, NB, tab);
+            const Unit un = at_unit(u);
             const bool any = un.c1 > un.c0;
             const uint32_t taddr = tmem + acc * kMaxI + ((uint32_t)(sub * 32) << 16);
             const uint32_t te = tempty0 + 8 * acc;
@@ -519,6 +617,7 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
                     if (lane == 0 && !*abort_flag) {
                         record_error(p.err, MOE_ERR_DEVICE_TIMEOUT, 64, blockIdx.x, u);
                         *abort_flag = 1;
+                        if (PAIR) raise_abort_pair(abort_flag, (uint32_t)crank);
                     }
                     break;
                 }
@@ -580,7 +679,12 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
             if (any) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(te);
+                if (lane == 0) {
+                    // (relaxed: what it orders are loads from tensor memory, which are complete; a release at the
+                    // other CTA would wait for the stores above)
+                    if (PAIR) mbar_arrive_relaxed(mapa_shared(te, 0));
+                    else mbar_arrive(te);
+                }
             }
         }
     }
@@ -591,10 +695,10 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
         __syncwarp();
         cluster_sync();  // every CTA's loads and MMAs are done
         const bool has = u0 < units;
-        const Unit un = has ? unit_at<OP>(p, u0, FB, NB, tab) : Unit{};
+        const Unit un = has ? at_unit(u0) : Unit{};
         const int2 kb = my_blocks(un, rank, cl);
-        const int quads = (un.n + 3) >> 2, per = (quads + cl - 1) / cl;  // four-row slots, of each rank
-        const uint32_t part = (uint32_t)(per * BF * 16);                 // bytes a rank sends another
+        const int quads = (un.n + 3) >> 2, slots = (quads + cl - 1) / cl;  // four-row slots, of each rank
+        const uint32_t part = (uint32_t)(slots * BF * 16);                 // bytes a rank sends another
         if (has && epi) {
             tc_fence_after();  // the accumulator was committed before the barrier
             const uint32_t taddr = tmem + ((uint32_t)(sub * 32) << 16);
@@ -627,7 +731,7 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
         if (has && epi && !(add && un.c0 == un.c1)) {
             const int e = threadIdx.x - 64, feat = un.f0 + (e & 127);
             const int64_t row0 = OP == kProductDw ? (int64_t)un.g * p.N + un.i0 : (int64_t)un.i0;
-            for (int i = e >> 7; i < per; i += kHalves) {
+            for (int i = e >> 7; i < slots; i += kHalves) {
                 const int row = (i * cl + rank) * 4;
                 if (row >= un.n) break;
                 float s[4] = {0, 0, 0, 0};
@@ -654,7 +758,12 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
     }
     tc_fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();  // no arrival or MMA of the other CTA is on its way here
     tc_fence_after();
+    if (PAIR) {
+        if (warp == 1) tmem_dealloc_pair(tmem, 512);
+        return;
+    }
     if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
@@ -681,11 +790,11 @@ struct Maps {
     CUtensorMap f, f16, r, r16;
 };
 
-template <int OP, int FEED, bool SPLIT> cudaError_t launch(const Maps& m, const Args& a, int grid, cudaStream_t s) {
-    cudaError_t e = ensure_smem_attr((const void*)product_tc_kernel<OP, FEED, SPLIT>, smem_bytes(FEED));
+template <int OP, int FEED, int CL> cudaError_t launch(const Maps& m, const Args& a, int grid, cudaStream_t s) {
+    cudaError_t e = ensure_smem_attr((const void*)product_tc_kernel<OP, FEED, CL>, smem_bytes(FEED));
     if (e != cudaSuccess) return e;
-    e = launch_kernel(product_tc_kernel<OP, FEED, SPLIT>, dim3(grid), dim3(threads_for(FEED)), smem_bytes(FEED), s,
-                      SPLIT ? a.split : 1, m.f, m.f16, m.r, m.r16, a);
+    e = launch_kernel(product_tc_kernel<OP, FEED, CL>, dim3(grid), dim3(threads_for(FEED)), smem_bytes(FEED), s,
+                      CL == kSplit ? a.split : CL == kPair ? 2 : 1, m.f, m.f16, m.r, m.r16, a);
     count_launches(1);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -707,14 +816,23 @@ template <int OP> cudaError_t plan_and_launch(const Maps& m, Args& a, int feed, 
         const int64_t tiles = cdiv(units(256), num_sms) * num_sms / fb;
         if (tiles > 0) a.tile_i = (int)std::min<int64_t>(256, cdiv(cdiv(a.rows, tiles), 16) * 16);
     }
-    a.stage_bytes = kFBytes + (int)cdiv(a.tile_i, 64) * 64 * BK * 2;
-    a.stages = std::min(kMaxStages, kRing / a.stage_bytes);
     // dw: a group's rows, at most (an average would leave the largest to one CTA)
     const int64_t kb = cdiv(OP == kProductFwd ? a.K : OP == kProductDx ? a.N : a.rows, BK);
     a.split = 1;
     while (a.split < kMaxSplit && units(a.tile_i) * a.split * 2 <= num_sms && kb >= 4 * a.split) a.split *= 2;
+    // Pairs: where they leave no more than one in eight of the f tiles empty, and there is a unit for each.  dw
+    // with few rows a group is bound by its epilogue, which two CTAs wait for: 64 groups of 256 rows, 1024 x 4096,
+    // fp32 dw 193 us (pairs 238), of 512 rows 296 (239); bf16 dw, 256 rows 138 (132).
+    const bool pair = feed == kTma && a.split == 1 && (fb % 2 == 0 || fb >= 8) && units(a.tile_i) >= num_sms &&
+                      (OP != kProductDw || (a.tile_i >= 128 && a.rows >= (a.out_elem == kF32 ? 384 : 128) * (int64_t)a.G));
+    a.stage_bytes = kFBytes + (int)cdiv(a.tile_i, 64) * 64 * BK * 2 / (pair ? 2 : 1);
+    a.stages = std::min(kMaxStages, kRing / a.stage_bytes);
+    if (pair) {
+        const int64_t n = units(a.tile_i) / fb * cdiv(fb, 2);
+        return launch<OP, kTma, kPair>(m, a, 2 * (int)std::min<int64_t>(n, num_sms / 2), s);
+    }
     const int grid = a.split > 1 ? (int)units(a.tile_i) * a.split : (int)std::min<int64_t>(units(a.tile_i), num_sms);
-#define MOE_PTC(FEED) (a.split > 1 ? launch<OP, FEED, true>(m, a, grid, s) : launch<OP, FEED, false>(m, a, grid, s))
+#define MOE_PTC(FEED) (a.split > 1 ? launch<OP, FEED, kSplit>(m, a, grid, s) : launch<OP, FEED, kSingle>(m, a, grid, s))
     if (feed == kTma) return MOE_PTC(kTma);
     if constexpr (OP == kProductFwd) {
         if (feed == kCodes16) return MOE_PTC(kCodes16);
