@@ -1177,8 +1177,12 @@ moe_status check_groups(const int32_t* offsets, int32_t rows, int32_t G, int32_t
     return MOE_OK;
 }
 
-// Few rows a group: bound by the weights' bytes.
-bool few_rows(int64_t rows, int64_t G) { return rows <= 16 * G; }
+// Few rows a group, so that the weights' bytes bound: the kernels that take
+// eight rows at a time against the tensor-memory ones, us.  bf16 1024 x 4096:
+// 64 groups of 8 rows 79 against 89, of 12 rows 103 against 89; one matrix, 16
+// rows 5.6 against 6.7, 32 rows 6.2 against 6.9.  4 bits: 64 groups of 8 rows
+// 55 against 87, of 16 rows 103 against 87; one matrix, 32 rows 6.5 against 9.7.
+bool few_rows(int64_t rows, int64_t G) { return rows <= 8 * G || rows <= 32; }
 
 moe_status run_product(moe::GroupProduct& g, int32_t dtype, int32_t out_dtype, void* stream) {
     g.elem = float_elem(dtype);

@@ -208,7 +208,7 @@ template <int LG> cudaError_t launch_coded(const Args& a, int elem, int num_sms,
 
 cudaError_t launch_product_few(const GroupProduct& g, int num_sms, cudaStream_t stream) {
     using namespace few_rows;
-    if (g.rows > kRows * (int64_t)g.G || g.op != kProductFwd || g.elem != kBF16 || g.K % 8 || ((uintptr_t)g.b & 15)) return cudaErrorNotSupported;
+    if (g.op != kProductFwd || g.elem != kBF16 || g.K % 8 || ((uintptr_t)g.b & 15)) return cudaErrorNotSupported;
     Args a = {};
     a.offsets = g.offsets;
     a.rows = g.rows;

@@ -192,6 +192,8 @@ __global__ void __launch_bounds__(kAllThreads, 2) product_few_bulk_kernel(const 
                     }
                 }
             }
+            // What was loaded has been used (an arrival would not order loads on their way with the copies' writes).
+            asm volatile("" ::"f"(acc[0]), "f"(acc[1]), "f"(acc[2]), "f"(acc[3]) : "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(empty0 + 8 * stage);
             advance();

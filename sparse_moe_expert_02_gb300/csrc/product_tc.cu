@@ -555,8 +555,6 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
                     const uint8_t* line = smem + kOffCodes + mine * kCodeBytes + t * 32;
                     q[0] = *(const uint4*)(line + ((t >> 2) & 1) * 16);
                     q[1] = *(const uint4*)(line + (~(t >> 2) & 1) * 16);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(cempty0 + 8 * mine);
                 }
                 ok = __all_sync(0xffffffffu, mbar_wait(empty0 + 8 * stage, phase ^ 1, lim, abort_flag));
                 if (!ok) break;
@@ -571,6 +569,10 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) st_shared16(row + (((4 * h + j) ^ (t & 7)) << 4), values8<FEED>(w[j], z, sc[h]));
                     }
+                    __syncwarp();
+                    // Only now, when the codes have been used: an arrival does not order loads that are on their way
+                    // with TMA's writes, and right behind the loads it let the next codes overwrite some.
+                    if (lane == 0) mbar_arrive(cempty0 + 8 * mine);
                     fetch(k + kGroups);
                 } else if (p.f_copy) {
                     const bf16* src = OP == kProductFwd   ? p.f + ((int64_t)un.g * p.N + un.f0) * p.ldf + c
