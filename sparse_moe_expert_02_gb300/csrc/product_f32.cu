@@ -21,12 +21,13 @@ namespace f32 {
 constexpr int kThreads = 256;
 
 template <int BM> struct Tile {
-    static constexpr int BK = BM == 32 ? 32 : 16, kStages = BM == 128 ? 3 : 4, TM = BM / 16, LD = BM + 4;
-    static constexpr int V = TM < 4 ? TM : 4;  // floats of a read
+    static constexpr int BK = BM == 128 ? 16 : 32, kStages = BM == 32 ? 4 : 3, LD = BM + 4;
+    static constexpr int TM = BM == 32 ? 4 : 8;                             // a thread's sums: TM x TM
+    static constexpr int kSide = BM / TM, kGroups = kThreads / (kSide * kSide);  // threads along a side; groups that share a step's places
     static constexpr int kBytes = kStages * 2 * BK * LD * 4;
-    static constexpr int kBlocks = BM == 128 ? 2 : 4;  // an SM
+    static constexpr int kBlocks = BM == 32 ? 4 : 2;  // an SM
     // the thread's i-th row or column
-    __device__ __forceinline__ static int at(int i, int t) { return (i / V) * 16 * V + t * V + i % V; }
+    __device__ __forceinline__ static int at(int i, int t) { return (i / 4) * 4 * kSide + t * 4 + i % 4; }
 };
 
 // Four bytes to shared memory, or zeros.
@@ -49,7 +50,7 @@ __global__ void __launch_bounds__(kThreads, Tile<BM>::kBlocks) product_f32_kerne
     if (threadIdx.x < 32) group_table(tab, p.offsets, p.G, p.rows, BM);
     __syncthreads();
     pdl_release();
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int tid = threadIdx.x, group = tid / (T::kSide * T::kSide), tx = tid % T::kSide, ty = tid / T::kSide % T::kSide;
     const int cols = OP == kProductFwd ? p.N : p.K;  // of the output
     const int cb = (cols + BM - 1) / BM, nb = (p.N + BM - 1) / BM;
     const int64_t units = OP == kProductDw ? (int64_t)p.G * nb * cb : (int64_t)tab.tiles[p.G] * cb;
@@ -104,18 +105,13 @@ __global__ void __launch_bounds__(kThreads, Tile<BM>::kBlocks) product_f32_kerne
             const float* sa = ring + (s % T::kStages) * (2 * BK * LD);
             const float* sb = sa + BK * LD;
 #pragma unroll
-            for (int kk = 0; kk < BK; ++kk) {
+            for (int k = 0; k < BK / T::kGroups; ++k) {
+                const int kk = k * T::kGroups + group;
                 float x[TM], y[TM];
 #pragma unroll
-                for (int h = 0; h < TM / T::V; ++h) {
-                    const float *px = sa + kk * LD + T::at(h * T::V, ty), *py = sb + kk * LD + T::at(h * T::V, tx);
-                    if constexpr (T::V == 4) {
-                        *(float4*)(x + 4 * h) = *(const float4*)px;
-                        *(float4*)(y + 4 * h) = *(const float4*)py;
-                    } else {
-                        *(float2*)x = *(const float2*)px;
-                        *(float2*)y = *(const float2*)py;
-                    }
+                for (int h = 0; h < TM; h += 4) {
+                    *(float4*)(x + h) = *(const float4*)(sa + kk * LD + T::at(h, ty));
+                    *(float4*)(y + h) = *(const float4*)(sb + kk * LD + T::at(h, tx));
                 }
 #pragma unroll
                 for (int i = 0; i < TM; ++i)
@@ -124,7 +120,26 @@ __global__ void __launch_bounds__(kThreads, Tile<BM>::kBlocks) product_f32_kerne
             }
         }
         wait_all_but<0>();
-        __syncthreads();  // the ring is free for the next unit
+        __syncthreads();  // the ring is free
+        if constexpr (T::kGroups == 4) {  // groups 2 and 3 to 0 and 1, then 1 to 0
+            static_assert(T::kBytes >= 2 * BM * BM * 4, "the ring holds two tiles");
+            const int lane = tid % (T::kSide * T::kSide);
+#pragma unroll
+            for (int from = 2; from; from /= 2) {
+                float* half = ring + (group & (from - 1)) * BM * BM + lane;
+                if (group >= from && group < 2 * from) {
+#pragma unroll
+                    for (int i = 0; i < TM * TM; ++i) half[i * T::kSide * T::kSide] = acc[i / TM][i % TM];
+                }
+                __syncthreads();
+                if (group < from) {
+#pragma unroll
+                    for (int i = 0; i < TM * TM; ++i) acc[i / TM][i % TM] += half[i * T::kSide * T::kSide];
+                }
+                __syncthreads();
+            }
+            if (group) continue;
+        }
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
             const int r = i0 + T::at(i, ty);
@@ -162,8 +177,8 @@ template <int OP> cudaError_t launch_op(const GroupProduct& g, int num_sms, cuda
         if (OP == kProductDw) return g.G * cdiv(g.N, bm) * cdiv(cols, bm);
         return (cdiv(g.rows, bm) + std::min(g.G - 1, g.rows)) * cdiv(cols, bm);
     };
-    if (units(128) >= 2 * num_sms) return launch<OP, 128>(g, units(128), num_sms, s);
-    if (units(64) >= 2 * num_sms) return launch<OP, 64>(g, units(64), num_sms, s);
+    if (units(128) >= num_sms) return launch<OP, 128>(g, units(128), num_sms, s);
+    if (units(64) >= num_sms) return launch<OP, 64>(g, units(64), num_sms, s);
     return launch<OP, 32>(g, units(32), num_sms, s);
 }
 
