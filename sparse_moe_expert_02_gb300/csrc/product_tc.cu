@@ -304,7 +304,9 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     constexpr int kUnitF = PAIR ? 2 * BF : BF;
     const int F = f_size<OP>(p), FB = (F + kUnitF - 1) / kUnitF, NB = (p.N + p.tile_i - 1) / p.tile_i;
-    const int units = (OP == kProductDw ? p.G * NB : tab.tiles[p.G]) * FB;
+    // (a split has a cluster for each unit that ascending offsets can give)
+    const int most = SPLIT ? (int)gridDim.x / p.split : 0x7FFFFFFF;
+    const int units = min((OP == kProductDw ? p.G * NB : tab.tiles[p.G]) * FB, most);
     // Units of this CTA: u0, u0 + step, ...  Split: a cluster takes one unit or none.
     const int rank = SPLIT ? (int)cluster_rank() : 0, cl = SPLIT ? p.split : 1;
     const int crank = PAIR ? (int)cluster_rank() : 0, per = PAIR ? 2 : cl;  // of a pair: 0 leads (issues the MMAs)
