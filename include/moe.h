@@ -526,7 +526,8 @@ MOE_API moe_status moe_int4_dequantize(const uint8_t* codes, const void* scales,
 /* Rows of 16- or 32-bit activations times 4-bit weights, fp32 sums:
  *   out[r][n] = sum_k x[r][k] w_g[n][k]
  * x [rows, K] and out [rows, N] fp32 or bf16; w_g the values of [G, N] rows of
- * K columns as above. */
+ * K columns as above, exact where x is fp32 or rows is at most 8 G or 32; for
+ * more rows of bf16 each value is rounded to bf16 once. */
 MOE_API moe_status moe_int4_gemm(const void* x, int32_t dtype, int64_t ld_x, const uint8_t* codes, const void* scales,
                                  int32_t scale_dtype, const uint8_t* zeros, int32_t group, const int32_t* offsets,
                                  int32_t rows, int32_t G, int32_t N, int32_t K, void* out, int32_t out_dtype,

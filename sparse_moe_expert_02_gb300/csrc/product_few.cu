@@ -1,25 +1,28 @@
 // Products of a few rows with their groups' weights, bf16 or 4-bit
 // (moe_grouped_gemm, moe_int4_gemm): out[r][n] = sum_k x[r][k] w_g[n][k].
 //
-// Bound by the bytes of the weights, so they go from memory to registers and
-// straight into mma.sync (m16n8k16: 16 features by 8 rows), with nothing
-// between: a tensor-memory kernel would write what it decodes to shared memory
-// first, for tiles of 128 features that a few rows do not fill.  A block takes
-// 16 features of a group at a time, its eight warps a piece of the columns
-// each; a warp has the loads of its next 512 columns in flight while it
-// multiplies.  The order of the columns within a sum is free as long as x
-// follows it, so a lane loads 16 bytes of a row and hands them to successive
-// MMAs.  Eight partial sums meet in shared memory.  How the columns are
+// Bound by the bytes of the weights, and with 4 bits by the instructions that
+// decode them, so they go straight into mma.sync (m16n8k16: 16 features by 8
+// rows): a tensor-memory kernel would write what it decodes to shared memory
+// first, for tiles of 128 features by 16 rows that a few rows do not fill.  A
+// block takes 16 features of a group at a time, its eight warps a piece of the
+// columns each; eight partial sums meet in shared memory.  How the columns are
 // divided depends on K alone, so a row's result does not depend on the other
-// rows and groups.
+// rows and groups.  The order of the columns within a sum is free as long as x
+// follows it, so a lane loads 16 bytes of a row and hands them to successive
+// MMAs.
 //
 // 4 bits: the MMAs sum code - zero, exact in bf16, over one group of columns;
-// the fp32 sum is then multiplied by the scale.  Groups of 32 and 64 columns
-// need the four lanes that share an MMA's columns to hold codes of the same
-// group: they exchange words first.  fp32 rows go in as three bf16 parts,
-// which hold all 24 bits.  A group's sum may overflow where its product with
-// the scale does not, so what comes out as no finite number is summed again
-// with the weights' values.
+// the fp32 sum is then multiplied by the scale.  fp32 rows go in as three bf16
+// parts, which hold all 24 bits.  A group's sum may overflow where its product
+// with the scale does not, so what comes out as no finite number is summed
+// again with the weights' values.
+//
+// This kernel: any alignment of x and scales, and columns that 128 does not
+// divide; weights to registers, two chunks of 128 columns ahead.  Groups of 32
+// and 64 columns need the four lanes that share an MMA's columns to hold codes
+// of the same group: they exchange words.  The other, for the rest, is in
+// product_few_bulk.cu.
 #include <algorithm>
 
 #include "few_rows.cuh"
