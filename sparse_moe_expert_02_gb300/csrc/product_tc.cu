@@ -128,9 +128,9 @@ template <bool PAIR> __device__ __forceinline__ void load3(uint32_t dst, const C
             : "memory");
     }
 }
-// Arrival at another CTA's barrier that orders nothing before it.
-__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// Arrival at another CTA's barrier, which orders no writes for that CTA.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 __device__ __forceinline__ void st_shared16(uint32_t a, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
                                 fb = tail0 + 8 * stage;
                                 mbar_expect_tx(fb, bytes);
                             } else if (OP == kProductDw) {
-                                mbar_arrive_relaxed(mapa_shared(fb, 0));
+                                mbar_arrive_remote(mapa_shared(fb, 0));
                             }
                             if (!ragged) fb = mapa_shared(fb, 0);
                             else fb = mapa_shared(fb, (uint32_t)crank);
@@ -702,9 +702,9 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    // (relaxed: what it orders are loads from tensor memory, which are complete; a release at the
-                    // other CTA would wait for the stores above)
-                    if (PAIR) mbar_arrive_relaxed(mapa_shared(te, 0));
+                    // (what this orders are loads from tensor memory, which are complete; a release for the cluster
+                    // would wait for the stores above)
+                    if (PAIR) mbar_arrive_remote(mapa_shared(te, 0));
                     else mbar_arrive(te);
                 }
             }
