@@ -18,7 +18,7 @@
 namespace moe {
 namespace f32 {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kMaxSplit = 8;
 
 template <int BM> struct Tile {
     static constexpr int BK = BM == 128 ? 16 : 32, kStages = BM == 32 ? 4 : 3, LD = BM + 4;
@@ -45,8 +45,9 @@ __device__ __forceinline__ void copy4(uint32_t dst, const float* src, bool in) {
 __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void wait_all_but() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-template <int OP, int BM>
-__global__ void __launch_bounds__(kThreads, Tile<BM>::kBlocks) product_f32_kernel(const GroupProduct p) {
+// SPLIT: a cluster of `split` blocks shares each tile's sum.
+template <int OP, int BM, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, Tile<BM>::kBlocks) product_f32_kernel(const GroupProduct p, const int split) {
     using T = Tile<BM>;
     constexpr int TM = T::TM, BK = T::BK, LD = T::LD, kEach = BM * BK / kThreads;
     constexpr bool kAK = OP != kProductDw, kBK = OP == kProductFwd;  // contiguous along the sum
@@ -62,7 +63,8 @@ __global__ void __launch_bounds__(kThreads, Tile<BM>::kBlocks) product_f32_kerne
     const int cols = OP == kProductFwd ? p.N : p.K;  // of the output
     const int cb = (cols + BM - 1) / BM, nb = (p.N + BM - 1) / BM;
     const int64_t units = OP == kProductDw ? (int64_t)p.G * nb * cb : (int64_t)tab.tiles[p.G] * cb;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int rank = SPLIT ? (int)tc::cluster_rank() : 0, team = SPLIT ? split : 1;
+    for (int64_t u = blockIdx.x / team; u < units; u += gridDim.x / team) {
         const int t = (int)(u / cb), c0 = (int)(u - (int64_t)t * cb) * BM;
         int g, i0, i1, k0, k1;  // rows of the tile [i0, i1), the sum's range
         if (OP == kProductDw) {
@@ -83,6 +85,11 @@ __global__ void __launch_bounds__(kThreads, Tile<BM>::kBlocks) product_f32_kerne
         const int ak = kAK ? tid % BK : tid / BM, ai = kAK ? tid / BK : tid % BM;
         const int bk = kBK ? tid % BK : tid / BM, bi = kBK ? tid / BK : tid % BM;
         constexpr int kNextI = kThreads / BK, kNextK = kThreads / BM;
+        if (SPLIT) {  // this block's part of the sum
+            const int n = (k1 - k0 + BK - 1) / BK, from = k0;
+            k0 = from + (int)((int64_t)n * rank / split) * BK;
+            k1 = min(k1, from + (int)((int64_t)n * (rank + 1) / split) * BK);
+        }
         const float* pa = kAK ? a + (int64_t)(i0 + ai) * p.lda + k0 + ak : a + (int64_t)(k0 + ak) * p.lda + i0 + ai;
         const int64_t brow = OP == kProductDw ? 0 : (int64_t)g * p.N;  // row of B that its index 0 is
         const float* pb = kBK ? b + (brow + c0 + bi) * ldb + k0 + bk : b + (brow + k0 + bk) * ldb + c0 + bi;
@@ -153,8 +160,30 @@ __global__ void __launch_bounds__(kThreads, Tile<BM>::kBlocks) product_f32_kerne
                 }
                 __syncthreads();
             }
-            if (group) continue;
         }
+        if constexpr (SPLIT) {
+            // Every rank's tile to the first one's ring, [rank][sum][thread], which adds them up in their order.
+            constexpr int kTeam = T::kSide * T::kSide;
+            static_assert(T::kBytes >= kMaxSplit * BM * BM * 4, "the ring holds every rank's tile");
+            tc::cluster_sync();  // the first one's ring is free
+            if (group == 0) {
+                const uint32_t to = tc::mapa_shared(tc::smem_u32(ring) + (rank * BM * BM + tid) * 4, 0);
+#pragma unroll
+                for (int i = 0; i < TM * TM; ++i)
+                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + i * kTeam * 4), "f"(acc[i / TM][i % TM]) : "memory");
+            }
+            tc::cluster_sync();
+            if (rank == 0 && group == 0) {
+#pragma unroll
+                for (int i = 0; i < TM * TM; ++i) {
+                    float v = 0.0f;
+                    for (int r = 0; r < split; ++r) v += ring[r * BM * BM + i * kTeam + tid];
+                    acc[i / TM][i % TM] = v;
+                }
+            }
+            __syncthreads();  // the ring is free
+        }
+        if (group || (SPLIT && rank)) continue;
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
             const int r = i0 + T::at(i, ty);
@@ -177,11 +206,11 @@ __global__ void __launch_bounds__(kThreads, Tile<BM>::kBlocks) product_f32_kerne
     }
 }
 
-template <int OP, int BM> cudaError_t launch(const GroupProduct& g, int64_t units, int num_sms, cudaStream_t s) {
-    cudaError_t e = ensure_smem_attr((const void*)product_f32_kernel<OP, BM>, Tile<BM>::kBytes);
+template <int OP, int BM, bool SPLIT> cudaError_t launch(const GroupProduct& g, int64_t units, int split, int num_sms, cudaStream_t s) {
+    cudaError_t e = ensure_smem_attr((const void*)product_f32_kernel<OP, BM, SPLIT>, Tile<BM>::kBytes);
     if (e != cudaSuccess) return e;
-    e = launch_kernel(product_f32_kernel<OP, BM>, dim3((unsigned)std::min<int64_t>(units, Tile<BM>::kBlocks * num_sms)), dim3(kThreads),
-                      Tile<BM>::kBytes, s, 1, g);
+    e = launch_kernel(product_f32_kernel<OP, BM, SPLIT>, dim3((unsigned)(std::min<int64_t>(units, Tile<BM>::kBlocks * num_sms) * split)),
+                      dim3(kThreads), Tile<BM>::kBytes, s, split, g, split);
     count_launches(1);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -192,9 +221,15 @@ template <int OP> cudaError_t launch_op(const GroupProduct& g, int num_sms, cuda
         if (OP == kProductDw) return g.G * cdiv(g.N, bm) * cdiv(cols, bm);
         return (cdiv(g.rows, bm) + std::min(g.G - 1, g.rows)) * cdiv(cols, bm);
     };
-    if (units(128) >= num_sms) return launch<OP, 128>(g, units(128), num_sms, s);
-    if (units(64) >= num_sms) return launch<OP, 64>(g, units(64), num_sms, s);
-    return launch<OP, 32>(g, units(32), num_sms, s);
+    if (units(128) >= num_sms) return launch<OP, 128, false>(g, units(128), 1, num_sms, s);
+    if (units(64) >= num_sms) return launch<OP, 64, false>(g, units(64), 1, num_sms, s);
+    // Few tiles: a cluster for each, whose blocks split the sum (of dw at most all rows).  dx of 45 x 2536 x 41:
+    // 10.8 us, 38 without.
+    int split = 1;
+    const int64_t steps = cdiv(OP == kProductFwd ? g.K : OP == kProductDx ? g.N : g.rows, Tile<32>::BK);
+    while (split < kMaxSplit && units(32) * split * 2 <= num_sms && steps >= 8 * split) split *= 2;
+    if (split > 1) return launch<OP, 32, true>(g, units(32), split, num_sms, s);
+    return launch<OP, 32, false>(g, units(32), 1, num_sms, s);
 }
 
 }  // namespace f32

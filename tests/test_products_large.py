@@ -98,3 +98,34 @@ def test_few_rows_of_many_tiles(G, N, K):
     first = grouped.matmul(x, w, offsets_of(sizes))
     for _ in range(3):
         assert torch.equal(grouped.matmul(x, w, offsets_of(sizes)), first)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("op,rows,N,K,G", [("dx", 45, 2536, 41, 1), ("fwd", 33, 20, 5000, 1), ("fwd", 70, 40, 1111, 3), ("dw", 3001, 33, 65, 1), ("dw", 1501, 70, 40, 4),
+                                           ("dx", 1, 4096, 8, 1)])
+def test_product_of_few_tiles_and_long_sums(op, rows, N, K, G, dtype):
+    a, b = operands(op, rows + 3, N, K, G, DT[dtype])
+    at = offsets_of(ragged(rows, G, rows) if G > 1 else [rows], 2)
+    for out_dtype in DT.values():
+        check(op, a, b, at, randn(gen(5), *out_shape(op, rows + 3, N, K, G), dtype=out_dtype))
+        if op == "dw":
+            check(op, a, b, at, randn(gen(5), G, N, K, dtype=out_dtype), accumulate=True)
+    first = {"fwd": grouped.matmul, "dx": grouped.matmul_dx, "dw": grouped.matmul_dw}[op](a, b, at)
+    again = {"fwd": grouped.matmul, "dx": grouped.matmul_dx, "dw": grouped.matmul_dw}[op](a, b, at)
+    lo, hi = int(at[0]), int(at[-1])
+    assert torch.equal(first[lo:hi] if op != "dw" else first, again[lo:hi] if op != "dw" else again)
+
+
+@pytest.mark.parametrize("op", ["fwd", "dx", "dw"])
+@pytest.mark.parametrize("each", [3, 20])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_most_groups(op, each, dtype):
+    """1025 groups, every third of them empty."""
+    G, N, K = 1025, 40, 72
+    sizes = [each * (i % 3) for i in range(G)]
+    rows = sum(sizes)
+    a, b = operands(op, rows, N, K, G, DT[dtype])
+    check(op, a, b, offsets_of(sizes), randn(gen(1), *out_shape(op, rows, N, K, G)))
+    if op == "fwd":
+        x = randn(gen(3), rows, 96, dtype=DT[dtype])
+        check4(x, weights4(G, N, 96, 32, True, "bf16"), offsets_of(sizes), randn(gen(2), rows, N, dtype=DT[dtype]))
