@@ -355,7 +355,9 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
                     if (elect_one()) {
                         uint32_t fb = full0 + 8 * stage;
                         const uint32_t fs = smem0 + stage * p.stage_bytes, rs = fs + kFBytes;
-                        const int rlines = kRAlongC ? n16 * 16 : slabs * c16 * 16, flines = kFAlongC ? BF : 2 * c16 * 16;
+                        // boxes of 64 rows, then of 16 (of three, 64 once more: what they bring is ignored)
+                        const int n64 = (n16 + 1) >> 2, rows = max(n16, 4 * n64) * 16;
+                        const int rlines = kRAlongC ? rows : slabs * c16 * 16, flines = kFAlongC ? BF : 2 * c16 * 16;
                         const uint32_t bytes = (f_tma ? flines * kLine : 0) + (r_tma ? rlines * kLine : 0);
                         if (!PAIR) {
                             mbar_expect_tx(fb, bytes);
@@ -391,7 +393,6 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
                         }
                         if (r_tma) {
                             if (kRAlongC) {
-                                const int n64 = n16 >> 2;
                                 for (int j = 0; j < n64; ++j) load2<PAIR>(rs + j * 64 * kLine, &tm_r, fb, c, i0 + j * 64);
                                 for (int j = 4 * n64; j < n16; ++j) load2<PAIR>(rs + j * 16 * kLine, &tm_r16, fb, c, i0 + j * 16);
                             } else {
