@@ -13,7 +13,6 @@ namespace few_rows {
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kF = 16, kRows = 8;   // features and rows of a tile
 constexpr int kChunk = 128;         // columns a warp takes at a time
-constexpr int kPitch = 20;          // floats between the rows of a partial tile: lanes hit different banks
 
 struct Args {
     const int32_t* offsets;
@@ -49,18 +48,22 @@ template <int LG, typename TS> __device__ __forceinline__ float scale_of(const C
 // Units are (row tile, feature tile).  list: group and tile within it of each
 // row tile, so that a block finds its next unit without a search.
 constexpr int kMaxTiles = 2 * kProductMaxG;  // (8 rows a group; fp32 rows may be more)
-struct Tables {
+struct TileList {
     GroupTable groups;
     uint32_t list[kMaxTiles];
-    float part[2][kWarps][kRows * kPitch];
+};
+// F features a tile; their partial sums, for two units in turn or one.
+template <int F = kF, int BUFS = 2> struct Tables : TileList {
+    static constexpr int kPitch = F + 4;  // floats between the rows of a partial tile: lanes hit different banks
+    float part[BUFS][kWarps][kRows * kPitch];
 };
 struct Unit {
     int g, f0, row0, n;  // group, first feature, first row of the tile and how many
 };
-__device__ __forceinline__ Unit unit_at(int u, int FB, int G, const Tables& t) {
+template <int F = kF> __device__ __forceinline__ Unit unit_at(int u, int FB, int G, const TileList& t) {
     Unit r;
     const int rt = u / FB;
-    r.f0 = (u - rt * FB) * kF;
+    r.f0 = (u - rt * FB) * F;
     if (t.groups.tiles[G] <= kMaxTiles) {
         const uint32_t e = t.list[rt];
         r.g = (int)(e & 2047u);
@@ -74,7 +77,7 @@ __device__ __forceinline__ Unit unit_at(int u, int FB, int G, const Tables& t) {
 }
 
 // False where this block has no unit.
-__device__ __forceinline__ bool build_tables(Tables& t, const Args& p) {
+__device__ __forceinline__ bool build_tables(TileList& t, const Args& p) {
     if (threadIdx.x < 32) group_table(t.groups, p.offsets, p.G, p.rows, kRows);
     __syncthreads();
     pdl_release();
@@ -169,34 +172,36 @@ __device__ __forceinline__ __nv_bfloat162 zero_pair(uint32_t z, int gr) {
 
 // A warp's sums to its partial tile: D(g, 2t), D(g, 2t + 1), D(g + 8, 2t) and
 // D(g + 8, 2t + 1), feature and row.
-__device__ __forceinline__ void put_part(float* mine, const float (&acc)[4], int g, int t) {
+template <int F = kF> __device__ __forceinline__ void put_part(float* mine, const float (&acc)[4], int g, int t) {
 #pragma unroll
-    for (int m = 0; m < 4; ++m) mine[(2 * t + (m & 1)) * kPitch + g + 8 * (m >> 1)] = acc[m];
+    for (int m = 0; m < 4; ++m) mine[(2 * t + (m & 1)) * (F + 4) + g + 8 * (m >> 1)] = acc[m];
 }
 // The partial tiles' sum, stored; by kThreads threads.
-template <int LG, typename T>
-__device__ __forceinline__ void finish(const Args& p, const float (*part)[kRows * kPitch], const Unit& cur, int nb) {
-    const int f = threadIdx.x & (kF - 1), r = threadIdx.x / kF;
-    if (r >= cur.n || cur.f0 + f >= p.N) return;
-    float v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += part[w][r * kPitch + f];
-    if constexpr (LG != 0) {
-        if (!isfinite(v)) {  // a group's sum may have overflown before its scale
-            const T* x = (const T*)p.x + (int64_t)(cur.row0 + r) * p.ldx;
-            const int64_t row = (int64_t)cur.g * p.N + cur.f0 + f;
-            v = 0.0f;
-            for (int k = 0; k < p.K; ++k) {
-                const int64_t at = row * nb + (k >> LG);
-                const int cd = (p.q.codes[row * (p.K / 2) + (k >> 1)] >> (4 * (k & 1))) & 15;
-                const float s = p.q.scale_elem == kF32 ? ((const float*)p.q.scales)[at] : to_f32(((const bf16*)p.q.scales)[at]);
-                v = fmaf(to_f32(x[k]), (float)(cd - (p.q.zeros ? p.q.zeros[at] : 8)) * s, v);
+template <int LG, typename T, int F = kF>
+__device__ __forceinline__ void finish(const Args& p, const float (*part)[kRows * (F + 4)], const Unit& cur, int nb) {
+    const int f = threadIdx.x & (F - 1);
+    if (cur.f0 + f >= p.N) return;
+    for (int r = threadIdx.x / F; r < cur.n; r += kThreads / F) {
+        float v = 0.0f;
+    #pragma unroll
+        for (int w = 0; w < kWarps; ++w) v += part[w][r * (F + 4) + f];
+        if constexpr (LG != 0) {
+            if (!isfinite(v)) {  // a group's sum may have overflown before its scale
+                const T* x = (const T*)p.x + (int64_t)(cur.row0 + r) * p.ldx;
+                const int64_t row = (int64_t)cur.g * p.N + cur.f0 + f;
+                v = 0.0f;
+                for (int k = 0; k < p.K; ++k) {
+                    const int64_t at = row * nb + (k >> LG);
+                    const int cd = (p.q.codes[row * (p.K / 2) + (k >> 1)] >> (4 * (k & 1))) & 15;
+                    const float s = p.q.scale_elem == kF32 ? ((const float*)p.q.scales)[at] : to_f32(((const bf16*)p.q.scales)[at]);
+                    v = fmaf(to_f32(x[k]), (float)(cd - (p.q.zeros ? p.q.zeros[at] : 8)) * s, v);
+                }
             }
         }
+        const int64_t at = (int64_t)(cur.row0 + r) * p.ldo + cur.f0 + f;
+        if (p.out_elem == kF32) ((float*)p.out)[at] = v;
+        else ((bf16*)p.out)[at] = __float2bfloat16_rn(v);
     }
-    const int64_t at = (int64_t)(cur.row0 + r) * p.ldo + cur.f0 + f;
-    if (p.out_elem == kF32) ((float*)p.out)[at] = v;
-    else ((bf16*)p.out)[at] = __float2bfloat16_rn(v);
 }
 
 

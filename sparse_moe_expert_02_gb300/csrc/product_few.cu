@@ -62,7 +62,7 @@ template <int LG> __device__ __forceinline__ int column(int i, int t) {
 
 template <int LG, typename T, typename TS> __global__ void __launch_bounds__(kThreads, 2) product_few_kernel(const Args p) {
     constexpr int kDepth = 2;  // (4: the same within 5 %)
-    __shared__ Tables tab;
+    __shared__ Tables<> tab;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     pdl_wait();
     if (!build_tables(tab, p)) return;

@@ -129,3 +129,21 @@ def test_the_most_groups(op, each, dtype):
     if op == "fwd":
         x = randn(gen(3), rows, 96, dtype=DT[dtype])
         check4(x, weights4(G, N, 96, 32, True, "bf16"), offsets_of(sizes), randn(gen(2), rows, N, dtype=DT[dtype]))
+
+
+@pytest.mark.parametrize("group,zeros,scale", [(128, False, "bf16"), (64, True, "bf16"), (32, True, "f32"), (32, False, "bf16")])
+@pytest.mark.parametrize("G,N,K", [(128, 1000, 1024), (100, 1024, 384), (200, 960, 128), (60, 2056, 1024)])
+def test_int4_few_rows_of_short_columns(group, zeros, scale, G, N, K):
+    sizes = [(5 * i) % 11 for i in range(G)]
+    rows = sum(sizes)
+    x = randn(gen(1), rows, K, dtype=torch.bfloat16)
+    w = weights4(G, N, K, group, zeros, scale)
+    for out_dtype in DT.values():
+        check4(x, w, offsets_of(sizes), randn(gen(2), rows, N, dtype=out_dtype))
+    out = int4.matmul(x, w, offsets_of(sizes))
+    for _ in range(3):
+        assert torch.equal(int4.matmul(x, w, offsets_of(sizes)), out)
+    x[7] = float("nan")
+    bad = int4.matmul(x, w, offsets_of(sizes))
+    keep = [r for r in range(rows) if r != 7]
+    assert torch.isnan(bad[7]).all() and torch.equal(bad[keep], out[keep])
