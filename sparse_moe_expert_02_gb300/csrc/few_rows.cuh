@@ -76,8 +76,11 @@ template <int F = kF> __device__ __forceinline__ Unit unit_at(int u, int FB, int
     return r;
 }
 
-// False where this block has no unit.
-__device__ __forceinline__ bool build_tables(TileList& t, const Args& p) {
+// The tables, and the number of units with tiles of F features: a block at or
+// past it has none, and must not ask for one (its entry of the list is not
+// written).  The grid is made for the most tiles that the rows of x may give,
+// which are more than these where rows belong to no group or groups are empty.
+template <int F = kF> __device__ __forceinline__ int build_tables(TileList& t, const Args& p) {
     if (threadIdx.x < 32) group_table(t.groups, p.offsets, p.G, p.rows, kRows);
     __syncthreads();
     pdl_release();
@@ -85,7 +88,7 @@ __device__ __forceinline__ bool build_tables(TileList& t, const Args& p) {
         for (int i = threadIdx.x; i < p.G; i += blockDim.x)
             for (int j = t.groups.tiles[i], n = 0; j < t.groups.tiles[i + 1]; ++j, ++n) t.list[j] = (uint32_t)i | (uint32_t)n << 11;
     __syncthreads();
-    return (int64_t)blockIdx.x < (int64_t)t.groups.tiles[p.G] * ((p.N + kF - 1) / kF);
+    return t.groups.tiles[p.G] * ((p.N + F - 1) / F);
 }
 
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {

@@ -65,8 +65,8 @@ template <int LG, typename T, typename TS> __global__ void __launch_bounds__(kTh
     __shared__ Tables<> tab;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     pdl_wait();
-    if (!build_tables(tab, p)) return;
-    const int FB = (p.N + kF - 1) / kF, units = tab.groups.tiles[p.G] * FB, step = gridDim.x;
+    const int FB = (p.N + kF - 1) / kF, units = build_tables(tab, p), step = gridDim.x;
+    if ((int)blockIdx.x >= units) return;
     const int chunks = (p.K + kChunk - 1) / kChunk;
     const int k0 = chunks * warp / kWarps, nk = chunks * (warp + 1) / kWarps - k0, batches = (nk + kDepth - 1) / kDepth;
     const int nb = LG ? (p.K + (1 << LG) - 1) >> LG : 0;

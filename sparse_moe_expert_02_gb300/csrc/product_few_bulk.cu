@@ -71,8 +71,8 @@ __global__ void __launch_bounds__(kAllThreads, 2) product_few_bulk_kernel(const 
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     pdl_wait();
-    if (!build_tables(tab, p)) return;
-    const int FB = (p.N + F - 1) / F, units = tab.groups.tiles[p.G] * FB, step = gridDim.x;
+    const int FB = (p.N + F - 1) / F, units = build_tables<F>(tab, p), step = gridDim.x;
+    if ((int)blockIdx.x >= units) return;
     const int nb = kCoded ? p.K >> (kCoded ? LG : 7) : 0, chunks = p.K / kChunk;
     const int per_unit = kCoded ? 1 : (p.K + kDenseCols - 1) / kDenseCols;  // stages
     int stage = 0;
