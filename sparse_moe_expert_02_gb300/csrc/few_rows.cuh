@@ -100,7 +100,7 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
 // Weights are read once: no place in L1, which x keeps.
 __device__ __forceinline__ uint4 load_once(const void* p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
 
@@ -112,22 +112,22 @@ template <typename T> struct Parts { static constexpr int n = sizeof(T) == 4 ? 3
 
 template <bool VEC> __device__ __forceinline__ void load_x(const bf16* x, Parts<bf16>& o) {
     if constexpr (VEC) {
-        const uint4 v = __ldg((const uint4*)x);
+        const uint4 v = *(const uint4*)x;
         o.v[0][0] = v.x; o.v[0][1] = v.y; o.v[0][2] = v.z; o.v[0][3] = v.w;
     } else {
         const uint16_t* h = (const uint16_t*)x;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o.v[0][j] = (uint32_t)__ldg(h + 2 * j) | (uint32_t)__ldg(h + 2 * j + 1) << 16;
+        for (int j = 0; j < 4; ++j) o.v[0][j] = (uint32_t)h[2 * j] | (uint32_t)h[2 * j + 1] << 16;
     }
 }
 template <bool VEC> __device__ __forceinline__ void load_x(const float* x, Parts<float>& o) {
     float f[8];
     if constexpr (VEC) {
-        *(float4*)f = __ldg((const float4*)x);
-        *(float4*)(f + 4) = __ldg((const float4*)x + 1);
+        *(float4*)f = *(const float4*)x;
+        *(float4*)(f + 4) = *((const float4*)x + 1);
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = __ldg(x + j);
+        for (int j = 0; j < 8; ++j) f[j] = x[j];
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {

@@ -1,6 +1,12 @@
 // Which rows belong to which group, for the kernels of the experts' products.
 // The offsets live on the device, so every block builds the table of the
 // groups' tiles for itself, in shared memory.
+//
+// These kernels start while the one before them, which may write any of their
+// inputs, ends (common.cuh, programmatic dependent launch).  So none of them
+// loads by the read-only path, which is for data that nothing writes as long as
+// the kernel runs: offsets, rows, weights, scales and zero points come by plain
+// loads behind the wait, or by TMA.
 #pragma once
 
 #include "common.cuh"
@@ -20,8 +26,8 @@ struct GroupTable {
 // end lies before its start has none.
 __device__ __forceinline__ int2 group_rows(const int32_t* offsets, int g, int rows) {
     if (!offsets) return make_int2(0, rows);
-    const int lo = min(max(__ldg(offsets + g), 0), rows);
-    return make_int2(lo, min(max(__ldg(offsets + g + 1), lo), rows));
+    const int lo = min(max(offsets[g], 0), rows);
+    return make_int2(lo, min(max(offsets[g + 1], lo), rows));
 }
 
 // By one converged warp; the block synchronises afterwards.

@@ -106,14 +106,14 @@ template <int LG, typename T, typename TS> __global__ void __launch_bounds__(kTh
                 for (int j = 0; j < (C::kScale ? C::kScale : 1); ++j) v.s[h][j] = 0;
                 if (!on) continue;
                 const int64_t at = sp[h] + i * C::kGroups;
-                                    const int g0 = (k0 + fb * kDepth + i) * C::kGroups;
-                #pragma unroll
-                                    for (int j = 0; j < C::kGroups; ++j) {
-                                        if (g0 + j >= nb) continue;
-                                        if (sizeof(TS) == 4) v.s[h][j] = __ldg((const uint32_t*)p.q.scales + at + j);
-                                        else v.s[h][j >> 1] |= (uint32_t)__ldg((const uint16_t*)p.q.scales + at + j) << (16 * (j & 1));
-                                        if (p.q.zeros) v.z[h] = (v.z[h] & ~(255u << (8 * j))) | (uint32_t)__ldg(p.q.zeros + at + j) << (8 * j);
-                                    }
+                const int g0 = (k0 + fb * kDepth + i) * C::kGroups;
+#pragma unroll
+                for (int j = 0; j < C::kGroups; ++j) {
+                    if (g0 + j >= nb) continue;
+                    if (sizeof(TS) == 4) v.s[h][j] = ((const uint32_t*)p.q.scales)[at + j];
+                    else v.s[h][j >> 1] |= (uint32_t)((const uint16_t*)p.q.scales)[at + j] << (16 * (j & 1));
+                    if (p.q.zeros) v.z[h] = (v.z[h] & ~(255u << (8 * j))) | (uint32_t)p.q.zeros[at + j] << (8 * j);
+                }
             }
         }
     };

@@ -199,9 +199,9 @@ __device__ __forceinline__ void store_block(uint8_t* st, const uint32_t* w, bf16
 template <int WIDTH> __device__ __forceinline__ uint32_t load_if(const uint16_t* p, bool in) {
     uint32_t v;
     if (WIDTH == 2)
-        asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n mov.b32 %0, 0;\n @q ld.global.nc.b32 %0, [%1];\n}\n" : "=r"(v) : "l"(p), "r"((int)in));
+        asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n mov.b32 %0, 0;\n @q ld.global.b32 %0, [%1];\n}\n" : "=r"(v) : "l"(p), "r"((int)in));
     else
-        asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n mov.b32 %0, 0;\n @q ld.global.nc.u16 %0, [%1];\n}\n" : "=r"(v) : "l"(p), "r"((int)in));
+        asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n mov.b32 %0, 0;\n @q ld.global.u16 %0, [%1];\n}\n" : "=r"(v) : "l"(p), "r"((int)in));
     return v;
 }
 // Lines of an operand to shared memory at dst by a group of four warps, 64 at
@@ -554,9 +554,9 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
                     sc[h] = zp[h] = 0;  // (past the edge)
                     if (!in || k >= kb.y || c >= p.K) continue;
                     const int64_t at = wrow * nbk + c / p.w.group;
-                    sc[h] = FEED == kCodes16 ? __ldg((const uint16_t*)p.w.scales + at) : __ldg((const uint32_t*)p.w.scales + at);
+                    sc[h] = FEED == kCodes16 ? ((const uint16_t*)p.w.scales)[at] : ((const uint32_t*)p.w.scales)[at];
                     zp[h] = 8;
-                    if (p.w.zeros) zp[h] = __ldg(p.w.zeros + at);
+                    if (p.w.zeros) zp[h] = p.w.zeros[at];
                 }
             };
             const int skip = (mine - (int)(done % kGroups) + kGroups) % kGroups;  // to this group's first block
