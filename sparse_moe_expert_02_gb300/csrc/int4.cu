@@ -10,6 +10,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "int4.cuh"
 #include "internal.h"
 
 namespace moe {
@@ -94,8 +95,14 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const Int4 q, int6
         const uint2 w = *(const uint2*)(q.codes + u * 8);
         T* o = out + r * ld + c;
         __align__(16) T v[16];
+        auto code = [&](int j) { return (float)((int)(((j < 8 ? w.x : w.y) >> (4 * (j & 7))) & 15u) - z); };
+        if (sizeof(T) == 2 && q.scale_elem == kF32 && int4_on_ties(s)) {  // (with bf16 scales 13 bits hold a product)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = from_f32<T>((float)((int)(((j < 8 ? w.x : w.y) >> (4 * (j & 7))) & 15u) - z) * s);
+            for (int j = 0; j < 16; ++j) v[j] = from_f32<T>(int4_value(code(j), s));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = from_f32<T>(code(j) * s);
+        }
         if (vec) {
 #pragma unroll
             for (int j = 0; j < (int)sizeof(T); ++j) ((uint4*)o)[j] = ((const uint4*)v)[j];

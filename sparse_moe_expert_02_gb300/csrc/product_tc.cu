@@ -238,8 +238,9 @@ __device__ __forceinline__ void copy_lines(uint32_t dst, const bf16* src, int64_
     }
 }
 
-// Eight codes' values, rounded to bf16 once.  s: the scale's bits.
-template <int FEED> __device__ __forceinline__ uint4 values8(uint32_t w, __nv_bfloat162 z, uint32_t s) {
+// Eight codes' values, rounded to bf16 once.  s: the scale's bits; TIES: it may
+// be one of int4_on_ties.
+template <int FEED, bool TIES> __device__ __forceinline__ uint4 values8(uint32_t w, __nv_bfloat162 z, uint32_t s) {
     uint32_t o[4];
     int4_pairs(w, z, o);
 #pragma unroll
@@ -251,11 +252,25 @@ template <int FEED> __device__ __forceinline__ uint4 values8(uint32_t w, __nv_bf
             v = __hmul2(d, *(const __nv_bfloat162*)&ss);
         } else {
             const float2 x = __bfloat1622float2(d);
-            v = __floats2bfloat162_rn(x.x * __uint_as_float(s), x.y * __uint_as_float(s));
+            const float f = __uint_as_float(s);
+            v = TIES ? __floats2bfloat162_rn(int4_value(x.x, f), int4_value(x.y, f)) : __floats2bfloat162_rn(x.x * f, x.y * f);
         }
         o[j] = *(const uint32_t*)&v;
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// The line of 64 codes in q, two halves of one scale and zero point each; swap:
+// which 16 bytes of the line the swizzle puts first.
+template <int FEED, bool TIES>
+__device__ __forceinline__ void put_values(uint32_t row, int swap, const uint4 (&q)[2], const uint32_t (&zp)[2], const uint32_t (&sc)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t w[4] = {q[h].x, q[h].y, q[h].z, q[h].w};
+        const __nv_bfloat162 z = int4_zero((int)zp[h]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) st_shared16(row + (((4 * h + j) ^ swap) << 4), values8<FEED, TIES>(w[j], z, sc[h]));
+    }
 }
 
 template <int OP, int FEED, int CL>
@@ -577,19 +592,17 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
                     q[0] = *(const uint4*)(line + ((t >> 2) & 1) * 16);
                     q[1] = *(const uint4*)(line + (~(t >> 2) & 1) * 16);
                 }
+                bool ties = false;
+                if (FEED == kCodes32)
+                    ties = __any_sync(0xffffffffu, int4_on_ties(__uint_as_float(sc[0])) || (p.w.group == 32 && int4_on_ties(__uint_as_float(sc[1]))));
                 ok = __all_sync(0xffffffffu, mbar_wait(empty0 + 8 * stage, phase ^ 1, lim, abort_flag));
                 if (!ok) break;
                 const int c = un.c0 + k * BK, left = un.c1 - c, c16 = min(4, (left + 15) >> 4) * 16;
                 const uint32_t fs = smem0 + stage * p.stage_bytes, rs = fs + kFBytes;
                 if (FEED >= kCodes16) {
                     const uint32_t row = fs + t * kLine;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t w[4] = {q[h].x, q[h].y, q[h].z, q[h].w};
-                        const __nv_bfloat162 z = int4_zero((int)zp[h]);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) st_shared16(row + (((4 * h + j) ^ (t & 7)) << 4), values8<FEED>(w[j], z, sc[h]));
-                    }
+                    if (ties) put_values<FEED, true>(row, t & 7, q, zp, sc);
+                    else put_values<FEED, false>(row, t & 7, q, zp, sc);
                     __syncwarp();
                     // Only now, when the codes have been used: an arrival does not order loads that are on their way
                     // with TMA's writes, and right behind the loads it let the next codes overwrite some.
