@@ -337,8 +337,12 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
     const int crank = PAIR ? (int)cluster_rank() : 0, per = PAIR ? 2 : cl;  // of a pair: 0 leads (issues the MMAs)
     const int u0 = (int)blockIdx.x / per, step = (int)gridDim.x / per;
     const int64_t lim = p.spin_ns;
-    auto wait = [&](uint32_t bar, uint32_t parity, int where) {
-        const bool ok = warp_wait(bar, parity, lim, abort_flag, p.err, where);
+    // A wait for a unit's last block takes as long as the unit's sum, and that of dw goes over all rows of a group: 2 s, the
+    // limit of a block's wait, are 220 million rows of 9 x 9 (0.6 us a block; up to 1.6 where wide operands are copied).
+    // So it has ten times that for each of its blocks beside.
+    auto unit_lim = [&](int2 kb) { return lim + (int64_t)(kb.y - kb.x) * 16000; };
+    auto wait = [&](uint32_t bar, uint32_t parity, int where, int64_t limit) {
+        const bool ok = warp_wait(bar, parity, limit, abort_flag, p.err, where);
         if (PAIR && !ok && elect_one()) raise_abort_pair(abort_flag, (uint32_t)crank);
         return ok;
     };
@@ -362,7 +366,7 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
                 const int i0 = __shfl_sync(0xffffffffu, un.i0 + crank * n16 * 16, 0), f0 = __shfl_sync(0xffffffffu, un.f0, 0);
                 const int g = __shfl_sync(0xffffffffu, un.g, 0);
                 for (int k = kb.x; k < kb.y; ++k) {
-                    ok = wait(empty0 + 8 * stage, phase ^ 1, 61);
+                    ok = wait(empty0 + 8 * stage, phase ^ 1, 61, lim);
                     if (!ok) break;
                     const int c = __shfl_sync(0xffffffffu, un.c0 + k * BK, 0);
                     // dw: sixteens of this block's rows; the others read whole blocks, zeros past the edge
@@ -455,7 +459,7 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
                 const int left = (un.c1 - un.c0) & (BK - 1);
                 stage = (stage + kb.y - 1) % S;
                 if (left & 15) {
-                    ok = wait(tail0 + 8 * stage, tail_phase >> stage & 1, 66);
+                    ok = wait(tail0 + 8 * stage, tail_phase >> stage & 1, 66, unit_lim(kb));
                     if (!ok) break;
                     tail_phase ^= 1u << stage;
                     clear(smem0 + stage * p.stage_bytes, left, rslabs);
@@ -466,11 +470,11 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
                 continue;
             }
             const uint32_t id = idesc_bf16(PAIR ? 2 * BF : BF, n) | (kFAlongC ? 0u : 1u << 15) | (kRAlongC ? 0u : 1u << 16);
-            ok = wait(tempty0 + 8 * acc, acc_phase ^ 1, 62);
+            ok = wait(tempty0 + 8 * acc, acc_phase ^ 1, 62, lim);
             if (!ok) break;
             const uint32_t d = tmem + acc * kMaxI;
             for (int k = kb.x; k < kb.y; ++k) {
-                ok = wait(full0 + 8 * stage, phase, 63);
+                ok = wait(full0 + 8 * stage, phase, 63, lim);
                 if (!ok) break;
                 const uint32_t fs = smem0 + stage * p.stage_bytes, rs = fs + kFBytes;
                 const int left = un.c1 - un.c0 - k * BK;
@@ -648,7 +652,7 @@ __global__ void __launch_bounds__(threads_for(FEED), 1)
             const uint32_t taddr = tmem + acc * kMaxI + ((uint32_t)(sub * 32) << 16);
             const uint32_t te = tempty0 + 8 * acc;
             if (any) {
-                const bool ok = mbar_wait(tfull0 + 8 * acc, acc_phase, lim, abort_flag);
+                const bool ok = mbar_wait(tfull0 + 8 * acc, acc_phase, unit_lim(my_blocks(un, rank, cl)), abort_flag);
                 if (!__all_sync(0xffffffffu, ok)) {
                     if (lane == 0 && !*abort_flag) {
                         record_error(p.err, MOE_ERR_DEVICE_TIMEOUT, 64, blockIdx.x, u);
