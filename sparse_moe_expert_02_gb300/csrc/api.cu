@@ -1360,13 +1360,15 @@ moe::Int4 int4_of(const uint8_t* codes, const void* scales, int32_t scale_dtype,
 moe_status moe_int4_quantize(const void* x, int32_t dtype, int64_t ld_x, int64_t rows, int32_t cols, int32_t group, uint8_t* codes,
                              void* scales, int32_t scale_dtype, uint8_t* zeros, void* stream) {
     if (rows < 0) return arg_fail(MOE_ERR_INVALID_ARG, "rows < 0");
-    const moe_status st = check_int4(codes, scales, scale_dtype, group, cols, rows > 0);
+    moe_status st = check_int4(codes, scales, scale_dtype, group, cols, rows > 0);
     if (st != MOE_OK) return st;
     if (!float_type(dtype)) return arg_fail(MOE_ERR_UNSUPPORTED, "values must be fp32 or bf16");
     if (rows == 0) return MOE_OK;
     if (!rows_ok(x, dtype, ld_x, cols)) return arg_fail(MOE_ERR_INVALID_ARG, "values NULL or misaligned, or a row stride below cols");
+    int sms = 0;
+    if ((st = current_sms(&sms)) != MOE_OK) return st;
     moe::PdlScope scope(true);
-    MOE_CUDA(moe::launch_int4_quantize(x, float_elem(dtype), ld_x, rows, cols, int4_of(codes, scales, scale_dtype, zeros, group),
+    MOE_CUDA(moe::launch_int4_quantize(x, float_elem(dtype), ld_x, rows, cols, int4_of(codes, scales, scale_dtype, zeros, group), sms,
                                        (cudaStream_t)stream));
     return MOE_OK;
 }
@@ -1374,13 +1376,15 @@ moe_status moe_int4_quantize(const void* x, int32_t dtype, int64_t ld_x, int64_t
 moe_status moe_int4_dequantize(const uint8_t* codes, const void* scales, int32_t scale_dtype, const uint8_t* zeros, int32_t group,
                                int64_t rows, int32_t cols, void* out, int32_t out_dtype, int64_t ld_out, void* stream) {
     if (rows < 0) return arg_fail(MOE_ERR_INVALID_ARG, "rows < 0");
-    const moe_status st = check_int4(codes, scales, scale_dtype, group, cols, rows > 0);
+    moe_status st = check_int4(codes, scales, scale_dtype, group, cols, rows > 0);
     if (st != MOE_OK) return st;
     if (!float_type(out_dtype)) return arg_fail(MOE_ERR_UNSUPPORTED, "out must be fp32 or bf16");
     if (rows == 0) return MOE_OK;
     if (!rows_ok(out, out_dtype, ld_out, cols)) return arg_fail(MOE_ERR_INVALID_ARG, "out NULL or misaligned, or its row stride below cols");
+    int sms = 0;
+    if ((st = current_sms(&sms)) != MOE_OK) return st;
     moe::PdlScope scope(true);
-    MOE_CUDA(moe::launch_int4_dequantize(int4_of(codes, scales, scale_dtype, zeros, group), rows, cols, out, float_elem(out_dtype), ld_out,
+    MOE_CUDA(moe::launch_int4_dequantize(int4_of(codes, scales, scale_dtype, zeros, group), rows, cols, out, float_elem(out_dtype), ld_out, sms,
                                          (cudaStream_t)stream));
     return MOE_OK;
 }

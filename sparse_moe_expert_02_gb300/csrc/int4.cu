@@ -7,6 +7,10 @@
 // the nearest to the exact quotient by the stored scale (ties to even): the
 // rounded quotient's residuals to its neighbours, each one fused multiply-add
 // and so exact in sign, decide.
+//
+// Measured, 65536 x 4096 in groups of 128 with zero points: quantising 715 to 740
+// us (bf16 in: 100 at the copy's rate; a warp has one group, 128 loads of an
+// element, on its way), reading back 124 to 132 as bf16 (100), 285 as fp32 (180).
 #include <algorithm>
 
 #include "common.cuh"
@@ -113,12 +117,12 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const Int4 q, int6
     }
 }
 
-unsigned blocks_for(int64_t units) { return (unsigned)std::min<int64_t>(std::max<int64_t>(units, 1), 152 * 16); }
+unsigned blocks_for(int64_t units, int num_sms) { return (unsigned)std::min<int64_t>(std::max<int64_t>(units, 1), 16 * num_sms); }
 
 }  // namespace
 
-cudaError_t launch_int4_quantize(const void* x, int x_elem, int64_t ld, int64_t rows, int cols, const Int4& q, cudaStream_t s) {
-    const dim3 grid(blocks_for(cdiv(rows * cdiv(cols, q.group), kThreads / 32))), block(kThreads);
+cudaError_t launch_int4_quantize(const void* x, int x_elem, int64_t ld, int64_t rows, int cols, const Int4& q, int num_sms, cudaStream_t s) {
+    const dim3 grid(blocks_for(cdiv(rows * cdiv(cols, q.group), kThreads / 32), num_sms)), block(kThreads);
     uint8_t *codes = const_cast<uint8_t*>(q.codes), *zeros = const_cast<uint8_t*>(q.zeros);
     cudaError_t e;
 #define MOE_Q(T, TS) launch_kernel(quantize_kernel<T, TS>, grid, block, 0, s, 1, (const T*)x, ld, rows, cols, q.group, codes, (TS*)const_cast<void*>(q.scales), zeros)
@@ -129,8 +133,8 @@ cudaError_t launch_int4_quantize(const void* x, int x_elem, int64_t ld, int64_t 
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-cudaError_t launch_int4_dequantize(const Int4& q, int64_t rows, int cols, void* out, int out_elem, int64_t ld, cudaStream_t s) {
-    const dim3 grid(blocks_for(cdiv(rows * (cols / 16), kThreads))), block(kThreads);
+cudaError_t launch_int4_dequantize(const Int4& q, int64_t rows, int cols, void* out, int out_elem, int64_t ld, int num_sms, cudaStream_t s) {
+    const dim3 grid(blocks_for(cdiv(rows * (cols / 16), kThreads), num_sms)), block(kThreads);
     const bool vec = ((uintptr_t)out & 15) == 0 && ld * (out_elem == kF32 ? 4 : 2) % 16 == 0;
     const cudaError_t e = out_elem == kF32 ? launch_kernel(dequantize_kernel<float>, grid, block, 0, s, 1, q, rows, cols, (float*)out, ld, vec)
                                            : launch_kernel(dequantize_kernel<bf16>, grid, block, 0, s, 1, q, rows, cols, (bf16*)out, ld, vec);

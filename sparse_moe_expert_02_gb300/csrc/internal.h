@@ -338,8 +338,9 @@ struct Int4 {
     const uint8_t* zeros;  // [rows, ceil(cols/group)] or nullptr (8 everywhere)
     int group;             // 32, 64 or 128
 };
-cudaError_t launch_int4_quantize(const void* x, int x_elem, int64_t ld, int64_t rows, int cols, const Int4& q, cudaStream_t stream);
-cudaError_t launch_int4_dequantize(const Int4& q, int64_t rows, int cols, void* out, int out_elem, int64_t ld, cudaStream_t stream);
+cudaError_t launch_int4_quantize(const void* x, int x_elem, int64_t ld, int64_t rows, int cols, const Int4& q, int num_sms, cudaStream_t stream);
+cudaError_t launch_int4_dequantize(const Int4& q, int64_t rows, int cols, void* out, int out_elem, int64_t ld, int num_sms,
+                                   cudaStream_t stream);
 struct Int4Product {
     const void* x;           // [rows, ldx]
     int elem;
