@@ -513,8 +513,9 @@ MOE_API moe_status moe_swiglu_grad(const void* dh, int64_t ld_dh, const void* ga
  * last of a row may be short.  value = scale * (code - zero), zero one byte a
  * group (0 .. 15), or 8 where zeros is NULL.  codes 16-byte aligned.
  * Quantising: scale = amax/7, or with zeros (max(0, v) - min(0, v))/15,
- * rounded to its type (1 where that gives 0); zero = -min(0, v)/scale and
- * codes v/scale + zero to the nearest, ties to even, in 0 .. 15.  A group with
+ * rounded to its type (1 where that gives 0); zero = -min(0, v)/scale to the
+ * nearest, ties to even, in 0 .. 15; code = v/scale to the nearest, ties to even,
+ * plus zero, in 0 .. 15.  A group with
  * an infinity or a NaN reads back as NaN. */
 MOE_API moe_status moe_int4_quantize(const void* x, int32_t dtype, int64_t ld_x, int64_t rows, int32_t cols,
                                      int32_t group, uint8_t* codes, void* scales, int32_t scale_dtype, uint8_t* zeros,
@@ -527,7 +528,8 @@ MOE_API moe_status moe_int4_dequantize(const uint8_t* codes, const void* scales,
  *   out[r][n] = sum_k x[r][k] w_g[n][k]
  * x [rows, K] and out [rows, N] fp32 or bf16; w_g the values of [G, N] rows of
  * K columns as above, exact where x is fp32 or rows is at most 8 G or 32; for
- * more rows of bf16 each value is rounded to bf16 once. */
+ * more rows of bf16 each value is rounded to bf16 once.  rows counts all rows of
+ * x, those of no group too: which of the two it is does not depend on offsets. */
 MOE_API moe_status moe_int4_gemm(const void* x, int32_t dtype, int64_t ld_x, const uint8_t* codes, const void* scales,
                                  int32_t scale_dtype, const uint8_t* zeros, int32_t group, const int32_t* offsets,
                                  int32_t rows, int32_t G, int32_t N, int32_t K, void* out, int32_t out_dtype,

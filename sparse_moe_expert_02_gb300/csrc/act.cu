@@ -56,8 +56,11 @@ template <typename T, int V> struct Pack {
 
 // s = 1 / (1 + e^-g) and 1 - s, both from e^-|g|, which neither overflows nor
 // cancels (e^89 is past fp32's range, but -89 e^-89 is not).  FULL: to a few
-// ulp, where results stay in fp32; else by the hardware's exponential and
-// reciprocal, some 2^-21 about zero, below a 2000th of a bf16 step.
+// ulp, where h, dgate and dup stay in fp32; else by the hardware's exponential
+// and reciprocal, some 2^-21 about zero, below a 2000th of a bf16 step.  dweight
+// is fp32 all the same, but a sum of bf16 products: 1.3e-7 of its rms off 64 bits
+// either way (1.1e-7 by tensor operations in 32 bits), and the full form takes 150
+// us instead of 140 for 81920 x 1024, 21 instead of 17 for 4097 x 1000.
 template <bool FULL> __device__ __forceinline__ void sigmoid(float g, float& s, float& rest) {
     const float e = FULL ? expf(-fabsf(g)) : __expf(-fabsf(g));
     const float r = FULL ? 1.0f / (1.0f + e) : __fdividef(1.0f, 1.0f + e);

@@ -186,7 +186,7 @@ __device__ __forceinline__ void finish(const Args& p, const float (*part)[kRows 
     if (cur.f0 + f >= p.N) return;
     for (int r = threadIdx.x / F; r < cur.n; r += kThreads / F) {
         float v = 0.0f;
-    #pragma unroll
+#pragma unroll
         for (int w = 0; w < kWarps; ++w) v += part[w][r * (F + 4) + f];
         if constexpr (LG != 0) {
             if (!isfinite(v)) {  // a group's sum may have overflown before its scale
@@ -206,7 +206,6 @@ __device__ __forceinline__ void finish(const Args& p, const float (*part)[kRows 
         else ((bf16*)p.out)[at] = __float2bfloat16_rn(v);
     }
 }
-
 
 }  // namespace few_rows
 }  // namespace moe

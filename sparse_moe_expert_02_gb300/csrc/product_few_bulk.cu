@@ -17,7 +17,7 @@
 // 13 rows over 8 groups 12.7 (8.3 at the copy's rate: of some 420 units an SM
 // has two or three).  Codes, groups of 128 columns, 64 groups of a row: 49 us at
 // 1024 x 4096, 51 at 4096 x 1024 (72 with tiles of 16 features).  80 rows over
-// 128 groups, 1024 x 4096 with zero points in groups of 64 columns, 34 us
+// 128 groups, 1024 x 4096 with zero points in groups of 64 columns, 34 to 36 us
 // (11 to 13 at the copy's rate): the loads alone take 20 of them; decoding and
 // multiplying take 250 instructions a chunk of 16 x 128 codes and warp, 58 % of
 // the ALU pipe's cycles, and do not hide the loads in full.  One token by 4096 x

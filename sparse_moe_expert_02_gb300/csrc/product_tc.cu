@@ -20,11 +20,11 @@
 // by TMA; w is mapped as [G][N][K], so that dx's sum ends with its own matrix.
 //
 // Measured (us; bytes or operations at the measured copy and GEMM rates in
-// brackets).  16384 rows in 8 groups, 4096 x 4096: 338 (275) in a loop, 303 at
+// brackets).  16384 rows in 8 groups, 4096 x 4096: 338 to 347 (275) in a loop, 303 at
 // the first calls after a pause: the power limit.  One CTA a tile took 369,
 // with 73 % of the tensor pipe's cycles used and 4 stages of 48 KB on the way;
 // pairs have 6 of 32.  64 ragged groups: forward of 4001 rows, 1024 x 4096, 100
-// (86); dx of 16380 rows 127 (105); dw, fp32, 220 (185): HBM, at 5.6 to 5.8 of
+// (86); dx of 16380 rows 131 (105); dw, fp32, 220 (185): HBM, at 5.6 to 5.8 of
 // 6.7 TB/s.  2047 rows by 4096 x 4096 codes 57 (34): the MMAs (240 rows by 128
 // features) use 55 % of the tensor pipe's cycles, the rest are waits for decoded
 // stages, some 850 cycles each where the MMAs take 480.
@@ -238,8 +238,13 @@ __device__ __forceinline__ void copy_lines(uint32_t dst, const bf16* src, int64_
     }
 }
 
-// Eight codes' values, rounded to bf16 once.  s: the scale's bits; TIES: it may
-// be one of int4_on_ties.
+// Eight codes' values, rounded to bf16 once: a choice.  The tensor cores take
+// bf16 on both sides, and a value is code - zero times the scale, 12 bits with a
+// bf16 scale.  In two parts, which would be exact, a product would be twice the
+// MMAs and stores to shared memory, and those bound it (2047 rows, 4096 x 4096: the
+// outputs are 0.0022 of their rms off 64 bits, 0.0017 from their own rounding
+// alone).  Few rows, bound by the codes' bytes, multiply the codes and keep all
+// bits (product_few.cu).  s: the scale's bits; TIES: it may be one of int4_on_ties.
 template <int FEED, bool TIES> __device__ __forceinline__ uint4 values8(uint32_t w, __nv_bfloat162 z, uint32_t s) {
     uint32_t o[4];
     int4_pairs(w, z, o);

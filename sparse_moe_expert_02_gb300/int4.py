@@ -75,8 +75,8 @@ def matmul(x: torch.Tensor, w: I4Tensor, offsets: torch.Tensor = None, out: torc
            err: torch.Tensor = None) -> torch.Tensor:
     """x [rows, K] times w [N, K] (or its group's of w [G, N, K]) transposed, in out_dtype (x's if None).
 
-    Groups, rows of no group and err as in ``grouped``.  For bf16 x of more than max(8 G, 32) rows the weights' values are
-    rounded to bf16 once.
+    Groups, rows of no group and err as in ``grouped``.  For bf16 x of more than max(8 G, 32) rows (those of no group
+    counted) the weights' values are rounded to bf16 once; else, and for fp32 x, they are multiplied as they are.
     """
     if out is None:
         out = torch.empty((x.shape[0], w.codes.shape[-2]), dtype=out_dtype or x.dtype, device=x.device)
