@@ -179,28 +179,60 @@ template <int F = kF> __device__ __forceinline__ void put_part(float* mine, cons
 #pragma unroll
     for (int m = 0; m < 4; ++m) mine[(2 * t + (m & 1)) * (F + 4) + g + 8 * (m >> 1)] = acc[m];
 }
+// A feature's result for a row, where the tiles' sum is no finite number: a
+// group's sum may have overflown before its scale.  By whole warps, W lanes of
+// which have the same row (x; nullptr: none); again: whether this lane's is to be
+// summed.  A NaN of the row, or of the feature's scales, is one of the result and
+// needs no second sum: the lanes look for it together (80 rows of 128 experts,
+// 1024 x 4096, a call on a cold cache: 83 us, of NaN 145, 2400 when each was summed
+// again, of infinities, which are, 1650).
+template <int LG, typename T, int W>
+__device__ __forceinline__ float sum_again(const Args& p, const T* x, int64_t row, int nb, bool again, float v) {
+    const int lane = threadIdx.x & 31;
+    bool nan = false;
+    if (x)
+        for (int k = lane % W; k < p.K; k += W) nan |= isnan(to_f32(x[k]));
+    nan = (__ballot_sync(0xffffffffu, nan) >> (lane & ~(W - 1)) & (uint32_t)((1ull << W) - 1)) != 0;
+    if (!again) return v;
+    auto scale = [&](int g) {
+        const int64_t at = row * nb + g;
+        return p.q.scale_elem == kF32 ? ((const float*)p.q.scales)[at] : to_f32(((const bf16*)p.q.scales)[at]);
+    };
+    for (int g = 0; g < nb && !nan; ++g) nan = isnan(scale(g));
+    if (nan) return __int_as_float(0x7FC00000);
+    v = 0.0f;
+    for (int g = 0; g < nb; ++g) {
+        const float s = scale(g);
+        const int z = p.q.zeros ? p.q.zeros[row * nb + g] : 8;
+        const uint8_t* c = p.q.codes + row * (p.K / 2);
+        for (int k = g << LG; k < min(p.K, (g + 1) << LG); k += 2) {
+            const int cd = c[k >> 1];
+            v = fmaf(to_f32(x[k]), (float)((cd & 15) - z) * s, v);
+            v = fmaf(to_f32(x[k + 1]), (float)((cd >> 4) - z) * s, v);
+        }
+    }
+    return v;
+}
+
 // The partial tiles' sum, stored; by kThreads threads.
 template <int LG, typename T, int F = kF>
 __device__ __forceinline__ void finish(const Args& p, const float (*part)[kRows * (F + 4)], const Unit& cur, int nb) {
     const int f = threadIdx.x & (F - 1);
-    if (cur.f0 + f >= p.N) return;
-    for (int r = threadIdx.x / F; r < cur.n; r += kThreads / F) {
+    for (int r0 = 0; r0 < kRows; r0 += kThreads / F) {
+        const int r = r0 + (int)threadIdx.x / F;
+        const bool in = r < cur.n && cur.f0 + f < p.N;
         float v = 0.0f;
+        if (in) {
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) v += part[w][r * (F + 4) + f];
-        if constexpr (LG != 0) {
-            if (!isfinite(v)) {  // a group's sum may have overflown before its scale
-                const T* x = (const T*)p.x + (int64_t)(cur.row0 + r) * p.ldx;
-                const int64_t row = (int64_t)cur.g * p.N + cur.f0 + f;
-                v = 0.0f;
-                for (int k = 0; k < p.K; ++k) {
-                    const int64_t at = row * nb + (k >> LG);
-                    const int cd = (p.q.codes[row * (p.K / 2) + (k >> 1)] >> (4 * (k & 1))) & 15;
-                    const float s = p.q.scale_elem == kF32 ? ((const float*)p.q.scales)[at] : to_f32(((const bf16*)p.q.scales)[at]);
-                    v = fmaf(to_f32(x[k]), (float)(cd - (p.q.zeros ? p.q.zeros[at] : 8)) * s, v);
-                }
-            }
+            for (int w = 0; w < kWarps; ++w) v += part[w][r * (F + 4) + f];
         }
+        if constexpr (LG != 0) {
+            const bool again = !isfinite(v);
+            if (__any_sync(0xffffffffu, again))
+                v = sum_again<LG, T, (F < 32 ? F : 32)>(p, r < cur.n ? (const T*)p.x + (int64_t)(cur.row0 + r) * p.ldx : nullptr,
+                                                       (int64_t)cur.g * p.N + cur.f0 + f, nb, again, v);
+        }
+        if (!in) continue;
         const int64_t at = (int64_t)(cur.row0 + r) * p.ldo + cur.f0 + f;
         if (p.out_elem == kF32) ((float*)p.out)[at] = v;
         else ((bf16*)p.out)[at] = __float2bfloat16_rn(v);
